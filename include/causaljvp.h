@@ -385,6 +385,113 @@ caj_status caj_attn_bwd(const void *q, const void *k, const void *v, const void 
                         const caj_mask_desc *mask, void *dq, void *dk, void *dv, float *delta,
                         void *stream);
 
+/*
+ * Activation checkpoints in 8 bits. A row of `cols` values is kept as
+ * nb = ceil(cols/32) blocks of 32 codes and one scale byte a block: the value is
+ * code * 2^(scale - 127), code a whole number in [-127, 127], scale the smallest
+ * byte for which the block's largest magnitude is at most 127 * 2^(scale - 127)
+ * (at most 248: magnitudes above 127 * 2^121 = 3.376e38 are kept as that).
+ * Rounding is to the nearest code, ties to even: at most half of
+ * 2^(scale - 127). A decoded value is exactly a bf16 number. A block that holds
+ * an infinity or a NaN gets scale 255 and decodes to NaN throughout.
+ *   codes   [rows, 32*nb] int8, 16-byte aligned; codes past `cols` are 0
+ *   scales  [rows, 4*ceil(nb/4)] uint8, 4-byte aligned; bytes past nb are 0
+ *   x       rows of `cols` values of `dtype`, `ld` elements apart (ld >= cols);
+ *           aligned to its element
+ * pack reads x and writes codes and scales (padding included); unpack the
+ * reverse, and leaves what lies between the rows of x alone. rows = 0 returns
+ * CAJ_OK and launches nothing. rows * nb must be below 2^31
+ * (CAJ_ERR_UNSUPPORTED). Return CAJ_OK once enqueued, CAJ_ERR_INVALID_ARG
+ * without launching, or CAJ_ERR_CUDA.
+ */
+caj_status caj_ckpt_pack(const void *x, int64_t rows, int32_t cols, int64_t ld, int32_t dtype,
+                          int8_t *codes, uint8_t *scales, void *stream);
+caj_status caj_ckpt_unpack(const int8_t *codes, const uint8_t *scales, int64_t rows, int32_t cols,
+                            int64_t ld, int32_t dtype, void *x, void *stream);
+
+/*
+ * Rotary angles from positions: with angle = pos[n][axis[i]] * freq[i],
+ *   cos[n][i] = mscale * cos(angle),   sin[n][i] = mscale * sin(angle)
+ *   in : pos    [N, axes] int32 (pos64 = 0) or int64 (pos64 = 1), |pos| <= 2^53
+ *        freq   [pairs] fp64, radians per position; |pos * freq| < 2^50
+ *        axis   [pairs] int32, which column of pos turns pair i; null: column 0.
+ *               A pair whose axis is not in [0, axes) gets NaN.
+ *   out: cos, sin [N, pairs] fp32
+ * The product and its reduction are in 64 bits and carry the product's rounding
+ * error along, so far positions are as exact as near ones. Scaled frequencies
+ * (long contexts) are the caller's: freq is used as it is. Pointers aligned to
+ * their elements. N = 0 launches nothing. Returns as above.
+ */
+caj_status caj_rope_table(const void *pos, int32_t pos64, const double *freq, const int32_t *axis,
+                          int64_t N, int32_t axes, int32_t pairs, float mscale, float *cos, float *sin,
+                          void *stream);
+
+/*
+ * Norm and rotation of queries and keys for any of: norm over the head, over the
+ * token or none; interleaved or half layout; part of the head; strided inputs;
+ * fewer key heads than query heads; with or without tangents; and its gradient.
+ * (caj_qk_norm_rope_jvp is the primal-tangent form at full width, interleaved,
+ * one gain per channel.)  For q and k:
+ *   y  = R (g * x / r),  r = sqrt(mean(x^2) + eps);   no norm: y = R x
+ *   ty = R (g * (tx / r - x * mean(x * tx) / r^3))
+ * R turns the first 2*pairs channels of each head by the table's angles: pair i
+ * is channels (2i, 2i+1) (CAJ_ROPE_INTERLEAVED) or (i, i + pairs)
+ * (CAJ_ROPE_HALF); the others pass. v is copied into the new layout.
+ *   norm       caj_norm; HEAD: mean over D; TOKEN: over heads * D
+ *   gain_full  0: gq, gk are [D], shared by the heads (not with TOKEN);
+ *              1: [heads * D]
+ *   ld*        elements between the tokens of each input (token (b, n) starts at
+ *              (b*N + n) * ld), multiples of 16 bytes, >= heads * D
+ * Forward:
+ *   in : xq, xk, xv           [B, N, heads*D] of dtype (heads: Hq, Hk, Hk); xv null: no v
+ *        txq, txk, txv        their tangents, or all null
+ *        gq, gk               fp32 gains (null with norm NONE)
+ *        rope_cos, rope_sin   [N, pairs] fp32
+ *   out: q, k, v, tq, tk, tv  [B, heads, N, D] of dtype
+ * Backward (of the primal): with u = R^T dq,
+ *   dx = g u / r - x * mean(x * g * u) / r^3,  dg = sum of u * x / r (over the
+ *   heads too where they share a gain)
+ *   in : dq, dk, dv           [B, heads, N, D] of dtype (dv null: no v)
+ *        xq, xk               as in the forward, or with xq_scales, xk_scales
+ *                             non-null the codes of 8-bit checkpoints of rows of
+ *                             heads * D values (caj_ckpt_pack; ldq, ldk unused);
+ *                             null with norm NONE
+ *   out: dxq, dxk, dxv        [B, N, heads*D] of dtype, contiguous
+ *        dgq, dgk             fp32, as long as the gains (null with norm NONE)
+ *   workspace                 caj_qk_rope_bwd_workspace() bytes, 16-byte aligned;
+ *                             no other work may use it until the call is done
+ * Deterministic (no atomics). Supported: dtype F32 or BF16; D in
+ * {32, 64, 128, 256}; heads * D <= 8192; pairs a multiple of 8, at most D/2;
+ * B * N < 2^31. Pointers 16-byte aligned. B * N = 0 is not a call
+ * (CAJ_ERR_INVALID_ARG). Returns CAJ_OK once enqueued, CAJ_ERR_INVALID_ARG /
+ * CAJ_ERR_UNSUPPORTED without launching, or CAJ_ERR_CUDA.
+ */
+typedef enum { CAJ_NORM_NONE = 0, CAJ_NORM_HEAD = 1, CAJ_NORM_TOKEN = 2 } caj_norm;
+typedef enum { CAJ_ROPE_INTERLEAVED = 0, CAJ_ROPE_HALF = 1 } caj_rope_layout;
+typedef struct {
+  int32_t B, N, Hq, Hk, D;
+  int32_t pairs;
+  int32_t dtype;      /* caj_dtype */
+  int32_t norm;       /* caj_norm */
+  int32_t layout;     /* caj_rope_layout */
+  int32_t gain_full;
+  float eps;          /* > 0 with a norm */
+  int64_t ldq, ldk, ldv, ldtq, ldtk, ldtv;
+} caj_qk_rope_shape;
+
+caj_status caj_qk_rope_fwd(const void *xq, const void *xk, const void *xv, const void *txq,
+                           const void *txk, const void *txv, const float *gq, const float *gk,
+                           const float *rope_cos, const float *rope_sin,
+                           const caj_qk_rope_shape *shape, void *q, void *k, void *v, void *tq,
+                           void *tk, void *tv, void *stream);
+caj_status caj_qk_rope_bwd_workspace(const caj_qk_rope_shape *shape, size_t *bytes);
+caj_status caj_qk_rope_bwd(const void *dq, const void *dk, const void *dv, const void *xq,
+                           const void *xk, const uint8_t *xq_scales, const uint8_t *xk_scales,
+                           const float *gq, const float *gk, const float *rope_cos,
+                           const float *rope_sin, const caj_qk_rope_shape *shape, void *dxq,
+                           void *dxk, void *dxv, float *dgq, float *dgk, void *workspace,
+                           size_t workspace_bytes, void *stream);
+
 /* Synchronises `stream`, then reads and clears the library's device error word.
  * Returns CAJ_OK, CAJ_ERR_DEVICE_TIMEOUT (a kernel gave up: it abandoned a wait
  * or refused to run; its outputs are undefined) or CAJ_ERR_CUDA. */

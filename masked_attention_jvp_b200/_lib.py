@@ -20,6 +20,8 @@ EXPORTED = [
     "caj_attn_bwd", "caj_attn_fwd_jvp_host_workspace", "caj_attn_fwd_jvp_host", "caj_out_proj_jvp",
     "caj_attn_fwd_jvp_scatter", "caj_attn_fwd_jvp_host_static", "caj_signal_barrier",
     "caj_ipc_export", "caj_ipc_open", "caj_ipc_close", "caj_attn_fwd_jvp_part", "caj_part_query_tiles",
+    "caj_ckpt_pack", "caj_ckpt_unpack", "caj_rope_table", "caj_qk_rope_fwd", "caj_qk_rope_bwd",
+    "caj_qk_rope_bwd_workspace",
 ]
 
 
@@ -59,6 +61,16 @@ CAJ_FLAG_TOKEN_MAJOR_OUT = 2
 class PrologueShapeC(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int32), ("N", ctypes.c_int32), ("H", ctypes.c_int32),
                 ("D", ctypes.c_int32), ("eps", ctypes.c_float), ("norm_per_head", ctypes.c_int32)]
+
+
+NORMS = {"none": 0, "head": 1, "token": 2}  # caj_norm
+ROPE_LAYOUTS = {"interleaved": 0, "half": 1}  # caj_rope_layout
+
+
+class QkRopeShapeC(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("B", "N", "Hq", "Hk", "D", "pairs", "dtype", "norm", "layout",
+                                              "gain_full")] + [("eps", ctypes.c_float)] + \
+        [(n, ctypes.c_int64) for n in ("ldq", "ldk", "ldv", "ldtq", "ldtk", "ldtv")]
 
 
 class CajError(RuntimeError):
@@ -138,6 +150,19 @@ def lib() -> ctypes.CDLL:
         L.caj_attn_fwd_jvp_part.restype = ctypes.c_int
         L.caj_part_query_tiles.argtypes = [ctypes.POINTER(MaskDescC), i32, i32, ctypes.POINTER(i32), i32]
         L.caj_part_query_tiles.restype = i32
+        rope = ctypes.POINTER(QkRopeShapeC)
+        L.caj_ckpt_pack.argtypes = [vp, i64, i32, i64, i32, vp, vp, vp]
+        L.caj_ckpt_pack.restype = ctypes.c_int
+        L.caj_ckpt_unpack.argtypes = [vp, vp, i64, i32, i64, i32, vp, vp]
+        L.caj_ckpt_unpack.restype = ctypes.c_int
+        L.caj_rope_table.argtypes = [vp, i32, vp, vp, i64, i32, i32, ctypes.c_float, vp, vp, vp]
+        L.caj_rope_table.restype = ctypes.c_int
+        L.caj_qk_rope_fwd.argtypes = [vp] * 10 + [rope] + [vp] * 7
+        L.caj_qk_rope_fwd.restype = ctypes.c_int
+        L.caj_qk_rope_bwd_workspace.argtypes = [rope, ctypes.POINTER(ctypes.c_size_t)]
+        L.caj_qk_rope_bwd_workspace.restype = ctypes.c_int
+        L.caj_qk_rope_bwd.argtypes = [vp] * 11 + [rope] + [vp] * 6 + [ctypes.c_size_t, vp]
+        L.caj_qk_rope_bwd.restype = ctypes.c_int
         L.caj_version.argtypes = []
         L.caj_version.restype = i32
         _lib = L

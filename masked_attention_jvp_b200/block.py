@@ -1,0 +1,311 @@
+"""The operators around the attention of a transformer block (thin layer over the C-ABI
+library; contracts in include/causaljvp.h):
+
+    cos, sin = rope_table(pos, freq, axis)                   # angles from positions
+    q, k, v = qk_norm_rope_fwd(xq, xk, xv, gq, gk, cos, sin, H)
+    dxq, dxk, dxv, dgq, dgk = qk_norm_rope_bwd(dq, dk, dv, xq, xk, gq, gk, cos, sin)
+    c = ckpt8_pack(x); x = ckpt8_unpack(c)                   # activations kept in 8 bits
+
+Tensors are CUDA tensors; calls run on the current stream of the tensors' device, whichever
+device is current, and are asynchronous. Outputs are new tensors. Calls with no rows return
+empty outputs (and zero gradients) without a launch.
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+import math
+from typing import NamedTuple, Optional, Sequence, Tuple, Union
+
+import torch
+
+from . import _lib
+
+__all__ = ["Ckpt8", "ckpt8_pack", "ckpt8_unpack", "rope_frequencies", "rope_table", "qk_norm_rope_fwd",
+           "qk_norm_rope_bwd"]
+
+_DTYPES = {torch.float32: _lib.CAJ_DTYPE_F32, torch.bfloat16: _lib.CAJ_DTYPE_BF16}
+
+
+def _ptr(t: Optional[torch.Tensor]) -> ctypes.c_void_p:
+    return ctypes.c_void_p(t.data_ptr() if t is not None else 0)
+
+
+@contextlib.contextmanager
+def _on(t: torch.Tensor):
+    """Makes t's device current for the call; gives its current stream."""
+    with torch.cuda.device(t.device):
+        yield ctypes.c_void_p(torch.cuda.current_stream(t.device).cuda_stream)
+
+
+def _same_device(what: str, *tensors):
+    first = tensors[0]
+    for t in tensors:
+        if t is not None and not (t.is_cuda and t.device == first.device):
+            raise ValueError(f"{what}: all tensors must be CUDA tensors on one device")
+
+
+# ------------------------------------------------------------ 8-bit checkpoints
+
+class Ckpt8(NamedTuple):
+    """A tensor kept in 8 bits: codes int8 [rows, 32*nb], scales uint8 [rows, 4*ceil(nb/4)],
+    nb = ceil(C/32) blocks a row, and the shape [..., C] it stands for."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+    shape: Tuple[int, ...]
+
+    @property
+    def rows(self) -> int:
+        return math.prod(self.shape[:-1])
+
+    def nbytes(self) -> int:
+        return self.codes.numel() + self.scales.numel()
+
+
+def _ckpt_widths(C: int) -> Tuple[int, int]:
+    nb = -(-C // 32)
+    return 32 * nb, 4 * -(-nb // 4)
+
+
+def _check_ckpt(what: str, c: Ckpt8):
+    w, ns = _ckpt_widths(c.shape[-1])
+    for t, dtype, width in ((c.codes, torch.int8, w), (c.scales, torch.uint8, ns)):
+        if not (t.is_cuda and t.is_contiguous() and t.dtype == dtype and tuple(t.shape) == (c.rows, width)):
+            raise ValueError(f"{what}: a checkpoint's codes are int8 [rows, {w}] and its scales uint8 "
+                             f"[rows, {ns}], contiguous CUDA tensors")
+
+
+def _rows(t: torch.Tensor) -> Optional[Tuple[int, int]]:
+    """(rows, elements between rows) of t seen as rows of its last axis; None if its strides
+    do not allow it."""
+    rows = math.prod(t.shape[:-1])
+    if t.numel() == 0:
+        return rows, max(t.shape[-1], 1)
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        return None
+    ld, inner = None, 1  # the distance of the innermost axis with more than one row; rows below
+    for size, stride in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if size == 1:
+            continue
+        if ld is None:
+            ld = stride
+        elif stride != ld * inner:
+            return None
+        inner *= size
+    if ld is None:
+        ld = t.shape[-1]
+    return (rows, ld) if ld >= t.shape[-1] else None
+
+
+def ckpt8_pack(x: torch.Tensor) -> Ckpt8:
+    """x [..., C] (bf16 or fp32, rows at one distance) in 8 bits: whole numbers in [-127, 127]
+    times a power of two for each block of 32. An element is off by at most half a step, 1/127
+    of its block's largest magnitude at worst; a block with inf or NaN decodes to NaN."""
+    if not (x.is_cuda and x.dtype in _DTYPES and x.dim() >= 1 and x.shape[-1] >= 1):
+        raise ValueError("ckpt8_pack: x must be a bf16 or fp32 CUDA tensor with at least one column")
+    at = _rows(x)
+    if at is None:
+        x = x.contiguous()
+        at = _rows(x)
+    rows, ld = at
+    C = x.shape[-1]
+    w, ns = _ckpt_widths(C)
+    codes = torch.empty((rows, w), dtype=torch.int8, device=x.device)
+    scales = torch.empty((rows, ns), dtype=torch.uint8, device=x.device)
+    with _on(x) as s:
+        st = _lib.lib().caj_ckpt_pack(_ptr(x), rows, C, ld, _DTYPES[x.dtype], _ptr(codes), _ptr(scales), s)
+    _lib.check(st, "caj_ckpt_pack")
+    return Ckpt8(codes, scales, tuple(x.shape))
+
+
+def ckpt8_unpack(c: Ckpt8, dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+    """The values a checkpoint stands for, contiguous [..., C] (exact in bf16 and fp32)."""
+    _check_ckpt("ckpt8_unpack", c)
+    if dtype not in _DTYPES:
+        raise ValueError("ckpt8_unpack: dtype must be bf16 or fp32")
+    _same_device("ckpt8_unpack", c.codes, c.scales)
+    x = torch.empty(c.shape, dtype=dtype, device=c.codes.device)
+    with _on(x) as s:
+        st = _lib.lib().caj_ckpt_unpack(_ptr(c.codes), _ptr(c.scales), c.rows, c.shape[-1], c.shape[-1],
+                                        _DTYPES[dtype], _ptr(x), s)
+    _lib.check(st, "caj_ckpt_unpack")
+    return x
+
+
+# --------------------------------------------------------------- rotary positions
+
+def rope_frequencies(dims: Union[int, Sequence[int]], base: float = 10000.0, factor: float = 1.0,
+                     original_length: Optional[int] = None, fast: float = 32.0, slow: float = 1.0,
+                     device: Union[str, torch.device] = "cuda"):
+    """(freq, axis) for rope_table. dims: the rotated channels, one number or one for each
+    position axis (even numbers, e.g. frames, rows, columns of a video); pair i of an axis of
+    d channels turns by base^(-2i/d) a position.
+
+    factor > 1 stretches positions for longer contexts: without original_length every
+    frequency is divided by it (linear interpolation); with it, only pairs that turn at most
+    `slow` times within original_length are, those that turn at least `fast` times are kept,
+    and those between are blended linearly in their number of turns."""
+    dims = [int(dims)] if isinstance(dims, int) else [int(d) for d in dims]
+    if not dims or any(d <= 0 or d % 2 for d in dims):
+        raise ValueError("rope_frequencies: dims must be positive even numbers")
+    if not (base > 0 and factor >= 1 and fast > slow):
+        raise ValueError("rope_frequencies: base > 0, factor >= 1 and fast > slow are needed")
+    freq = torch.cat([float(base) ** (-torch.arange(0, d, 2, dtype=torch.float64) / d) for d in dims])
+    axis = torch.cat([torch.full((d // 2,), a, dtype=torch.int32) for a, d in enumerate(dims)])
+    if factor > 1:
+        if original_length is None:
+            freq = freq / factor
+        else:
+            keep = ((freq * original_length / (2 * math.pi) - slow) / (fast - slow)).clamp(0, 1)
+            freq = freq * keep + freq / factor * (1 - keep)
+    return freq.to(device), axis.to(device)
+
+
+def rope_table(pos: torch.Tensor, freq: torch.Tensor, axis: Optional[torch.Tensor] = None,
+               mscale: float = 1.0):
+    """(cos, sin), each [N, P] fp32: mscale times the cosine and sine of
+    pos[n, axis[i]] * freq[i]. pos: [N] or [N, axes] int32 or int64; freq: [P] fp64; axis: [P]
+    int32 (None: all pairs turn with the first axis). Far positions lose nothing."""
+    if not (pos.is_cuda and pos.dtype in (torch.int32, torch.int64) and pos.dim() in (1, 2) and pos.is_contiguous()):
+        raise ValueError("rope_table: pos must be a contiguous int32 or int64 CUDA tensor [N] or [N, axes]")
+    if not (freq.dtype == torch.float64 and freq.dim() == 1 and freq.is_contiguous() and freq.numel()):
+        raise ValueError("rope_table: freq must be a contiguous fp64 tensor [P]")
+    if axis is not None and not (axis.dtype == torch.int32 and axis.shape == freq.shape and axis.is_contiguous()):
+        raise ValueError("rope_table: axis must be a contiguous int32 tensor [P]")
+    _same_device("rope_table", pos, freq, axis)
+    N, P, A = pos.shape[0], freq.numel(), pos.shape[1] if pos.dim() == 2 else 1
+    cos, sin = (torch.empty((N, P), dtype=torch.float32, device=pos.device) for _ in range(2))
+    with _on(pos) as s:
+        st = _lib.lib().caj_rope_table(_ptr(pos), int(pos.dtype == torch.int64), _ptr(freq), _ptr(axis), N, A, P,
+                                       float(mscale), _ptr(cos), _ptr(sin), s)
+    _lib.check(st, "caj_rope_table")
+    return cos, sin
+
+
+def _token_rows(what: str, name: str, t: torch.Tensor, B: int, N: int, width: int, like: torch.Tensor):
+    """t [B, N, width] with one distance between tokens: that distance. Raises otherwise."""
+    if not (t.is_cuda and t.dtype == like.dtype and tuple(t.shape) == (B, N, width)):
+        raise ValueError(f"{what}: {name} must be a {like.dtype} CUDA tensor [{B}, {N}, {width}]")
+    at = _rows(t)
+    if at is None or at[1] * t.element_size() % 16 or t.data_ptr() % 16:
+        raise ValueError(f"{what}: {name}'s tokens must lie at one distance, a multiple of 16 bytes, "
+                         "16-byte aligned, with neighbouring channels side by side")
+    return at[1]
+
+
+def _rope_shape(what, B, N, Hq, Hk, D, dtype, gq, gk, rope_cos, rope_sin, eps, norm, layout):
+    if norm not in _lib.NORMS or layout not in _lib.ROPE_LAYOUTS:
+        raise ValueError(f"{what}: norm is one of {sorted(_lib.NORMS)}, layout one of {sorted(_lib.ROPE_LAYOUTS)}")
+    for t in (rope_cos, rope_sin):
+        if not (t.is_cuda and t.dtype == torch.float32 and t.is_contiguous() and t.dim() == 2 and t.shape[0] == N
+                and t.shape == rope_cos.shape):
+            raise ValueError(f"{what}: rope tables must be contiguous fp32 CUDA tensors [N, pairs]")
+    full = 0
+    if norm == "none":
+        if gq is not None or gk is not None:
+            raise ValueError(f"{what}: norm 'none' takes no gains")
+    else:
+        for t in (gq, gk):
+            if t is None or not (t.is_cuda and t.dtype == torch.float32 and t.is_contiguous() and t.dim() == 1):
+                raise ValueError(f"{what}: gains must be contiguous fp32 CUDA tensors")
+        full = int(norm == "token" or gq.numel() != D or gk.numel() != D)
+        if full and (gq.numel() != Hq * D or gk.numel() != Hk * D):
+            raise ValueError(f"{what}: gains hold D values (norm 'head', shared by the heads) or heads * D")
+    return _lib.QkRopeShapeC(B, N, Hq, Hk, D, rope_cos.shape[1], _DTYPES[dtype], _lib.NORMS[norm],
+                             _lib.ROPE_LAYOUTS[layout], full, float(eps))
+
+
+def qk_norm_rope_fwd(xq, xk, xv, gq, gk, rope_cos, rope_sin, H: int, Hk: Optional[int] = None, eps: float = 1e-6,
+                     norm: str = "head", layout: str = "interleaved", txq=None, txk=None, txv=None):
+    """RMS norm of q and k, their rotation, and the attention's layout for q, k, v, in one pass.
+
+    xq [B, N, H*D], xk and xv [B, N, Hk*D] (Hk None: H), bf16 or fp32; slices of one fused
+    projection are fine. xv may be None. norm: "head" (gains [D] or [heads*D]), "token" (gains
+    [heads*D]) or "none" (gains None). layout: pairs (2i, 2i+1) ("interleaved") or (i, i+P)
+    ("half") of the first 2P channels of each head, P = rope_cos.shape[1]. With tangents txq,
+    txk, txv also their JVP. Returns (q, k, v) or (q, k, v, tq, tk, tv), each
+    [B, heads, N, D]; without xv, v and tv are left out."""
+    what = "qk_norm_rope_fwd"
+    Hk = H if Hk is None else Hk
+    if xq.dim() != 3 or H <= 0 or Hk <= 0 or xq.shape[2] % H or xq.dtype not in _DTYPES:
+        raise ValueError(f"{what}: xq must be a bf16 or fp32 tensor [B, N, H*D]")
+    B, N, D = xq.shape[0], xq.shape[1], xq.shape[2] // H
+    tangents = (txq, txk, txv)
+    tan = txq is not None
+    if (txk is None) == tan or (txv is not None) != (tan and xv is not None):
+        raise ValueError(f"{what}: give the tangents of all inputs or of none")
+    _same_device(what, xq, xk, xv, *tangents, gq, gk, rope_cos, rope_sin)
+    shape = _rope_shape(what, B, N, H, Hk, D, xq.dtype, gq, gk, rope_cos, rope_sin, eps, norm, layout)
+    for name, t, heads in (("q", xq, H), ("k", xk, Hk), ("v", xv, Hk), ("tq", txq, H), ("tk", txk, Hk),
+                           ("tv", txv, Hk)):
+        if t is not None:
+            setattr(shape, "ld" + name, _token_rows(what, "x" + name if len(name) == 1 else "tx" + name[1], t, B, N,
+                                                    heads * D, xq))
+
+    def out(t, heads):
+        return None if t is None else torch.empty((B, heads, N, D), dtype=xq.dtype, device=xq.device)
+    outs = [out(t, h) for t, h in zip((xq, xk, xv) + tangents, (H, Hk, Hk) * 2)]
+    if B * N:
+        with _on(xq) as s:
+            st = _lib.lib().caj_qk_rope_fwd(*[_ptr(t) for t in (xq, xk, xv) + tangents], _ptr(gq), _ptr(gk),
+                                            _ptr(rope_cos), _ptr(rope_sin), ctypes.byref(shape),
+                                            *[_ptr(t) for t in outs], s)
+        _lib.check(st, "caj_qk_rope_fwd")
+    return tuple(t for t in outs if t is not None)
+
+
+def qk_norm_rope_bwd(dq, dk, dv, xq, xk, gq, gk, rope_cos, rope_sin, eps: float = 1e-6, norm: str = "head",
+                     layout: str = "interleaved"):
+    """Gradients of qk_norm_rope_fwd's primal: (dxq, dxk, dxv, dgq, dgk).
+
+    dq [B, H, N, D], dk and dv [B, Hk, N, D] (dv None: no v, dxv None); xq, xk: the forward's
+    inputs, or their 8-bit checkpoints (Ckpt8 of shape [B, N, heads*D]), read as they are; None
+    with norm "none" (then dgq, dgk are None). dx [B, N, heads*D]; dg fp32, as long as the
+    gains. Deterministic."""
+    what = "qk_norm_rope_bwd"
+    if dq.dim() != 4 or dk.dim() != 4 or dq.dtype not in _DTYPES:
+        raise ValueError(f"{what}: dq, dk must be bf16 or fp32 tensors [B, heads, N, D]")
+    B, H, N, D = dq.shape
+    Hk = dk.shape[1]
+    for t, h in ((dq, H), (dk, Hk), (dv, Hk)):
+        if t is not None and not (t.is_cuda and t.is_contiguous() and t.dtype == dq.dtype
+                                  and tuple(t.shape) == (B, h, N, D)):
+            raise ValueError(f"{what}: dq, dk, dv must be contiguous CUDA tensors [B, heads, N, D] of one dtype")
+    shape = _rope_shape(what, B, N, H, Hk, D, dq.dtype, gq, gk, rope_cos, rope_sin, eps, norm, layout)
+    ckpt = isinstance(xq, Ckpt8)
+    xs, scales = [None, None], [None, None]
+    if norm == "none":
+        if xq is not None or xk is not None:
+            raise ValueError(f"{what}: norm 'none' reads no inputs: give None")
+    elif ckpt != isinstance(xk, Ckpt8):
+        raise ValueError(f"{what}: xq and xk are both tensors or both checkpoints")
+    else:
+        for i, (name, x, h) in enumerate((("xq", xq, H), ("xk", xk, Hk))):
+            if ckpt:
+                if tuple(x.shape) != (B, N, h * D):
+                    raise ValueError(f"{what}: {name}'s checkpoint must be of shape [{B}, {N}, {h * D}]")
+                _check_ckpt(what, x)
+                xs[i], scales[i] = x.codes, x.scales
+            else:
+                if x is None:
+                    raise ValueError(f"{what}: {name} is needed")
+                setattr(shape, ("ldq", "ldk")[i], _token_rows(what, name, x, B, N, h * D, dq))
+                xs[i] = x
+    _same_device(what, dq, dk, dv, *xs, *scales, gq, gk, rope_cos, rope_sin)
+
+    def out(t, h):
+        return None if t is None else torch.empty((B, N, h * D), dtype=dq.dtype, device=dq.device)
+    dx = [out(dq, H), out(dk, Hk), out(dv, Hk)]
+    dg = [None if g is None else torch.zeros_like(g) if B * N == 0 else torch.empty_like(g) for g in (gq, gk)]
+    if B * N:
+        nbytes = ctypes.c_size_t(0)
+        _lib.check(_lib.lib().caj_qk_rope_bwd_workspace(ctypes.byref(shape), ctypes.byref(nbytes)),
+                   "caj_qk_rope_bwd_workspace")
+        with _on(dq) as s:
+            ws = torch.empty(nbytes.value, dtype=torch.uint8, device=dq.device)
+            st = _lib.lib().caj_qk_rope_bwd(_ptr(dq), _ptr(dk), _ptr(dv), _ptr(xs[0]), _ptr(xs[1]), _ptr(scales[0]),
+                                            _ptr(scales[1]), _ptr(gq), _ptr(gk), _ptr(rope_cos), _ptr(rope_sin),
+                                            ctypes.byref(shape), *[_ptr(t) for t in dx], _ptr(dg[0]), _ptr(dg[1]),
+                                            _ptr(ws), nbytes.value, s)
+        _lib.check(st, "caj_qk_rope_bwd")
+    return (*dx, *dg)

@@ -1,0 +1,228 @@
+// C-ABI front end of the block operators around the attention: rotary tables, the
+// norm + rotation of q and k, and 8-bit checkpoints. Arguments are checked on the
+// host before anything is launched (contracts: include/causaljvp.h).
+#include <cmath>
+
+#include "api_internal.h"
+#include "ckpt8.cuh"
+#include "kernels.h"
+
+using caj::aligned_to;
+
+namespace {
+
+caj_status done(cudaError_t e) { return e == cudaSuccess ? CAJ_OK : caj::cuda_fail(e); }
+
+int64_t size_of(int32_t dtype) { return dtype == CAJ_DTYPE_BF16 ? 2 : 4; }
+
+caj_status ckpt8(const void *x, void *out, const int8_t *codes, const uint8_t *scales, int64_t rows, int32_t cols,
+                 int64_t ld, int32_t dtype, bool unpack, void *stream) {
+  if (dtype != CAJ_DTYPE_F32 && dtype != CAJ_DTYPE_BF16) return CAJ_ERR_INVALID_ARG;
+  if (rows < 0 || cols <= 0 || ld < cols) return CAJ_ERR_INVALID_ARG;
+  if (rows == 0) return CAJ_OK;
+  const void *values = unpack ? out : x;
+  if (!values || !aligned_to(values, uintptr_t(size_of(dtype)))) return CAJ_ERR_INVALID_ARG;
+  if (!codes || !aligned_to(codes, 16) || !scales || !aligned_to(scales, 4)) return CAJ_ERR_INVALID_ARG;
+  const int64_t nb = (int64_t(cols) + caj::ck::kBlock - 1) / caj::ck::kBlock;
+  const int64_t limit = (int64_t(1) << 31) - 1;
+  if (rows > limit / nb) return CAJ_ERR_UNSUPPORTED;
+  const caj_status st = caj::check_device();
+  if (st != CAJ_OK) return st;
+  caj::Ckpt8Params p{};
+  p.x = x;
+  p.out = out;
+  p.codes = const_cast<int8_t *>(codes);
+  p.scales = const_cast<uint8_t *>(scales);
+  p.ld = ld;
+  p.total = uint32_t(rows * nb);
+  p.cols = cols;
+  p.nb = int32_t(nb);
+  p.ns = int32_t((nb + 3) & ~int64_t(3));
+  return done(caj::launch_ckpt8(p, unpack, dtype == CAJ_DTYPE_BF16, static_cast<cudaStream_t>(stream)));
+}
+
+// The checks that the forward and the backward share.
+caj_status check_rope(const caj_qk_rope_shape *s, const float *gq, const float *gk, const float *cos,
+                      const float *sin) {
+  if (!s) return CAJ_ERR_INVALID_ARG;
+  if (s->B <= 0 || s->N <= 0 || s->Hq <= 0 || s->Hk <= 0 || s->D <= 0 || s->pairs <= 0) return CAJ_ERR_INVALID_ARG;
+  if (s->dtype != CAJ_DTYPE_F32 && s->dtype != CAJ_DTYPE_BF16) return CAJ_ERR_INVALID_ARG;
+  if (s->norm < CAJ_NORM_NONE || s->norm > CAJ_NORM_TOKEN) return CAJ_ERR_INVALID_ARG;
+  if (s->layout != CAJ_ROPE_INTERLEAVED && s->layout != CAJ_ROPE_HALF) return CAJ_ERR_INVALID_ARG;
+  if (s->gain_full != 0 && s->gain_full != 1) return CAJ_ERR_INVALID_ARG;
+  if (s->norm == CAJ_NORM_TOKEN && !s->gain_full) return CAJ_ERR_INVALID_ARG;
+  if (!cos || !sin || !aligned_to(cos, 16) || !aligned_to(sin, 16)) return CAJ_ERR_INVALID_ARG;
+  if (2 * int64_t(s->pairs) > s->D) return CAJ_ERR_INVALID_ARG;
+  if (s->norm != CAJ_NORM_NONE) {
+    if (!gq || !gk || !aligned_to(gq, 16) || !aligned_to(gk, 16)) return CAJ_ERR_INVALID_ARG;
+    if (!(s->eps > 0.f) || std::isinf(s->eps)) return CAJ_ERR_INVALID_ARG;
+  }
+  if (s->D != 32 && s->D != 64 && s->D != 128 && s->D != 256) return CAJ_ERR_UNSUPPORTED;
+  if (s->pairs % 8) return CAJ_ERR_UNSUPPORTED;
+  const int64_t wide = int64_t(s->Hq > s->Hk ? s->Hq : s->Hk) * s->D;
+  if (wide > 8192) return CAJ_ERR_UNSUPPORTED;
+  if (int64_t(s->B) * s->N > (int64_t(1) << 31) - 1) return CAJ_ERR_UNSUPPORTED;
+  return CAJ_OK;
+}
+
+bool good_ld(int64_t ld, int64_t width, int32_t dtype) {
+  return ld >= width && ld * size_of(dtype) % 16 == 0 && ld < (int64_t(1) << 31);
+}
+
+void fill_rope(caj::QkRopeParams *p, const caj_qk_rope_shape *s, const float *gq, const float *gk, const float *cos,
+               const float *sin) {
+  p->g[0] = gq;
+  p->g[1] = gk;
+  p->cos = cos;
+  p->sin = sin;
+  p->B = s->B;
+  p->N = s->N;
+  p->Hq = s->Hq;
+  p->Hk = s->Hk;
+  p->D = s->D;
+  p->P = s->pairs;
+  p->eps = s->eps;
+  p->norm = s->norm;
+  p->half = s->layout == CAJ_ROPE_HALF;
+  p->gain_full = s->gain_full;
+}
+
+size_t rope_gain_len(const caj_qk_rope_shape *s, int32_t heads) {
+  return size_t(s->gain_full ? int64_t(heads) * s->D : s->D);
+}
+
+}  // namespace
+
+extern "C" {
+
+caj_status caj_ckpt_pack(const void *x, int64_t rows, int32_t cols, int64_t ld, int32_t dtype, int8_t *codes,
+                          uint8_t *scales, void *stream) {
+  return ckpt8(x, nullptr, codes, scales, rows, cols, ld, dtype, false, stream);
+}
+
+caj_status caj_ckpt_unpack(const int8_t *codes, const uint8_t *scales, int64_t rows, int32_t cols, int64_t ld,
+                            int32_t dtype, void *x, void *stream) {
+  return ckpt8(nullptr, x, codes, scales, rows, cols, ld, dtype, true, stream);
+}
+
+caj_status caj_rope_table(const void *pos, int32_t pos64, const double *freq, const int32_t *axis, int64_t N,
+                          int32_t axes, int32_t pairs, float mscale, float *cos, float *sin, void *stream) {
+  if (N < 0 || axes <= 0 || pairs <= 0 || (pos64 != 0 && pos64 != 1)) return CAJ_ERR_INVALID_ARG;
+  if (!std::isfinite(mscale)) return CAJ_ERR_INVALID_ARG;
+  if (N == 0) return CAJ_OK;
+  if (!pos || !aligned_to(pos, pos64 ? 8 : 4) || !freq || !aligned_to(freq, 8)) return CAJ_ERR_INVALID_ARG;
+  if (axis && !aligned_to(axis, 4)) return CAJ_ERR_INVALID_ARG;
+  if (!cos || !sin || !aligned_to(cos, 4) || !aligned_to(sin, 4)) return CAJ_ERR_INVALID_ARG;
+  if (N > (int64_t(1) << 40) / pairs) return CAJ_ERR_UNSUPPORTED;
+  const caj_status st = caj::check_device();
+  if (st != CAJ_OK) return st;
+  caj::RopeTableParams p{};
+  p.pos = pos;
+  p.freq = freq;
+  p.axis = axis;
+  p.cos = cos;
+  p.sin = sin;
+  p.N = N;
+  p.A = axes;
+  p.P = pairs;
+  p.mscale = mscale;
+  return done(caj::launch_rope_table(p, pos64 != 0, static_cast<cudaStream_t>(stream)));
+}
+
+caj_status caj_qk_rope_fwd(const void *xq, const void *xk, const void *xv, const void *txq, const void *txk,
+                           const void *txv, const float *gq, const float *gk, const float *rope_cos,
+                           const float *rope_sin, const caj_qk_rope_shape *shape, void *q, void *k, void *v,
+                           void *tq, void *tk, void *tv, void *stream) {
+  caj_status st = check_rope(shape, gq, gk, rope_cos, rope_sin);
+  if (st != CAJ_OK) return st;
+  const bool tan = txq || txk || txv;
+  const void *x[3] = {xq, xk, xv}, *tx[3] = {txq, txk, txv};
+  void *y[3] = {q, k, v}, *ty[3] = {tq, tk, tv};
+  const int64_t ld[3] = {shape->ldq, shape->ldk, shape->ldv}, tld[3] = {shape->ldtq, shape->ldtk, shape->ldtv};
+  caj::QkRopeParams p{};
+  fill_rope(&p, shape, gq, gk, rope_cos, rope_sin);
+  for (int i = 0; i < 3; ++i) {
+    if (i == 2 && !xv) {
+      if (v || txv || tv) return CAJ_ERR_INVALID_ARG;
+      continue;
+    }
+    const int64_t width = int64_t(i ? shape->Hk : shape->Hq) * shape->D;
+    if (!x[i] || !y[i] || !aligned_to(x[i], 16) || !aligned_to(y[i], 16)) return CAJ_ERR_INVALID_ARG;
+    if (!good_ld(ld[i], width, shape->dtype)) return CAJ_ERR_INVALID_ARG;
+    if (tan) {
+      if (!tx[i] || !ty[i] || !aligned_to(tx[i], 16) || !aligned_to(ty[i], 16)) return CAJ_ERR_INVALID_ARG;
+      if (!good_ld(tld[i], width, shape->dtype)) return CAJ_ERR_INVALID_ARG;
+    }
+    p.x[i] = x[i];
+    p.tx[i] = tx[i];
+    p.y[i] = y[i];
+    p.ty[i] = ty[i];
+    p.ld[i] = ld[i];
+    p.tld[i] = tld[i];
+  }
+  st = caj::check_device();
+  if (st != CAJ_OK) return st;
+  return done(caj::launch_qk_rope_fwd(p, shape->dtype == CAJ_DTYPE_BF16, static_cast<cudaStream_t>(stream)));
+}
+
+caj_status caj_qk_rope_bwd_workspace(const caj_qk_rope_shape *shape, size_t *bytes) {
+  static const float probe[4] __attribute__((aligned(16))) = {};
+  if (!bytes) return CAJ_ERR_INVALID_ARG;
+  const caj_status st = check_rope(shape, probe, probe, probe, probe);
+  if (st != CAJ_OK) return st;
+  *bytes = 0;
+  if (shape->norm != CAJ_NORM_NONE) {
+    const size_t blocks = size_t(caj::qk_rope_bwd_blocks(shape->B, shape->N, shape->Hq, shape->Hk, shape->D));
+    *bytes = blocks * (rope_gain_len(shape, shape->Hq) + rope_gain_len(shape, shape->Hk)) * sizeof(float);
+  }
+  return CAJ_OK;
+}
+
+caj_status caj_qk_rope_bwd(const void *dq, const void *dk, const void *dv, const void *xq, const void *xk,
+                           const uint8_t *xq_scales, const uint8_t *xk_scales, const float *gq, const float *gk,
+                           const float *rope_cos, const float *rope_sin, const caj_qk_rope_shape *shape, void *dxq,
+                           void *dxk, void *dxv, float *dgq, float *dgk, void *workspace, size_t workspace_bytes,
+                           void *stream) {
+  caj_status st = check_rope(shape, gq, gk, rope_cos, rope_sin);
+  if (st != CAJ_OK) return st;
+  const void *dy[3] = {dq, dk, dv}, *x[2] = {xq, xk};
+  void *dx[3] = {dxq, dxk, dxv};
+  const uint8_t *scales[2] = {xq_scales, xk_scales};
+  float *dg[2] = {dgq, dgk};
+  const int64_t ld[2] = {shape->ldq, shape->ldk};
+  caj::QkRopeParams p{};
+  fill_rope(&p, shape, gq, gk, rope_cos, rope_sin);
+  const bool normed = shape->norm != CAJ_NORM_NONE;
+  if (!xq_scales != !xk_scales) return CAJ_ERR_INVALID_ARG;
+  for (int i = 0; i < 3; ++i) {
+    if (i == 2 && !dv) {
+      if (dxv) return CAJ_ERR_INVALID_ARG;
+      continue;
+    }
+    if (!dy[i] || !dx[i] || !aligned_to(dy[i], 16) || !aligned_to(dx[i], 16)) return CAJ_ERR_INVALID_ARG;
+    p.dy[i] = dy[i];
+    p.dx[i] = dx[i];
+    if (i == 2 || !normed) continue;
+    const int32_t heads = i ? shape->Hk : shape->Hq;
+    if (!x[i] || !aligned_to(x[i], 16) || !dg[i] || !aligned_to(dg[i], 4)) return CAJ_ERR_INVALID_ARG;
+    if (!scales[i] && !good_ld(ld[i], int64_t(heads) * shape->D, shape->dtype)) return CAJ_ERR_INVALID_ARG;
+    p.x[i] = x[i];
+    p.x_scales[i] = scales[i];
+    p.ld[i] = ld[i];
+    p.dg[i] = dg[i];
+  }
+  size_t need = 0;
+  st = caj_qk_rope_bwd_workspace(shape, &need);
+  if (st != CAJ_OK) return st;
+  if (need && (!workspace || !aligned_to(workspace, 16) || workspace_bytes < need)) return CAJ_ERR_INVALID_ARG;
+  st = caj::check_device();
+  if (st != CAJ_OK) return st;
+  p.blocks = caj::qk_rope_bwd_blocks(shape->B, shape->N, shape->Hq, shape->Hk, shape->D);
+  if (normed) {
+    p.partial[0] = static_cast<float *>(workspace);
+    p.partial[1] = p.partial[0] + size_t(p.blocks) * rope_gain_len(shape, shape->Hq);
+  }
+  return done(caj::launch_qk_rope_bwd(p, shape->dtype == CAJ_DTYPE_BF16, static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

@@ -1,0 +1,199 @@
+// 8-bit activation checkpoints: packing rows of bf16 or fp32 values into codes and
+// scale bytes, and back (format and rounding: ckpt8.cuh).
+//
+// Memory-bound: 3.03 bytes a value for bf16 (2 in, 1.03 out, or the reverse).
+// Vector form: four lanes hold a block, eight values each (one or two 16-byte
+// loads); the block's largest magnitude is a two-step shuffle of ordered bits.
+// Each thread takes kUnroll blocks a grid apart, with all loads issued first, to
+// keep enough bytes in flight.
+// Rows whose 16-byte vectors do not line up (C not a multiple of 8, or a base or
+// row stride that is not 16-byte aligned) take the lane form: one lane per value,
+// coalesced 2- or 4-byte accesses, the maximum by one redux instruction.
+#include <cuda_runtime.h>
+
+#include "ckpt8.cuh"
+#include "kernels.h"
+#include "vec8.cuh"
+
+namespace caj {
+namespace {
+
+constexpr int kUnroll = 4;
+constexpr int kThreads = 256;
+
+// Scale byte of block `blk`; the row's last block also zeroes the padding bytes.
+__device__ __forceinline__ void store_scale(uint8_t *row, int32_t blk, int32_t nb, int32_t ns, uint32_t s) {
+  row[blk] = uint8_t(s);
+  if (blk == nb - 1)
+    for (int32_t i = nb; i < ns; ++i) row[i] = 0;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) pack_vec_kernel(const Ckpt8Params p) {
+  const uint32_t nb = uint32_t(p.nb), total = p.total;
+  const uint32_t step = gridDim.x * (kThreads / 4);
+  const uint32_t first = blockIdx.x * (kThreads / 4) + (threadIdx.x >> 2);
+  const int part = threadIdx.x & 3;
+  v8::Raw<T> raw[kUnroll];
+  uint32_t row[kUnroll], blk[kUnroll];
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) {
+    const uint64_t g = uint64_t(first) + uint64_t(u) * step;
+    row[u] = g < total ? uint32_t(g) / nb : 0xFFFFFFFFu;
+    blk[u] = uint32_t(g) - row[u] * nb;
+    raw[u] = v8::zero<T>();
+    const int32_t c = int32_t(blk[u]) * ck::kBlock + 8 * part;
+    if (g < total && c < p.cols)  // cols is a multiple of 8 here
+      raw[u] = v8::load(static_cast<const T *>(p.x) + size_t(row[u]) * p.ld + c);
+  }
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) {
+    float f[8];
+    v8::unpack(raw[u], f);
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, ck::mag_bits(f[i]));
+    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+    if (row[u] == 0xFFFFFFFFu) continue;
+    const uint32_t s = ck::scale_of(m);
+    uint2 codes = make_uint2(0, 0);
+    if (s != 255u) {
+      const float up = ck::up_of(s);
+      ck::saturate(f, s);
+      codes.x = ck::pack_codes4(f[0], f[1], f[2], f[3], up);
+      codes.y = ck::pack_codes4(f[4], f[5], f[6], f[7], up);
+    }
+    const size_t base = (size_t(row[u]) * nb + blk[u]) * ck::kBlock + 8 * part;
+    __stcs(reinterpret_cast<uint2 *>(p.codes + base), codes);
+    if (part == 0) store_scale(p.scales + size_t(row[u]) * p.ns, int32_t(blk[u]), p.nb, p.ns, s);
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) unpack_vec_kernel(const Ckpt8Params p) {
+  const uint32_t nb = uint32_t(p.nb), total = p.total;
+  const uint32_t step = gridDim.x * (kThreads / 4);
+  const uint32_t first = blockIdx.x * (kThreads / 4) + (threadIdx.x >> 2);
+  const int part = threadIdx.x & 3;
+  uint2 codes[kUnroll];
+  uint32_t row[kUnroll], scale[kUnroll];
+  int32_t col[kUnroll];
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) {
+    const uint64_t g = uint64_t(first) + uint64_t(u) * step;
+    row[u] = g < total ? uint32_t(g) / nb : 0xFFFFFFFFu;
+    const uint32_t blk = uint32_t(g) - row[u] * nb;
+    col[u] = int32_t(blk) * ck::kBlock + 8 * part;
+    codes[u] = make_uint2(0, 0);
+    scale[u] = 0;
+    if (g < total) {
+      codes[u] = __ldcs(reinterpret_cast<const uint2 *>(p.codes + (size_t(row[u]) * nb + blk) * ck::kBlock + 8 * part));
+      scale[u] = __ldg(p.scales + size_t(row[u]) * p.ns + blk);
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) {
+    if (row[u] == 0xFFFFFFFFu || col[u] >= p.cols) continue;
+    const float unit = ck::unit_of(scale[u]);
+    float f[8];
+    ck::unpack_codes4(codes[u].x, unit, f[0], f[1], f[2], f[3]);
+    ck::unpack_codes4(codes[u].y, unit, f[4], f[5], f[6], f[7]);
+    v8::Raw<T> r;
+    v8::pack(f, r);
+    v8::store(static_cast<T *>(p.out) + size_t(row[u]) * p.ld + col[u], r);
+  }
+}
+
+// One lane per value: blocks are dealt to warps a grid apart, kLaneUnroll at a time.
+constexpr int kLaneUnroll = 8;
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) pack_lane_kernel(const Ckpt8Params p) {
+  const uint32_t nb = uint32_t(p.nb), total = p.total;
+  const uint32_t step = gridDim.x * (kThreads / 32);
+  const uint32_t first = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  float v[kLaneUnroll];
+  uint32_t row[kLaneUnroll], blk[kLaneUnroll];
+#pragma unroll
+  for (int u = 0; u < kLaneUnroll; ++u) {
+    const uint64_t g = uint64_t(first) + uint64_t(u) * step;
+    row[u] = g < total ? uint32_t(g) / nb : 0xFFFFFFFFu;
+    blk[u] = uint32_t(g) - row[u] * nb;
+    const int32_t c = int32_t(blk[u]) * ck::kBlock + lane;
+    v[u] = 0.f;
+    if (g < total && c < p.cols) v[u] = v8::to_float(static_cast<const T *>(p.x)[size_t(row[u]) * p.ld + c]);
+  }
+#pragma unroll
+  for (int u = 0; u < kLaneUnroll; ++u) {
+    const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, ck::mag_bits(v[u]));
+    if (row[u] == 0xFFFFFFFFu) continue;
+    const uint32_t s = ck::scale_of(m);
+    float f[1] = {v[u]};
+    ck::saturate(f, s);
+    const uint32_t code = s == 255u ? 0u : ck::code_word(f[0], ck::up_of(s));
+    p.codes[(size_t(row[u]) * nb + blk[u]) * ck::kBlock + lane] = int8_t(code & 0xFFu);
+    if (lane == 0) store_scale(p.scales + size_t(row[u]) * p.ns, int32_t(blk[u]), p.nb, p.ns, s);
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) unpack_lane_kernel(const Ckpt8Params p) {
+  const uint32_t nb = uint32_t(p.nb), total = p.total;
+  const uint32_t step = gridDim.x * (kThreads / 32);
+  const uint32_t first = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  int8_t code[kLaneUnroll];
+  uint32_t row[kLaneUnroll], scale[kLaneUnroll];
+  int32_t col[kLaneUnroll];
+#pragma unroll
+  for (int u = 0; u < kLaneUnroll; ++u) {
+    const uint64_t g = uint64_t(first) + uint64_t(u) * step;
+    row[u] = g < total ? uint32_t(g) / nb : 0xFFFFFFFFu;
+    const uint32_t blk = uint32_t(g) - row[u] * nb;
+    col[u] = int32_t(blk) * ck::kBlock + lane;
+    code[u] = 0;
+    scale[u] = 0;
+    if (g < total) {
+      code[u] = p.codes[(size_t(row[u]) * nb + blk) * ck::kBlock + lane];
+      scale[u] = __ldg(p.scales + size_t(row[u]) * p.ns + blk);
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kLaneUnroll; ++u) {
+    if (row[u] == 0xFFFFFFFFu || col[u] >= p.cols) continue;
+    T o;
+    v8::from_float(float(code[u]) * ck::unit_of(scale[u]), o);
+    static_cast<T *>(p.out)[size_t(row[u]) * p.ld + col[u]] = o;
+  }
+}
+
+template <typename T>
+cudaError_t launch(const Ckpt8Params &p, bool unpack, bool vec, cudaStream_t stream) {
+  const uint32_t per_cta = vec ? kThreads / 4 * kUnroll : kThreads / 32 * kLaneUnroll;
+  const unsigned grid = unsigned((uint64_t(p.total) + per_cta - 1) / per_cta);
+  if (unpack) {
+    if (vec)
+      unpack_vec_kernel<T><<<grid, kThreads, 0, stream>>>(p);
+    else
+      unpack_lane_kernel<T><<<grid, kThreads, 0, stream>>>(p);
+  } else {
+    if (vec)
+      pack_vec_kernel<T><<<grid, kThreads, 0, stream>>>(p);
+    else
+      pack_lane_kernel<T><<<grid, kThreads, 0, stream>>>(p);
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_ckpt8(const Ckpt8Params &p, bool unpack, bool bf16, cudaStream_t stream) {
+  const void *base = unpack ? p.out : p.x;
+  const int64_t size = bf16 ? 2 : 4;
+  const bool vec = p.cols % 8 == 0 && (reinterpret_cast<uintptr_t>(base) & 15u) == 0 && (p.ld * size) % 16 == 0;
+  return bf16 ? launch<__nv_bfloat16>(p, unpack, vec, stream) : launch<float>(p, unpack, vec, stream);
+}
+
+}  // namespace caj

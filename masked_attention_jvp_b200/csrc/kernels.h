@@ -158,6 +158,45 @@ struct OutProjParams {
   int32_t fault_mode;    // test hook: 1 = the producer issues no copies
 };
 
+// Rotary tables: cos, sin [N, P] of pos[n][axis[i]] * freq[i].
+struct RopeTableParams {
+  const void *pos;       // [N, A] int32 or int64
+  const double *freq;    // [P]
+  const int32_t *axis;   // [P], or null: all 0
+  float *cos, *sin;      // [N, P]
+  int64_t N;
+  int32_t A, P;
+  float mscale;
+};
+
+// Norm + rotation of q and k (and v's new layout), forward or backward; index 0, 1, 2
+// is q, k, v.
+struct QkRopeParams {
+  const void *x[3], *tx[3];    // [B, N, heads * D], token distance ld / tld elements
+  void *y[3], *ty[3];          // [B, heads, N, D]
+  const void *dy[3];           // backward: [B, heads, N, D]
+  void *dx[3];                 // [B, N, heads * D]
+  const uint8_t *x_scales[2];  // backward: x[] holds an 8-bit checkpoint's codes, these its scales
+  float *dg[2], *partial[2];   // gains' gradient; [blocks][gain length]
+  int64_t ld[3], tld[3];
+  const float *g[2];           // [D], or [heads * D] with gain_full
+  const float *cos, *sin;      // [N, P]
+  int32_t B, N, Hq, Hk, D, P;
+  float eps;
+  int32_t norm, half, gain_full, blocks;
+};
+
+// 8-bit checkpoints of `rows` rows: nb blocks and ns scale bytes a row, total = rows * nb.
+struct Ckpt8Params {
+  const void *x;       // pack: rows of `cols` values, ld elements apart
+  void *out;           // unpack: likewise
+  int8_t *codes;       // [rows, 32 nb]
+  uint8_t *scales;     // [rows, ns]
+  int64_t ld;
+  uint32_t total;
+  int32_t cols, nb, ns;
+};
+
 // Signal barrier of a context-parallel group: pads[r] is rank r's pad of
 // kMaxShards words as mapped in this process.
 struct SignalParams {
@@ -189,6 +228,11 @@ cudaError_t launch_fwd_jvp_simt_f32(const SimtParams &p, int D, cudaStream_t str
 cudaError_t launch_qk_norm_rope_jvp(const PrologueParams &p, cudaStream_t stream);
 cudaError_t launch_attn_bwd_sm100(const BwdParams &p, int D, cudaStream_t stream);
 cudaError_t read_and_clear_bwd_error(uint32_t *out);
+cudaError_t launch_rope_table(const RopeTableParams &p, bool pos64, cudaStream_t stream);
+cudaError_t launch_qk_rope_fwd(const QkRopeParams &p, bool bf16, cudaStream_t stream);
+cudaError_t launch_qk_rope_bwd(const QkRopeParams &p, bool bf16, cudaStream_t stream);
+int32_t qk_rope_bwd_blocks(int32_t B, int32_t N, int32_t Hq, int32_t Hk, int32_t D);
+cudaError_t launch_ckpt8(const Ckpt8Params &p, bool unpack, bool bf16, cudaStream_t stream);
 cudaError_t launch_signal_barrier(const SignalParams &p, cudaStream_t stream);
 cudaError_t launch_out_proj_sm100(const OutProjParams &p, cudaStream_t stream);
 cudaError_t read_and_clear_proj_error(uint32_t *out);
