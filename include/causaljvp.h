@@ -492,6 +492,67 @@ caj_status caj_qk_rope_bwd(const void *dq, const void *dk, const void *dv, const
                            void *dxk, void *dxv, float *dgq, float *dgk, void *workspace,
                            size_t workspace_bytes, void *stream);
 
+/*
+ * Linear layer with its epilogue in primal-tangent form, and its gradient. (caj_out_proj_jvp
+ * is the plain projection of a primal-tangent pair.) With z = x W^T + b:
+ *   y   = act(z) + res
+ *   ty  = act'(z) * (tx W^T) + tres
+ *   pre = z as an 8-bit checkpoint (caj_ckpt_pack's format), for the gradient
+ * act is a caj_act: none, GELU in its tanh form, GELU, or SiLU.
+ *   in : x, tx      [M, K] bf16, rows ldx, ldtx elements apart; tx null: primal only
+ *        w          [C, K] bf16, contiguous
+ *        bias       [C] bf16, or null
+ *        res, tres  [M, C] bf16, rows ldres, ldtres apart, or null (tres needs tx)
+ *   out: y, ty      [M, C] bf16, contiguous, fully overwritten (ty null without tx)
+ *        pre_codes, pre_scales  z's checkpoint, rows of C values; both null: none
+ *   workspace       caj_linear_act_fwd_workspace() bytes (0 for most sizes), 16-byte
+ *                   aligned; no other work may use it until the call is done
+ * Sums are fp32; bias, activation, tangent and residual are applied in fp32 before
+ * the one rounding to bf16.
+ *
+ * Gradient of the primal, with dz = dy * act'(z) (the residual's gradient is dy):
+ *   dx = dz W,  dW = dz^T x,  db = sum over rows of dz
+ *   in : dy         [M, C] bf16, rows ldy apart
+ *        x          [M, K] bf16, rows ldx apart, or with x_scales non-null the codes of
+ *                   its 8-bit checkpoint (needed for dw)
+ *        w          as above (needed for dx)
+ *        pre_codes, pre_scales  z's checkpoint (needed with an activation): act' is
+ *                   taken at the value that the checkpoint holds
+ *   out: dx         [M, K] bf16;  dw [C, K] bf16;  db [C] fp32; each may be null
+ *   workspace       caj_linear_act_bwd_workspace() bytes, 256-byte aligned
+ * dz is rounded to bf16 for the products; db sums it unrounded. Deterministic (no
+ * atomics; the split of a long contraction depends on the sizes alone).
+ *
+ * Pointers 16-byte aligned (scales and db 4), row distances multiples of 8 elements
+ * and at least the row; K and C multiples of 8 (CAJ_ERR_UNSUPPORTED otherwise, and
+ * for M > 2^30 or more than 2^31 checkpoint blocks). M = 0 is not a call
+ * (CAJ_ERR_INVALID_ARG). Return CAJ_OK once enqueued, CAJ_ERR_INVALID_ARG /
+ * CAJ_ERR_UNSUPPORTED without launching, or CAJ_ERR_CUDA. Bounded-wait failures are
+ * reported by caj_last_device_status.
+ */
+typedef enum { CAJ_ACT_NONE = 0, CAJ_ACT_GELU_TANH = 1, CAJ_ACT_GELU = 2, CAJ_ACT_SILU = 3 } caj_act;
+typedef struct {
+  int64_t M;
+  int32_t K, C;
+  int32_t act;                          /* caj_act */
+  int64_t ldx, ldtx, ldres, ldtres;     /* forward (ldx: backward too) */
+  int64_t ldy;                          /* backward: dy */
+} caj_linear_act_shape;
+
+caj_status caj_linear_act_fwd_workspace(const caj_linear_act_shape *shape, int32_t tangent,
+                                        size_t *bytes);
+caj_status caj_linear_act_fwd(const void *x, const void *tx, const void *w, const void *bias,
+                              const void *res, const void *tres,
+                              const caj_linear_act_shape *shape, void *y, void *ty,
+                              int8_t *pre_codes, uint8_t *pre_scales, void *workspace,
+                              size_t workspace_bytes, void *stream);
+caj_status caj_linear_act_bwd_workspace(const caj_linear_act_shape *shape, int32_t x_ckpt,
+                                        size_t *bytes);
+caj_status caj_linear_act_bwd(const void *dy, const void *x, const uint8_t *x_scales,
+                              const void *w, const int8_t *pre_codes, const uint8_t *pre_scales,
+                              const caj_linear_act_shape *shape, void *dx, void *dw, float *db,
+                              void *workspace, size_t workspace_bytes, void *stream);
+
 /* Synchronises `stream`, then reads and clears the library's device error word.
  * Returns CAJ_OK, CAJ_ERR_DEVICE_TIMEOUT (a kernel gave up: it abandoned a wait
  * or refused to run; its outputs are undefined) or CAJ_ERR_CUDA. */
@@ -500,7 +561,8 @@ caj_status caj_last_device_status(void *stream);
 /* Detail of the last device error (0 if none). Valid after
  * caj_last_device_status returned CAJ_ERR_DEVICE_TIMEOUT:
  *   0x100 | site   a bounded wait expired at the numbered wait site (site 0xF0:
- *                  the signal barrier, caj_signal_barrier);
+ *                  the signal barrier, caj_signal_barrier; sites 0x21 to 0x26:
+ *                  the linear layer's products);
  *   0x200          the dynamic shared memory was not 1 KiB aligned;
  *   0x300          a forward launch met a query tile of the other kind than it
  *                  was built for (an internal partitioning error). */

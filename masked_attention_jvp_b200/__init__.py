@@ -33,15 +33,15 @@ __all__ = ["attention_jvp", "attn_fwd_jvp", "attn_fwd_jvp_out", "attn_fwd_jvp_sc
            "ipc_export", "ipc_open", "ipc_close", "part_query_tiles", "attn_bwd", "qk_norm_rope_jvp", "out_proj_jvp", "MaskDesc", "CajError", "visible_pairs",
            "row_key_ranges", "qtile_key_tiles", "device_status", "flops", "EXPORTED", "LIB_PATH",
            "BLOCK_M", "BLOCK_N", "Ckpt8", "ckpt8_pack", "ckpt8_unpack", "rope_frequencies", "rope_table",
-           "qk_norm_rope_fwd", "qk_norm_rope_bwd"]
+           "qk_norm_rope_fwd", "qk_norm_rope_bwd", "linear_act_fwd", "linear_act_bwd"]
 
 BLOCK_M = 128  # query rows per tile of both kernels
 BLOCK_N = 64   # keys per tile of the tensor-core kernel
 
 _DTYPES = {torch.float32: _lib.CAJ_DTYPE_F32, torch.bfloat16: _lib.CAJ_DTYPE_BF16}
 
-from .block import (Ckpt8, ckpt8_pack, ckpt8_unpack, qk_norm_rope_bwd, qk_norm_rope_fwd,  # noqa: E402
-                    rope_frequencies, rope_table)
+from .block import (Ckpt8, ckpt8_pack, ckpt8_unpack, linear_act_bwd, linear_act_fwd,  # noqa: E402
+                    qk_norm_rope_bwd, qk_norm_rope_fwd, rope_frequencies, rope_table)
 from .autograd import attention_jvp  # noqa: E402  (autograd binding: fused forward, backward kernels)
 
 

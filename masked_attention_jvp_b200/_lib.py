@@ -21,7 +21,8 @@ EXPORTED = [
     "caj_attn_fwd_jvp_scatter", "caj_attn_fwd_jvp_host_static", "caj_signal_barrier",
     "caj_ipc_export", "caj_ipc_open", "caj_ipc_close", "caj_attn_fwd_jvp_part", "caj_part_query_tiles",
     "caj_ckpt_pack", "caj_ckpt_unpack", "caj_rope_table", "caj_qk_rope_fwd", "caj_qk_rope_bwd",
-    "caj_qk_rope_bwd_workspace",
+    "caj_qk_rope_bwd_workspace", "caj_linear_act_fwd", "caj_linear_act_fwd_workspace", "caj_linear_act_bwd",
+    "caj_linear_act_bwd_workspace",
 ]
 
 
@@ -71,6 +72,14 @@ class QkRopeShapeC(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("B", "N", "Hq", "Hk", "D", "pairs", "dtype", "norm", "layout",
                                               "gain_full")] + [("eps", ctypes.c_float)] + \
         [(n, ctypes.c_int64) for n in ("ldq", "ldk", "ldv", "ldtq", "ldtk", "ldtv")]
+
+
+ACTS = {"none": 0, "gelu_tanh": 1, "gelu": 2, "silu": 3}  # caj_act
+
+
+class LinearActShapeC(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int64), ("K", ctypes.c_int32), ("C", ctypes.c_int32), ("act", ctypes.c_int32)] + \
+        [(n, ctypes.c_int64) for n in ("ldx", "ldtx", "ldres", "ldtres", "ldy")]
 
 
 class CajError(RuntimeError):
@@ -163,6 +172,15 @@ def lib() -> ctypes.CDLL:
         L.caj_qk_rope_bwd_workspace.restype = ctypes.c_int
         L.caj_qk_rope_bwd.argtypes = [vp] * 11 + [rope] + [vp] * 6 + [ctypes.c_size_t, vp]
         L.caj_qk_rope_bwd.restype = ctypes.c_int
+        lin, size = ctypes.POINTER(LinearActShapeC), ctypes.POINTER(ctypes.c_size_t)
+        L.caj_linear_act_fwd_workspace.argtypes = [lin, i32, size]
+        L.caj_linear_act_fwd_workspace.restype = ctypes.c_int
+        L.caj_linear_act_fwd.argtypes = [vp] * 6 + [lin] + [vp] * 5 + [ctypes.c_size_t, vp]
+        L.caj_linear_act_fwd.restype = ctypes.c_int
+        L.caj_linear_act_bwd_workspace.argtypes = [lin, i32, size]
+        L.caj_linear_act_bwd_workspace.restype = ctypes.c_int
+        L.caj_linear_act_bwd.argtypes = [vp] * 6 + [lin] + [vp] * 4 + [ctypes.c_size_t, vp]
+        L.caj_linear_act_bwd.restype = ctypes.c_int
         L.caj_version.argtypes = []
         L.caj_version.restype = i32
         _lib = L

@@ -4,6 +4,8 @@ library; contracts in include/causaljvp.h):
     cos, sin = rope_table(pos, freq, axis)                   # angles from positions
     q, k, v = qk_norm_rope_fwd(xq, xk, xv, gq, gk, cos, sin, H)
     dxq, dxk, dxv, dgq, dgk = qk_norm_rope_bwd(dq, dk, dv, xq, xk, gq, gk, cos, sin)
+    y, ty, pre = linear_act_fwd(x, w, bias, act="gelu_tanh", tx=tx, save_pre=True)
+    dx, dw, db = linear_act_bwd(dy, x, w, act="gelu_tanh", pre=pre)
     c = ckpt8_pack(x); x = ckpt8_unpack(c)                   # activations kept in 8 bits
 
 Tensors are CUDA tensors; calls run on the current stream of the tensors' device, whichever
@@ -22,7 +24,7 @@ import torch
 from . import _lib
 
 __all__ = ["Ckpt8", "ckpt8_pack", "ckpt8_unpack", "rope_frequencies", "rope_table", "qk_norm_rope_fwd",
-           "qk_norm_rope_bwd"]
+           "qk_norm_rope_bwd", "linear_act_fwd", "linear_act_bwd"]
 
 _DTYPES = {torch.float32: _lib.CAJ_DTYPE_F32, torch.bfloat16: _lib.CAJ_DTYPE_BF16}
 
@@ -309,3 +311,133 @@ def qk_norm_rope_bwd(dq, dk, dv, xq, xk, gq, gk, rope_cos, rope_sin, eps: float 
                                             _ptr(ws), nbytes.value, s)
         _lib.check(st, "caj_qk_rope_bwd")
     return (*dx, *dg)
+
+
+# --------------------------------------------------------------------- linear layers
+
+def _matrix(what: str, name: str, t: torch.Tensor, rows: Optional[int], cols: int) -> int:
+    """t [..., cols] bf16 as rows at one distance, 16-byte aligned: that distance."""
+    if not (t.is_cuda and t.dtype == torch.bfloat16 and t.dim() >= 1 and t.shape[-1] == cols
+            and (rows is None or t.numel() == rows * cols)):
+        raise ValueError(f"{what}: {name} must be a bf16 CUDA tensor with rows of {cols} elements"
+                         + ("" if rows is None else f", {rows} of them"))
+    at = _rows(t)
+    if at is None or at[1] % 8 or t.data_ptr() % 16:
+        raise ValueError(f"{what}: {name}'s rows must lie at one distance, a multiple of 16 bytes, 16-byte aligned")
+    return at[1]
+
+
+def _weight(what: str, w: torch.Tensor, bias: Optional[torch.Tensor]):
+    if not (w.is_cuda and w.dtype == torch.bfloat16 and w.dim() == 2 and w.is_contiguous()):
+        raise ValueError(f"{what}: w must be a contiguous bf16 CUDA tensor [C, K]")
+    if w.shape[0] % 8 or w.shape[1] % 8 or 0 in w.shape:
+        raise ValueError(f"{what}: C and K must be positive multiples of 8")
+    if bias is not None and not (bias.is_cuda and bias.dtype == torch.bfloat16 and bias.is_contiguous()
+                                 and tuple(bias.shape) == (w.shape[0],)):
+        raise ValueError(f"{what}: bias must be a contiguous bf16 CUDA tensor [C]")
+
+
+def linear_act_fwd(x, w, bias=None, act: str = "none", residual=None, tx=None, tresidual=None,
+                   save_pre: bool = False):
+    """(y, ty, pre): y = act(z) + residual with z = x W^T + bias, its tangent
+    ty = act'(z) * (tx W^T) + tresidual, and z as an 8-bit checkpoint for linear_act_bwd.
+
+    x, tx [..., K] and residual, tresidual [..., C] bf16 (rows at one distance: slices are
+    fine); w [C, K], bias [C] bf16; act "none", "gelu_tanh", "gelu" or "silu". y, ty [..., C]
+    bf16. Without tx, ty is None; without save_pre, pre is. Everything after the product is
+    done in fp32 in its epilogue."""
+    what = "linear_act_fwd"
+    _weight(what, w, bias)
+    if act not in _lib.ACTS:
+        raise ValueError(f"{what}: act is one of {sorted(_lib.ACTS)}")
+    if tresidual is not None and tx is None:
+        raise ValueError(f"{what}: tresidual needs tx")
+    C, K = w.shape
+    ldx = _matrix(what, "x", x, None, K)
+    M, lead = x.numel() // K, tuple(x.shape[:-1])
+    for name, t in (("tx", tx), ("residual", residual), ("tresidual", tresidual)):
+        if t is not None and tuple(t.shape[:-1]) != lead:
+            raise ValueError(f"{what}: {name} must have x's leading shape")
+    shape = _lib.LinearActShapeC(M, K, C, _lib.ACTS[act], ldx)
+    if tx is not None:
+        shape.ldtx = _matrix(what, "tx", tx, M, K)
+    if residual is not None:
+        shape.ldres = _matrix(what, "residual", residual, M, C)
+    if tresidual is not None:
+        shape.ldtres = _matrix(what, "tresidual", tresidual, M, C)
+    _same_device(what, x, w, bias, residual, tx, tresidual)
+    y = torch.empty(lead + (C,), dtype=torch.bfloat16, device=x.device)
+    ty = torch.empty_like(y) if tx is not None else None
+    pre = None
+    if save_pre:
+        cw, sw = _ckpt_widths(C)
+        pre = Ckpt8(torch.empty((M, cw), dtype=torch.int8, device=x.device),
+                    torch.empty((M, sw), dtype=torch.uint8, device=x.device), lead + (C,))
+    if M:
+        nbytes = ctypes.c_size_t(0)
+        _lib.check(_lib.lib().caj_linear_act_fwd_workspace(ctypes.byref(shape), int(tx is not None),
+                                                           ctypes.byref(nbytes)), "caj_linear_act_fwd_workspace")
+        with _on(x) as s:
+            ws = torch.empty(nbytes.value, dtype=torch.uint8, device=x.device) if nbytes.value else None
+            st = _lib.lib().caj_linear_act_fwd(
+                _ptr(x), _ptr(tx), _ptr(w), _ptr(bias), _ptr(residual), _ptr(tresidual), ctypes.byref(shape), _ptr(y),
+                _ptr(ty), _ptr(pre.codes if pre else None), _ptr(pre.scales if pre else None), _ptr(ws),
+                nbytes.value, s)
+        _lib.check(st, "caj_linear_act_fwd")
+    return y, ty, pre
+
+
+def linear_act_bwd(dy, x, w, act: str = "none", pre: Optional[Ckpt8] = None, bias: bool = True,
+                   need: Tuple[bool, bool] = (True, True)):
+    """Gradients (dx, dw, db) of linear_act_fwd's primal (the residual's is dy itself).
+
+    dy [..., C] bf16; x [..., K] bf16 or its Ckpt8 (may be None if dw is not needed); w [C, K];
+    pre: the forward's checkpoint of z, needed with an activation. need: whether dx and dw are
+    wanted; bias: whether db is. dx [..., K] and dw [C, K] bf16, db [C] fp32 (None where not
+    wanted). Deterministic."""
+    what = "linear_act_bwd"
+    _weight(what, w, None)
+    if act not in _lib.ACTS:
+        raise ValueError(f"{what}: act is one of {sorted(_lib.ACTS)}")
+    if not (need[0] or need[1] or bias):
+        raise ValueError(f"{what}: no gradient is wanted")
+    C, K = w.shape
+    ldy = _matrix(what, "dy", dy, None, C)
+    M, lead = dy.numel() // C, tuple(dy.shape[:-1])
+    shape = _lib.LinearActShapeC(M, K, C, _lib.ACTS[act], 0, 0, 0, 0, ldy)
+    ckpt = isinstance(x, Ckpt8)
+    if need[1]:
+        if ckpt:
+            if x.rows != M or x.shape[-1] != K:
+                raise ValueError(f"{what}: x's checkpoint must be of {M} rows of {K}")
+            _check_ckpt(what, x)
+        elif x is None:
+            raise ValueError(f"{what}: dw needs x")
+        else:
+            shape.ldx = _matrix(what, "x", x, M, K)
+    if act == "none":
+        if pre is not None:
+            raise ValueError(f"{what}: without an activation no checkpoint is read")
+    else:
+        if pre is None or pre.rows != M or pre.shape[-1] != C:
+            raise ValueError(f"{what}: an activation needs the checkpoint of z, {M} rows of {C}")
+        _check_ckpt(what, pre)
+    xs = x.codes if ckpt else x
+    _same_device(what, dy, w, *(t for t in (xs if need[1] else None, x.scales if ckpt else None,
+                                            *(pre[:2] if pre else ()))))
+    dx = torch.empty(lead + (K,), dtype=torch.bfloat16, device=dy.device) if need[0] else None
+    make = torch.empty if M else torch.zeros
+    dw = make((C, K), dtype=torch.bfloat16, device=dy.device) if need[1] else None
+    db = make((C,), dtype=torch.float32, device=dy.device) if bias else None
+    if M:
+        nbytes = ctypes.c_size_t(0)
+        _lib.check(_lib.lib().caj_linear_act_bwd_workspace(ctypes.byref(shape), int(ckpt), ctypes.byref(nbytes)),
+                   "caj_linear_act_bwd_workspace")
+        with _on(dy) as s:
+            ws = torch.empty(nbytes.value, dtype=torch.uint8, device=dy.device) if nbytes.value else None
+            st = _lib.lib().caj_linear_act_bwd(
+                _ptr(dy), _ptr(xs if need[1] else None), _ptr(x.scales if ckpt and need[1] else None), _ptr(w),
+                _ptr(pre.codes if pre else None), _ptr(pre.scales if pre else None), ctypes.byref(shape), _ptr(dx),
+                _ptr(dw), _ptr(db), _ptr(ws), nbytes.value, s)
+        _lib.check(st, "caj_linear_act_bwd")
+    return dx, dw, db

@@ -16,10 +16,11 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libcausaljvp.so")
-SOURCES = ["api.cpp", "api_block.cpp", "fwd_jvp_sm100.cu", "fwd_jvp_simt.cu", "prologue.cu", "bwd_sm100.cu",
+SOURCES = ["api.cpp", "api_block.cpp", "api_linear.cpp", "fwd_jvp_sm100.cu", "fwd_jvp_simt.cu", "prologue.cu", "bwd_sm100.cu",
            "host_static.cu", "signal.cu", "out_proj_sm100.cu",
-           "qk_rope.cu", "ckpt8.cu"]
-HEADERS = ["api_internal.h", "kernels.h", "mask_schedule.h", "ptx_sm100.cuh", "vec8.cuh", "ckpt8.cuh"]
+           "qk_rope.cu", "ckpt8.cu", "linear_sm100.cu"]
+HEADERS = ["api_internal.h", "kernels.h", "mask_schedule.h", "ptx_sm100.cuh", "vec8.cuh", "ckpt8.cuh",
+           "linear_act.cuh", "pair_sm100.cuh"]
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2", "--expt-relaxed-constexpr",

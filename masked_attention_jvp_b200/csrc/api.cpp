@@ -938,7 +938,11 @@ caj_status caj_last_device_status(void *stream) {
   if (e != cudaSuccess) return cuda_fail(e);
   if (!code) code = bcode;
   if (!code) code = scode;
+  uint32_t lcode = 0;
+  e = caj::read_and_clear_linear_error(&lcode);
+  if (e != cudaSuccess) return cuda_fail(e);
   if (!code) code = pcode;
+  if (!code) code = lcode;
   if (code != 0) {
     g_last_device_code = code;
     return CAJ_ERR_DEVICE_TIMEOUT;

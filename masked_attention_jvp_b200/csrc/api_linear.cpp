@@ -1,0 +1,275 @@
+// C-ABI front end of the linear operators (products with bias, activation and
+// residual, their tangents and gradients): argument checks, the split of the
+// contraction, tensor maps and workspaces (contracts: include/causaljvp.h).
+#include <algorithm>
+
+#include "api_internal.h"
+#include "ckpt8.cuh"
+#include "kernels.h"
+
+using caj::aligned_to;
+
+namespace {
+
+caj_status done(cudaError_t e) { return e == cudaSuccess ? CAJ_OK : caj::cuda_fail(e); }
+
+constexpr int64_t kTileRows = 256, kTileCols = 256, kBlock = 64;
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+size_t padded(int64_t bytes) { return size_t((bytes + 255) & ~int64_t(255)); }
+
+// In how many parts a contraction of k_blocks runs when there are `tiles` output
+// tiles and `elems` outputs. 74 pairs of SMs work at a time; a block of the
+// contraction takes a pair about 0.4 us and a tile 1.5 us besides, and the parts
+// are written and read again (about 5 TB/s) by one more launch (3 us). The least
+// estimate wins; the numbers only weigh one split against another.
+int32_t pick_splits(int64_t tiles, int64_t k_blocks, int64_t elems) {
+  int32_t best = 1;
+  double best_us = 0;
+  for (int32_t s = 1; s <= 32 && s <= k_blocks; ++s) {
+    const int64_t per = ceil_div(k_blocks, s);
+    if (ceil_div(k_blocks, per) != s) continue;  // a part would be empty
+    const double us = double(ceil_div(tiles * s, 74)) * (0.4 * double(per) + 1.5) +
+                      (s > 1 ? 3.0 + 8.0 * s * double(elems) / 5e6 : 0.0);
+    if (s == 1 || us < best_us) {
+      best = s;
+      best_us = us;
+    }
+  }
+  return best;
+}
+
+struct Plan {
+  int32_t m_tiles, n_tiles, k_blocks, splits, split_blocks;
+  int64_t part_rows, part_bytes;
+};
+// rows x cols outputs (and as many tangents), contraction of `depth`.
+Plan plan(int64_t rows, int64_t cols, int64_t depth, bool tangent) {
+  Plan p{};
+  const int64_t tile_rows = tangent ? kTileRows / 2 : kTileRows, ops = tangent ? 2 : 1;
+  p.m_tiles = int32_t(ceil_div(rows, tile_rows));
+  p.n_tiles = int32_t(ceil_div(cols, kTileCols));
+  p.k_blocks = int32_t(ceil_div(depth, kBlock));
+  p.splits = pick_splits(int64_t(p.m_tiles) * p.n_tiles, p.k_blocks, rows * cols * ops);
+  p.split_blocks = int32_t(ceil_div(p.k_blocks, p.splits));
+  p.part_rows = p.m_tiles * tile_rows;
+  p.part_bytes = p.splits > 1 ? int64_t(p.splits) * ops * p.part_rows * cols * 4 : 0;
+  return p;
+}
+bool few_rows(int64_t M, bool tangent) { return (tangent ? 2 : 1) * M <= caj::kLinearFewRows; }
+
+bool use_plan(caj::LinearParams *p, const Plan &pl, int64_t rows, int64_t cols, int64_t depth, bool tangent,
+              void *workspace) {
+  p->M = int32_t(rows);
+  p->N = int32_t(cols);
+  p->K = int32_t(depth);
+  p->m_tiles = pl.m_tiles;
+  p->n_tiles = pl.n_tiles;
+  p->k_blocks = pl.k_blocks;
+  p->splits = pl.splits;
+  p->split_blocks = pl.split_blocks;
+  p->part_rows = pl.part_rows;
+  p->part = static_cast<float *>(workspace);
+  p->timeout_ns = caj::wait_timeout_ns();
+  p->fault_mode = caj::fault_mode();
+  return pl.splits == 1 || caj::encode_map_2d_f32(&p->tm_part, workspace, int64_t(pl.splits) * (tangent ? 2 : 1) * pl.part_rows,
+                                                  cols, cols, 32);
+}
+
+caj_status check_shape(const caj_linear_act_shape *s) {
+  if (!s || s->M <= 0 || s->K <= 0 || s->C <= 0) return CAJ_ERR_INVALID_ARG;
+  if (s->act < CAJ_ACT_NONE || s->act > CAJ_ACT_SILU) return CAJ_ERR_INVALID_ARG;
+  if (s->K % 8 || s->C % 8) return CAJ_ERR_UNSUPPORTED;  // 16-byte rows
+  // rows, tiles and parts are counted in 32 bits
+  if (s->M > (int64_t(1) << 30) || s->K > (1 << 24) || s->C > (1 << 24)) return CAJ_ERR_UNSUPPORTED;
+  const int64_t limit = (int64_t(1) << 31) - 1;
+  if (ceil_div(s->M, 128) * ceil_div(std::max(s->K, s->C), 256) > limit / 32) return CAJ_ERR_UNSUPPORTED;
+  if (s->M > limit / ceil_div(std::max(s->K, s->C), 32)) return CAJ_ERR_UNSUPPORTED;  // checkpoint blocks
+  return CAJ_OK;
+}
+bool good_rows(const void *p, int64_t ld, int64_t width) {
+  return p && aligned_to(p, 16) && ld >= width && ld % 8 == 0 && ld < (int64_t(1) << 36);
+}
+
+struct BwdSizes {
+  Plan dx, dw;
+  int32_t chunk_rows;
+  size_t x, dz, sums, parts, total;
+};
+BwdSizes bwd_sizes(const caj_linear_act_shape *s, bool x_ckpt, bool want_dx, bool want_dw, bool want_db) {
+  BwdSizes b{};
+  b.dx = plan(s->M, s->K, s->C, false);
+  b.dw = plan(s->C, s->K, s->M, false);
+  b.chunk_rows = caj::linear_dz_chunk_rows(s->M, s->C);
+  if (x_ckpt && want_dw) b.x = padded(s->M * s->K * 2);
+  if (s->act != CAJ_ACT_NONE) b.dz = padded(s->M * s->C * 2);
+  if (want_db) b.sums = padded(ceil_div(s->M, b.chunk_rows) * s->C * 4);
+  b.parts = padded(std::max(want_dx ? b.dx.part_bytes : 0, want_dw ? b.dw.part_bytes : 0));
+  b.total = b.x + b.dz + b.sums + b.parts;
+  return b;
+}
+
+}  // namespace
+
+extern "C" {
+
+caj_status caj_linear_act_fwd_workspace(const caj_linear_act_shape *shape, int32_t tangent, size_t *bytes) {
+  if (!bytes || (tangent != 0 && tangent != 1)) return CAJ_ERR_INVALID_ARG;
+  const caj_status st = check_shape(shape);
+  if (st != CAJ_OK) return st;
+  *bytes = few_rows(shape->M, tangent) ? 0 : size_t(plan(shape->M, shape->C, shape->K, tangent).part_bytes);
+  return CAJ_OK;
+}
+
+caj_status caj_linear_act_fwd(const void *x, const void *tx, const void *w, const void *bias, const void *res,
+                              const void *tres, const caj_linear_act_shape *shape, void *y, void *ty,
+                              int8_t *pre_codes, uint8_t *pre_scales, void *workspace, size_t workspace_bytes,
+                              void *stream) {
+  caj_status st = check_shape(shape);
+  if (st != CAJ_OK) return st;
+  const int64_t M = shape->M, K = shape->K, C = shape->C;
+  const bool tan = tx != nullptr;
+  if (!good_rows(x, shape->ldx, K) || !w || !aligned_to(w, 16) || !y || !aligned_to(y, 16)) return CAJ_ERR_INVALID_ARG;
+  if (tan != (ty != nullptr) || (tan && (!good_rows(tx, shape->ldtx, K) || !aligned_to(ty, 16))))
+    return CAJ_ERR_INVALID_ARG;
+  if (bias && !aligned_to(bias, 16)) return CAJ_ERR_INVALID_ARG;
+  if (res && !good_rows(res, shape->ldres, C)) return CAJ_ERR_INVALID_ARG;
+  if (tres && (!tan || !good_rows(tres, shape->ldtres, C))) return CAJ_ERR_INVALID_ARG;
+  if (!pre_codes != !pre_scales) return CAJ_ERR_INVALID_ARG;
+  if (pre_codes && (!aligned_to(pre_codes, 16) || !aligned_to(pre_scales, 4))) return CAJ_ERR_INVALID_ARG;
+  const bool few = few_rows(M, tan);
+  const Plan pl = plan(M, C, K, tan);
+  if (!few && pl.part_bytes && (!workspace || !aligned_to(workspace, 16) || workspace_bytes < size_t(pl.part_bytes)))
+    return CAJ_ERR_INVALID_ARG;
+  st = caj::check_device();
+  if (st != CAJ_OK) return st;
+  caj::LinearParams p{};
+  p.x = x;
+  p.tx = tx;
+  p.w = w;
+  p.bias = bias;
+  p.res = res;
+  p.tres = tres;
+  p.y = y;
+  p.ty = ty;
+  p.codes = pre_codes;
+  p.scales = pre_scales;
+  p.ld_x = shape->ldx;
+  p.ld_tx = shape->ldtx;
+  p.ld_res = shape->ldres;
+  p.ld_tres = shape->ldtres;
+  p.nb = caj::ck::blocks_of(shape->C);
+  p.ns = caj::ck::scale_bytes(shape->C);
+  p.act = shape->act;
+  bool ok = true;
+  if (few) {
+    p.M = int32_t(M);
+    p.N = shape->C;
+    p.K = shape->K;
+  } else {
+    ok = use_plan(&p, pl, M, C, K, tan, workspace) &&
+         caj::encode_map_2d_ld(&p.tm_a, x, M, K, shape->ldx, tan ? 64 : 128) &&
+         caj::encode_map_2d_ld(&p.tm_b, w, C, K, K, 128) && caj::encode_map_2d_ld(&p.tm_y, y, M, C, C, 32);
+    if (ok && tan)
+      ok = caj::encode_map_2d_ld(&p.tm_a2, tx, M, K, shape->ldtx, 64) &&
+           caj::encode_map_2d_ld(&p.tm_y2, ty, M, C, C, 32);
+  }
+  if (!ok) return caj::cuda_fail(cudaErrorInvalidValue);
+  return done(caj::launch_linear_fwd(p, static_cast<cudaStream_t>(stream)));
+}
+
+caj_status caj_linear_act_bwd_workspace(const caj_linear_act_shape *shape, int32_t x_ckpt, size_t *bytes) {
+  if (!bytes || (x_ckpt != 0 && x_ckpt != 1)) return CAJ_ERR_INVALID_ARG;
+  const caj_status st = check_shape(shape);
+  if (st != CAJ_OK) return st;
+  *bytes = bwd_sizes(shape, x_ckpt != 0, true, true, true).total;
+  return CAJ_OK;
+}
+
+caj_status caj_linear_act_bwd(const void *dy, const void *x, const uint8_t *x_scales, const void *w,
+                              const int8_t *pre_codes, const uint8_t *pre_scales, const caj_linear_act_shape *shape,
+                              void *dx, void *dw, float *db, void *workspace, size_t workspace_bytes, void *stream) {
+  caj_status st = check_shape(shape);
+  if (st != CAJ_OK) return st;
+  const int64_t M = shape->M, K = shape->K, C = shape->C;
+  const bool act = shape->act != CAJ_ACT_NONE;
+  if (!dx && !dw && !db) return CAJ_ERR_INVALID_ARG;
+  if (!good_rows(dy, shape->ldy, C)) return CAJ_ERR_INVALID_ARG;
+  if (dx && (!w || !aligned_to(w, 16) || !aligned_to(dx, 16))) return CAJ_ERR_INVALID_ARG;
+  if (dw) {
+    if (!aligned_to(dw, 16)) return CAJ_ERR_INVALID_ARG;
+    if (x_scales ? (!x || !aligned_to(x, 16) || !aligned_to(x_scales, 4)) : !good_rows(x, shape->ldx, K))
+      return CAJ_ERR_INVALID_ARG;
+  }
+  if (db && !aligned_to(db, 4)) return CAJ_ERR_INVALID_ARG;
+  if (act && (!pre_codes || !aligned_to(pre_codes, 16) || !pre_scales || !aligned_to(pre_scales, 4)))
+    return CAJ_ERR_INVALID_ARG;
+  const BwdSizes b = bwd_sizes(shape, x_scales != nullptr, dx != nullptr, dw != nullptr, db != nullptr);
+  if (b.total && (!workspace || !aligned_to(workspace, 256) || workspace_bytes < b.total)) return CAJ_ERR_INVALID_ARG;
+  st = caj::check_device();
+  if (st != CAJ_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  char *at = static_cast<char *>(workspace);
+  void *x_values = at;
+  void *dz = at + b.x;
+  float *sums = reinterpret_cast<float *>(at + b.x + b.dz);
+  void *parts = at + b.x + b.dz + b.sums;
+
+  int64_t ld_dz = C;
+  if (!act) {
+    dz = const_cast<void *>(dy);
+    ld_dz = shape->ldy;
+  }
+  if (act || db) {
+    caj::LinearDzParams d{};
+    d.dy = dy;
+    d.codes = pre_codes;
+    d.scales = pre_scales;
+    d.dz = dz;
+    d.partial = db ? sums : nullptr;
+    d.M = M;
+    d.ld_dy = shape->ldy;
+    d.C = shape->C;
+    d.nb = caj::ck::blocks_of(shape->C);
+    d.ns = caj::ck::scale_bytes(shape->C);
+    d.act = shape->act;
+    d.chunk_rows = b.chunk_rows;
+    st = done(caj::launch_linear_dz(d, db, s));
+    if (st != CAJ_OK) return st;
+  }
+  if (dx) {
+    caj::LinearParams p{};
+    p.y = dx;
+    if (!use_plan(&p, b.dx, M, K, C, false, parts) || !caj::encode_map_2d_ld(&p.tm_a, dz, M, C, ld_dz, 128) ||
+        !caj::encode_map_2d_ld(&p.tm_b, w, C, K, K, 64) || !caj::encode_map_2d_ld(&p.tm_y, dx, M, K, K, 32))
+      return caj::cuda_fail(cudaErrorInvalidValue);
+    st = done(caj::launch_linear_dx(p, s));
+    if (st != CAJ_OK) return st;
+  }
+  if (dw) {
+    int64_t ld_x = shape->ldx;
+    if (x_scales) {
+      caj::Ckpt8Params c{};
+      c.codes = static_cast<int8_t *>(const_cast<void *>(x));
+      c.scales = const_cast<uint8_t *>(x_scales);
+      c.out = x_values;
+      c.ld = ld_x = K;
+      c.cols = shape->K;
+      c.nb = caj::ck::blocks_of(shape->K);
+      c.ns = caj::ck::scale_bytes(shape->K);
+      c.total = uint32_t(M * c.nb);
+      st = done(caj::launch_ckpt8(c, true, true, s));
+      if (st != CAJ_OK) return st;
+      x = x_values;
+    }
+    caj::LinearParams p{};
+    p.y = dw;
+    if (!use_plan(&p, b.dw, C, K, M, false, parts) || !caj::encode_map_2d_ld(&p.tm_a, dz, M, C, ld_dz, 64) ||
+        !caj::encode_map_2d_ld(&p.tm_b, x, M, K, ld_x, 64) || !caj::encode_map_2d_ld(&p.tm_y, dw, C, K, K, 32))
+      return caj::cuda_fail(cudaErrorInvalidValue);
+    st = done(caj::launch_linear_dw(p, s));
+  }
+  return st;
+}
+
+}  // extern "C"

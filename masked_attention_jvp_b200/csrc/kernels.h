@@ -186,6 +186,38 @@ struct QkRopeParams {
   int32_t norm, half, gain_full, blocks;
 };
 
+// Matrix products of the linear operators; the operands' maps have 128-byte-swizzled
+// boxes of 64 bf16 columns (K-major operands: 128 rows, 64 with tangents; MN-major: 64).
+constexpr int32_t kLinearFewRows = 8;  // rows (tangents counted) up to which W is streamed
+struct LinearParams {
+  CUtensorMap tm_a, tm_a2, tm_b;  // x (or dz), tx, W (or x)
+  CUtensorMap tm_y, tm_y2;        // outputs, boxes of 64 x 32
+  CUtensorMap tm_part;            // splits > 1: fp32 parts, boxes of 32 x 32
+  const void *x, *tx, *w;         // few rows: x, tx, W themselves; tx also says whether there are tangents
+  const void *bias, *res, *tres;  // bf16 or null
+  void *y, *ty;                   // [M, N] bf16
+  float *part;                    // [splits][1 or 2][part_rows][N]
+  int8_t *codes;                  // z's 8-bit checkpoint, or null
+  uint8_t *scales;
+  int64_t ld_x, ld_tx, ld_res, ld_tres;
+  int64_t part_rows;
+  int32_t M, N, K;                // output rows and columns, contraction
+  int32_t m_tiles, n_tiles, k_blocks, splits, split_blocks;
+  int32_t nb, ns;
+  int32_t act;
+  int32_t fault_mode;             // test hook: 1 = the producer issues no copies
+  uint64_t timeout_ns;
+};
+struct LinearDzParams {
+  const void *dy;         // [M, C] bf16, rows ld_dy apart
+  const int8_t *codes;    // z's checkpoint (act != none)
+  const uint8_t *scales;
+  void *dz;               // [M, C] bf16 (act != none)
+  float *partial;         // [chunks][C], or null
+  int64_t M, ld_dy;
+  int32_t C, nb, ns, act, chunk_rows;
+};
+
 // 8-bit checkpoints of `rows` rows: nb blocks and ns scale bytes a row, total = rows * nb.
 struct Ckpt8Params {
   const void *x;       // pack: rows of `cols` values, ld elements apart
@@ -232,6 +264,12 @@ cudaError_t launch_rope_table(const RopeTableParams &p, bool pos64, cudaStream_t
 cudaError_t launch_qk_rope_fwd(const QkRopeParams &p, bool bf16, cudaStream_t stream);
 cudaError_t launch_qk_rope_bwd(const QkRopeParams &p, bool bf16, cudaStream_t stream);
 int32_t qk_rope_bwd_blocks(int32_t B, int32_t N, int32_t Hq, int32_t Hk, int32_t D);
+cudaError_t launch_linear_fwd(const LinearParams &p, cudaStream_t stream);
+cudaError_t launch_linear_dx(const LinearParams &p, cudaStream_t stream);
+cudaError_t launch_linear_dw(const LinearParams &p, cudaStream_t stream);
+cudaError_t launch_linear_dz(const LinearDzParams &p, float *db, cudaStream_t stream);
+int32_t linear_dz_chunk_rows(int64_t M, int32_t C);
+cudaError_t read_and_clear_linear_error(uint32_t *out);
 cudaError_t launch_ckpt8(const Ckpt8Params &p, bool unpack, bool bf16, cudaStream_t stream);
 cudaError_t launch_signal_barrier(const SignalParams &p, cudaStream_t stream);
 cudaError_t launch_out_proj_sm100(const OutProjParams &p, cudaStream_t stream);

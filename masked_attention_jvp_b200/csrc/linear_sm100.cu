@@ -1,0 +1,815 @@
+// Matrix products of the linear operators on B200 tensor cores (sm_100a):
+//   forward    z = x W^T + b,  y = act(z) + res,  ty = act'(z) * (tx W^T) + tres,
+//              optionally z kept as an 8-bit checkpoint
+//   gradients  dx = dz W,  dW = dz^T x
+// All are one persistent kernel over 256 x 256 output tiles, instantiated by where
+// the contraction runs in each operand:
+//   forward  x [M, K], W [C, K]: both along the rows (K-major)
+//   dx       dz [M, C] along the rows, W [C, K] across them (MN-major B)
+//   dW       dz [M, C] and x [M, K], contraction over the tokens: both MN-major
+//
+// Design (clusters of two CTAs, one CTA per SM, 10 warps per CTA):
+//   A pair computes 256 x 256 tiles with tcgen05 cta_group::2 (M = 256, N = 256):
+//   each CTA loads its 128 rows of A and its 128 of the tile's 256 rows of B, 32 KiB
+//   per 64-wide block of the contraction, and the leader issues four products that
+//   read both CTAs' halves. fp32 accumulators are double-buffered in tensor memory.
+//   Against a 128 x 256 tile of one CTA this cuts the copies by a third, and the
+//   copies are the limit: 64 bytes a clock per SM at the products' full rate.
+//   Tangents: a tile holds 128 tokens. Each CTA's A rows are 64 tokens of x, then
+//   the same 64 of tx, so primal and tangent share every weight tile, the product
+//   shape and the copies stay those of the primal alone, and both halves of a
+//   token's result land in one CTA. The tangent's factor act'(z) crosses from the
+//   warps that hold the primal rows to those that hold the tangent rows through
+//   4 KiB of shared memory per pair of warps, 32 columns at a time. (Two products
+//   of N = 128 per weight tile would keep both in one thread, but copy 25% more.)
+//   warp 0      TMA producer (both CTAs)
+//   warp 1      MMA issuer (the leader's)
+//   warps 2-9   epilogue: two warps per 32 rows, 128 columns each, so that an
+//               activation costs less than the products of the next tile.
+// Column blocks run fastest, so the pairs work on one band of A at a time and it is
+// read from DRAM once; weights stay in L2.
+//
+// Few tiles and a long contraction (dW of a narrow layer, a frame of tokens): the
+// contraction is split, each part stores fp32 partial tiles, and a second kernel
+// adds them in a fixed order and does the epilogue. The split goes by sizes alone,
+// so results do not depend on the device's state.
+// Up to 8 rows (tokens being decoded, and their tangents) a tile would be almost
+// empty and the weights' bytes are all there is: rows_kernel streams W once through
+// CUDA cores, 16 bytes a lane.
+//
+// Every wait is bounded: on expiry the kernel records an error code, drains its
+// copies, products and stores, frees tensor memory and returns.
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <atomic>
+
+#include "ckpt8.cuh"
+#include "kernels.h"
+#include "linear_act.cuh"
+#include "pair_sm100.cuh"
+#include "ptx_sm100.cuh"
+#include "vec8.cuh"
+
+namespace caj {
+namespace {
+
+using namespace ptx;
+
+__device__ uint32_t g_linear_error = 0;
+
+constexpr int TN = 256, TK = 64;
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 32 * (2 + kEpiWarps);
+constexpr uint32_t A_BYTES = 128 * TK * 2, B_BYTES = 128 * TK * 2, STAGE_BYTES = A_BYTES + B_BYTES;
+constexpr uint32_t OUT_BYTES = 32 * 128;  // a warp's staging tile: 32 rows of 128 bytes
+constexpr uint32_t EX_BYTES = 32 * 128;   // a pair of warps' act'(z): 32 rows x 32 columns
+constexpr uint32_t kTmemCols = 512;
+
+enum : uint32_t { kSiteEmpty = 0x21, kSiteFull, kSiteAccEmpty, kSiteAccFull, kSiteExEmpty, kSiteExFull };
+
+template <bool JVP>
+struct Lay {
+  static constexpr int STAGES = JVP ? 5 : 6;
+  static constexpr uint32_t OFF_OUT = STAGES * STAGE_BYTES;
+  static constexpr uint32_t OFF_EX = OFF_OUT + kEpiWarps * OUT_BYTES;
+  static constexpr uint32_t OFF_BAR = OFF_EX + (JVP ? 4 * EX_BYTES : 0);
+  // offsets from OFF_BAR
+  static constexpr uint32_t FULL = 0, EMPTY = 8 * STAGES, ACC_FULL = 16 * STAGES, ACC_EMPTY = ACC_FULL + 16,
+                            DRAIN = ACC_EMPTY + 16, EX_FULL = DRAIN + 8, EX_EMPTY = EX_FULL + 32,
+                            TMEM_SLOT = EX_EMPTY + 32, ABORT = TMEM_SLOT + 4, END = ABORT + 4;
+  static constexpr uint32_t SMEM = OFF_BAR + END + 1024;  // + slack for the 1 KiB alignment
+  static_assert(SMEM <= 232448, "shared memory per CTA");
+};
+
+// The 16-byte unit `u` of row `row` in a 128-byte-swizzled tile at `base`.
+__device__ __forceinline__ uint32_t swz(uint32_t base, uint32_t row, uint32_t u) {
+  return base + row * 128u + ((u ^ (row & 7u)) << 4);
+}
+__device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a)
+               : "memory");
+  return v;
+}
+
+// The warp's staging tile is complete: makes it visible to the copy engine and stores it.
+__device__ __forceinline__ void fence_async_smem_then_store(const CUtensorMap *m, uint32_t src, int32_t x, int32_t y,
+                                                            int lane) {
+  pair::fence_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    pair::store_2d(m, src, x, y);
+    pair::store_commit();
+  }
+  __syncwarp();
+}
+
+// JVP: tangent rows beside the primal's. AMN, BMN: the operand is MN-major. EPI:
+// bias, activation, residual and checkpoint (otherwise the plain product).
+template <bool JVP, bool AMN, bool BMN, bool EPI>
+__global__ void __launch_bounds__(kThreads, 1) linear_sm100_kernel(const __grid_constant__ LinearParams p) {
+  using L = Lay<JVP>;
+  constexpr int TM = JVP ? 128 : 256;  // tokens (or output rows) of a tile
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t sbase = (raw + 1023u) & ~1023u;
+  uint8_t *sgen = smem_raw + (sbase - raw);
+  const uint32_t bars = sbase + L::OFF_BAR;
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(sgen + L::OFF_BAR + L::ABORT);
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sgen + L::OFF_BAR + L::TMEM_SLOT);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = pair::cluster_rank();
+  const int32_t first = int32_t(pair::cluster_id()), step = int32_t(pair::clusters());
+  const int32_t n_tiles = p.m_tiles * p.n_tiles, n_units = n_tiles * p.splits;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < L::STAGES; ++s) {
+      mbar_init(bars + L::FULL + 8 * s, 1);
+      mbar_init(bars + L::EMPTY + 8 * s, 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(bars + L::ACC_FULL + 8 * b, 1);
+      mbar_init(bars + L::ACC_EMPTY + 8 * b, 2 * kEpiWarps);  // both CTAs' epilogue warps
+    }
+    mbar_init(bars + L::DRAIN, 1);
+    for (int b = 0; b < 4; ++b) {
+      mbar_init(bars + L::EX_FULL + 8 * b, 1);
+      mbar_init(bars + L::EX_EMPTY + 8 * b, 1);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0) {
+    prefetch_tmap(&p.tm_a);
+    if (JVP) prefetch_tmap(&p.tm_a2);
+    prefetch_tmap(&p.tm_b);
+    prefetch_tmap(&p.tm_y);
+    if (JVP) prefetch_tmap(&p.tm_y2);
+  }
+  if (warp == 1) pair::tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+  tc_fence_before();
+  pair::sync_cluster();  // barriers of both CTAs initialised, tensor memory allocated
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  auto wait = [&](uint32_t bar, uint32_t parity, uint32_t site) {
+    return pair::wait_warp(bar, parity, &g_linear_error, abort_flag, p.timeout_ns, 0x100u | site);
+  };
+
+  if (warp == 0) {
+    // ---------------------------------------------------- TMA producer (both CTAs)
+    const uint32_t leader = elect_one();
+    uint32_t stage = 0, phase = 0, issued = 0;
+    bool ok = true;
+    for (int32_t u = first; ok && u < n_units; u += step) {
+      const int32_t t = u % n_tiles, split = u / n_tiles;
+      const int32_t m0 = (t / p.n_tiles) * TM + int32_t(rank) * (TM / 2);
+      const int32_t n0 = (t % p.n_tiles) * TN + int32_t(rank) * (TN / 2);
+      const int32_t kb1 = min(p.k_blocks, (split + 1) * p.split_blocks);
+      for (int32_t kb = split * p.split_blocks; kb < kb1; ++kb) {
+        if (!wait(bars + L::EMPTY + 8 * stage, phase ^ 1u, kSiteEmpty)) {
+          ok = false;
+          break;
+        }
+        if (p.fault_mode == 0) {
+          const uint32_t sa = sbase + stage * STAGE_BYTES, sb = sa + A_BYTES;
+          const uint32_t fb = pair::at_rank(bars + L::FULL + 8 * stage, 0);  // the leader's barrier
+          if (rank == 0) mbar_arrive_expect_tx_if(leader, bars + L::FULL + 8 * stage, 2 * STAGE_BYTES);
+          if (AMN) {
+            pair::load_2d(leader, sa, &p.tm_a, fb, m0, kb * TK);
+            pair::load_2d(leader, sa + A_BYTES / 2, &p.tm_a, fb, m0 + 64, kb * TK);
+          } else if (JVP) {
+            pair::load_2d(leader, sa, &p.tm_a, fb, kb * TK, m0);
+            pair::load_2d(leader, sa + A_BYTES / 2, &p.tm_a2, fb, kb * TK, m0);
+          } else {
+            pair::load_2d(leader, sa, &p.tm_a, fb, kb * TK, m0);
+          }
+          if (BMN) {
+            pair::load_2d(leader, sb, &p.tm_b, fb, n0, kb * TK);
+            pair::load_2d(leader, sb + B_BYTES / 2, &p.tm_b, fb, n0 + 64, kb * TK);
+          } else {
+            pair::load_2d(leader, sb, &p.tm_b, fb, kb * TK, n0);
+          }
+          ++issued;
+        }
+        __syncwarp();
+        if (++stage == uint32_t(L::STAGES)) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    if (!ok && leader && rank == 0) {  // the leader's barriers count both CTAs' copies
+      const uint32_t inflight = issued < uint32_t(L::STAGES) ? issued : uint32_t(L::STAGES);
+      uint32_t s = stage, ph = phase;
+      for (uint32_t i = 0; i < inflight; ++i) {
+        if (s == 0) {
+          s = L::STAGES;
+          ph ^= 1u;
+        }
+        --s;
+        pair::drain(bars + L::FULL + 8 * s, ph, p.timeout_ns);
+      }
+    }
+  } else if (warp == 1) {
+    if (rank == 0) {
+      // ---------------------------------------------------- MMA issuer (leader only)
+      const uint32_t leader = elect_one();
+      constexpr uint32_t IDESC = idesc_bf16_f32(256, TN, BMN ? 1 : 0) | (AMN ? 1u << 15 : 0u);
+      // per 16-wide step of the contraction: 32 bytes along a K-major row, 16 rows of
+      // 128 bytes of an MN-major block
+      constexpr uint64_t A_STEP = AMN ? 128 : 2, B_STEP = BMN ? 128 : 2;
+      constexpr uint32_t A_LBO = AMN ? A_BYTES / 2 : 16, B_LBO = BMN ? B_BYTES / 2 : 16;
+      uint32_t stage = 0, phase = 0, count = 0;
+      bool ok = true;
+      for (int32_t u = first; ok && u < n_units; u += step, ++count) {
+        const uint32_t buf = count & 1u, use = count >> 1;
+        if (!wait(bars + L::ACC_EMPTY + 8 * buf, (use & 1u) ^ 1u, kSiteAccEmpty)) break;
+        tc_fence_after();
+        const uint32_t d_tmem = tmem + buf * TN;
+        const int32_t split = u / n_tiles, kb0 = split * p.split_blocks;
+        const int32_t kb1 = min(p.k_blocks, kb0 + p.split_blocks);
+        for (int32_t kb = kb0; kb < kb1; ++kb) {
+          if (!wait(bars + L::FULL + 8 * stage, phase, kSiteFull)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sa = sbase + stage * STAGE_BYTES, sb = sa + A_BYTES;
+          const uint64_t da = sdesc_sw128(sa, A_LBO, 1024), db = sdesc_sw128(sb, B_LBO, 1024);
+#pragma unroll
+          for (int kk = 0; kk < TK / 16; ++kk)
+            pair::mma(leader, d_tmem, da + kk * A_STEP, db + kk * B_STEP, IDESC, kb != kb0 || kk != 0);
+          pair::commit(leader, bars + L::EMPTY + 8 * stage);  // both CTAs' stage is free
+          __syncwarp();
+          if (++stage == uint32_t(L::STAGES)) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        pair::commit(leader, bars + L::ACC_FULL + 8 * buf);  // both CTAs' accumulator half is complete
+        __syncwarp();
+      }
+      pair::commit(leader, bars + L::DRAIN);
+      __syncwarp();
+      if (leader) pair::drain(bars + L::DRAIN, 0, p.timeout_ns);
+      __syncwarp();
+    }
+  } else {
+    // ---------------------------------------------------------- epilogue (both CTAs)
+    const int q = warp & 3, half = (warp - 2) >> 2;
+    const int op = JVP ? q >> 1 : 0;  // 1: this warp's rows are tangents
+    const uint32_t lane_taddr = tmem + (uint32_t(32 * q) << 16) + uint32_t(128 * half);
+    const uint32_t sbuf = sbase + L::OFF_OUT + uint32_t(warp - 2) * OUT_BYTES;
+    const uint32_t ex_id = uint32_t((q & 1) + 2 * half);
+    const uint32_t ex = sbase + L::OFF_EX + ex_id * EX_BYTES;
+    const uint32_t acc_empty_leader = pair::at_rank(bars + L::ACC_EMPTY, 0);
+    const CUtensorMap *om = op ? &p.tm_y2 : &p.tm_y;
+    const uint16_t *res = static_cast<const uint16_t *>(op ? p.tres : p.res);
+    const int64_t ld_res = op ? p.ld_tres : p.ld_res;
+    uint32_t count = 0, exchanged = 0;
+    bool ok = true;
+    for (int32_t u = first; ok && u < n_units; u += step, ++count) {
+      const int32_t t = u % n_tiles, split = u / n_tiles;
+      const int32_t row0 = (t / p.n_tiles) * TM + int32_t(rank) * (TM / 2) + 32 * (JVP ? q & 1 : q);
+      const int32_t n0 = (t % p.n_tiles) * TN + 128 * half;
+      const uint32_t buf = count & 1u, use = count >> 1;
+      if (!wait(bars + L::ACC_FULL + 8 * buf, use & 1u, kSiteAccFull)) break;
+      tc_fence_after();
+      const bool rows_in = row0 < p.M;
+      uint32_t scale_word = 0;
+#pragma unroll 1
+      for (int c = 0; ok && c < 2; ++c) {
+        uint32_t acc[2][32];
+        tmem_ld32x2(lane_taddr + buf * TN + 64 * c, lane_taddr + buf * TN + 64 * c + 32, acc[0], acc[1]);
+        if (c == 1) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) pair::arrive_remote(acc_empty_leader + 8 * buf);
+        }
+        const int32_t col0 = n0 + 64 * c;
+        if (!rows_in || col0 >= p.N) continue;
+        if (p.splits > 1) {  // fp32 partial tiles, 32 columns at a time
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            if (col0 + 32 * s >= p.N) continue;
+            if (lane == 0) pair::store_wait_read<0>();
+            __syncwarp();
+#pragma unroll
+            for (int g = 0; g < 8; ++g)
+              sts128(swz(sbuf, lane, g), acc[s][4 * g], acc[s][4 * g + 1], acc[s][4 * g + 2], acc[s][4 * g + 3]);
+            fence_async_smem_then_store(&p.tm_part, sbuf, col0 + 32 * s,
+                                        (split * (JVP ? 2 : 1) + op) * p.part_rows + row0, lane);
+          }
+          continue;
+        }
+        uint4 rv[8];
+        if (EPI && res) {  // coalesced: eight lanes a row, four rows at a time
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int32_t r = row0 + 4 * i + (lane >> 3), cc = col0 + 8 * (lane & 7);
+            rv[i] = make_uint4(0, 0, 0, 0);
+            if (r < p.M && cc < p.N) rv[i] = __ldcs(reinterpret_cast<const uint4 *>(res + r * ld_res + cc));
+          }
+        }
+#pragma unroll
+        for (int s = 0; EPI && s < 2; ++s) {
+          float v[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(acc[s][i]);
+          const int32_t cs = col0 + 32 * s;
+          if (op == 0) {
+            if (p.bias) {
+              const uint4 *bp = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.bias) + cs);
+#pragma unroll
+              for (int g = 0; g < 4; ++g) {
+                if (cs + 8 * g >= p.N) continue;
+                const uint4 w = __ldg(bp + g);
+                const uint32_t w4[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  v[8 * g + 2 * e] += lin::bf_lo(w4[e]);
+                  v[8 * g + 2 * e + 1] += lin::bf_hi(w4[e]);
+                }
+              }
+            }
+            if (p.codes && cs < 32 * p.nb) {
+              uint32_t m = 0;
+#pragma unroll
+              for (int i = 0; i < 32; ++i) m = max(m, ck::mag_bits(v[i]));
+              const uint32_t sc = ck::scale_of(m);
+              scale_word |= sc << (8 * (2 * c + s));
+              uint32_t w[8];
+              if (sc == 255u) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) w[i] = 0;
+              } else {
+                float f[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) f[i] = v[i];
+                ck::saturate(f, sc);
+                const float up = ck::up_of(sc);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                  w[i] = ck::pack_codes4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3], up);
+              }
+              if (row0 + lane < p.M) {
+                uint4 *dst = reinterpret_cast<uint4 *>(p.codes + size_t(row0 + lane) * (32 * size_t(p.nb)) + cs);
+                dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+              }
+            }
+          }
+          if (p.act != lin::kActNone) {
+            if constexpr (JVP) {
+              if (op == 0) {
+                float sl[32];
+                lin::act_all<true>(p.act, v, sl);
+                if (!wait(bars + L::EX_EMPTY + 8 * ex_id, (exchanged & 1u) ^ 1u, kSiteExEmpty)) {
+                  ok = false;
+                  break;
+                }
+#pragma unroll
+                for (int g = 0; g < 8; ++g)
+                  sts128(swz(ex, lane, g), __float_as_uint(sl[4 * g]), __float_as_uint(sl[4 * g + 1]),
+                         __float_as_uint(sl[4 * g + 2]), __float_as_uint(sl[4 * g + 3]));
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bars + L::EX_FULL + 8 * ex_id);
+              } else {
+                if (!wait(bars + L::EX_FULL + 8 * ex_id, exchanged & 1u, kSiteExFull)) {
+                  ok = false;
+                  break;
+                }
+#pragma unroll
+                for (int g = 0; g < 8; ++g) {
+                  const uint4 w = lds128(swz(ex, lane, g));
+                  v[4 * g] *= __uint_as_float(w.x);
+                  v[4 * g + 1] *= __uint_as_float(w.y);
+                  v[4 * g + 2] *= __uint_as_float(w.z);
+                  v[4 * g + 3] *= __uint_as_float(w.w);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bars + L::EX_EMPTY + 8 * ex_id);
+              }
+              ++exchanged;
+            } else {
+              float sl[32];
+              lin::act_all<false>(p.act, v, sl);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 32; ++i) acc[s][i] = __float_as_uint(v[i]);
+        }
+        if (!ok) break;
+        if (lane == 0) pair::store_wait_read<0>();
+        __syncwarp();
+        if (EPI && res) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            sts128(swz(sbuf, 4 * i + (lane >> 3), lane & 7), rv[i].x, rv[i].y, rv[i].z, rv[i].w);
+          __syncwarp();
+        }
+#pragma unroll
+        for (int g = 0; g < 8; ++g) {
+          float f[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(acc[g >> 2][8 * (g & 3) + e]);
+          const uint32_t a = swz(sbuf, lane, g);
+          if (EPI && res) {
+            const uint4 w = lds128(a);
+            const uint32_t w4[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              f[2 * e] += lin::bf_lo(w4[e]);
+              f[2 * e + 1] += lin::bf_hi(w4[e]);
+            }
+          }
+          sts128(a, pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+        }
+        fence_async_smem_then_store(om, sbuf, col0, row0, lane);
+      }
+      if (EPI && p.codes && p.splits == 1 && op == 0 && rows_in && row0 + lane < p.M && n0 < 32 * p.nb)
+        *reinterpret_cast<uint32_t *>(p.scales + size_t(row0 + lane) * p.ns + n0 / 32) = scale_word;
+    }
+    if (lane == 0) pair::store_wait<0>();
+    __syncwarp();
+  }
+
+  // neither CTA leaves while the pair's products may still read its shared memory
+  // or the peer may still signal its barriers
+  tc_fence_before();
+  pair::sync_cluster();
+  if (warp == 1) {
+    tc_fence_after();
+    pair::tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// ------------------------------------------------- the split contraction's second half
+// Adds the parts of p.part ([splits][1 or 2 operands][part_rows][N] fp32) in order and
+// does the epilogue. Four lanes hold a block of 32 columns, eight each.
+template <bool JVP, bool EPI>
+__global__ void __launch_bounds__(256) linear_finish_kernel(const LinearParams p) {
+  const int32_t vecs = ck::blocks_of(p.N) * 4;
+  const int64_t g = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t row = g / vecs;
+  const int32_t col = int32_t(g - row * vecs) * 8;
+  const bool on = row < p.M, in = on && col < p.N;
+  float v[2][8];
+#pragma unroll
+  for (int op = 0; op < (JVP ? 2 : 1); ++op) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[op][i] = 0.f;
+    if (!in) continue;
+#pragma unroll 4
+    for (int32_t s = 0; s < p.splits; ++s) {
+      const float4 *src = reinterpret_cast<const float4 *>(
+          p.part + (size_t(s * (JVP ? 2 : 1) + op) * p.part_rows + row) * p.N + col);
+      const float4 a = __ldcs(src), b = __ldcs(src + 1);
+      v[op][0] += a.x; v[op][1] += a.y; v[op][2] += a.z; v[op][3] += a.w;
+      v[op][4] += b.x; v[op][5] += b.y; v[op][6] += b.z; v[op][7] += b.w;
+    }
+  }
+  if (EPI) {
+    if (p.bias && in) {
+      v8::Raw<__nv_bfloat16> r;
+      r.a = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.bias) + col));
+      float b[8];
+      v8::unpack(r, b);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[0][i] += b[i];
+    }
+    if (p.codes) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m = max(m, ck::mag_bits(v[0][i]));
+      m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+      m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+      if (on) {
+        const uint32_t s = ck::scale_of(m);
+        uint2 w = make_uint2(0, 0);
+        if (s != 255u) {
+          float f[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) f[i] = v[0][i];
+          ck::saturate(f, s);
+          w.x = ck::pack_codes4(f[0], f[1], f[2], f[3], ck::up_of(s));
+          w.y = ck::pack_codes4(f[4], f[5], f[6], f[7], ck::up_of(s));
+        }
+        *reinterpret_cast<uint2 *>(p.codes + size_t(row) * (32 * size_t(p.nb)) + col) = w;
+        if ((col & 31) == 0) {
+          p.scales[size_t(row) * p.ns + col / 32] = uint8_t(s);
+          if (col / 32 == p.nb - 1)
+            for (int32_t i = p.nb; i < p.ns; ++i) p.scales[size_t(row) * p.ns + i] = 0;
+        }
+      }
+    }
+    float sl[8];
+    lin::act_all<JVP>(p.act, v[0], sl);
+    if (JVP) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[1][i] *= sl[i];
+    }
+  }
+  if (!in) return;
+#pragma unroll
+  for (int op = 0; op < (JVP ? 2 : 1); ++op) {
+    if (EPI && (op ? p.tres : p.res)) {
+      float r8[8];
+      v8::unpack(v8::load(static_cast<const __nv_bfloat16 *>(op ? p.tres : p.res) + row * (op ? p.ld_tres : p.ld_res) + col), r8);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[op][i] += r8[i];
+    }
+    v8::Raw<__nv_bfloat16> o;
+    v8::pack(v[op], o);
+    v8::store(static_cast<__nv_bfloat16 *>(op ? p.ty : p.y) + size_t(row) * p.N + col, o);
+  }
+}
+
+// --------------------------------------------------------------------- a few rows
+// R rows (primal rows, then as many tangent rows) against all of W, which is read
+// once, 16 bytes a lane: a warp takes CPW rows of W at a time, its lanes 256
+// neighbouring elements of each, U such pieces in flight. x comes through L1.
+// The sums of a row of W are shuffled together; then one warp per token does the
+// epilogue of the block's 8 * CPW columns.
+template <int R, int CPW>
+__global__ void __launch_bounds__(256) linear_rows_kernel(const LinearParams p) {
+  constexpr int U = 8 / CPW;
+  __shared__ float z[R][8 * CPW];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int32_t base = int32_t(blockIdx.x) * 8 * CPW, c0 = base + warp * CPW;
+  const int32_t rows = p.M;  // primal rows
+  const uint16_t *w = static_cast<const uint16_t *>(p.w);
+  const bool jvp = p.tx != nullptr;
+  float acc[R][CPW];
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int c = 0; c < CPW; ++c) acc[r][c] = 0.f;
+  for (int32_t k0 = 8 * lane; k0 < p.K; k0 += 256 * U) {
+    v8::Raw<__nv_bfloat16> wr[U][CPW];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int c = 0; c < CPW; ++c) {
+        wr[u][c] = v8::zero<__nv_bfloat16>();
+        const int32_t k = k0 + 256 * u;
+        if (k < p.K && c0 + c < p.N)
+          wr[u][c].a = __ldg(reinterpret_cast<const uint4 *>(w + size_t(c0 + c) * p.K + k));
+      }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int32_t k = k0 + 256 * u;
+      if (k >= p.K) break;
+      float wf[CPW][8];
+#pragma unroll
+      for (int c = 0; c < CPW; ++c) v8::unpack(wr[u][c], wf[c]);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const bool tan = jvp && r >= rows;
+        if (r >= (jvp ? 2 * rows : rows)) break;
+        const uint16_t *src = tan ? static_cast<const uint16_t *>(p.tx) + (r - rows) * p.ld_tx
+                                  : static_cast<const uint16_t *>(p.x) + r * p.ld_x;
+        v8::Raw<__nv_bfloat16> xr;
+        xr.a = __ldg(reinterpret_cast<const uint4 *>(src + k));
+        float xf[8];
+        v8::unpack(xr, xf);
+#pragma unroll
+        for (int c = 0; c < CPW; ++c)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) acc[r][c] = fmaf(xf[i], wf[c][i], acc[r][c]);
+      }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int c = 0; c < CPW; ++c) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) acc[r][c] += __shfl_xor_sync(0xFFFFFFFFu, acc[r][c], o);
+      if (lane == 0) z[r][warp * CPW + c] = acc[r][c];
+    }
+  __syncthreads();
+  if (warp >= rows) return;
+  const int32_t col = base + lane;
+  const bool in = lane < 8 * CPW && col < p.N;
+  float v[1] = {in ? z[warp][lane < 8 * CPW ? lane : 0] : 0.f}, sl[1];
+  if (in && p.bias) v[0] += __uint_as_float(uint32_t(static_cast<const uint16_t *>(p.bias)[col]) << 16);
+  if (CPW == 4 && p.codes) {
+    const uint32_t s = ck::scale_of(__reduce_max_sync(0xFFFFFFFFu, ck::mag_bits(v[0])));
+    float f[1] = {v[0]};
+    ck::saturate(f, s);
+    p.codes[size_t(warp) * (32 * size_t(p.nb)) + col] = s == 255u ? 0 : int8_t(ck::code_word(f[0], ck::up_of(s)) & 0xFFu);
+    if (lane == 0) {
+      p.scales[size_t(warp) * p.ns + base / 32] = uint8_t(s);
+      if (base / 32 == p.nb - 1)
+        for (int32_t i = p.nb; i < p.ns; ++i) p.scales[size_t(warp) * p.ns + i] = 0;
+    }
+  }
+  if (!in) return;
+  lin::act_all<true>(p.act, v, sl);
+  const __nv_bfloat16 *res = static_cast<const __nv_bfloat16 *>(p.res), *tres = static_cast<const __nv_bfloat16 *>(p.tres);
+  if (res) v[0] += __bfloat162float(res[warp * p.ld_res + col]);
+  static_cast<__nv_bfloat16 *>(p.y)[size_t(warp) * p.N + col] = __float2bfloat16_rn(v[0]);
+  if (jvp) {
+    float t = sl[0] * z[R > 1 ? warp + rows : 0][lane];
+    if (tres) t += __bfloat162float(tres[warp * p.ld_tres + col]);
+    static_cast<__nv_bfloat16 *>(p.ty)[size_t(warp) * p.N + col] = __float2bfloat16_rn(t);
+  }
+}
+
+// ----------------------------------------------------- gradient of the activation
+// dz = dy * act'(z), z from its 8-bit checkpoint, and the columns' sums of dz for the
+// bias, in one pass over dy. A warp's lanes hold 256 neighbouring columns, eight a
+// lane, and walk over the rows of their block's chunk; the eight warps' sums meet in
+// shared memory. ACT none: only the sums, dz is dy.
+constexpr int kDzUnroll = 4;
+template <bool ACT>
+__global__ void __launch_bounds__(256) linear_dz_kernel(const LinearDzParams p) {
+  __shared__ float red[8][256];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int32_t col = int32_t(blockIdx.x) * 256 + 8 * lane;
+  const int64_t r0 = int64_t(blockIdx.y) * p.chunk_rows;
+  const int64_t r1 = min(r0 + p.chunk_rows, p.M);
+  const bool in = col < p.C;
+  const __nv_bfloat16 *dy = static_cast<const __nv_bfloat16 *>(p.dy);
+  float sum[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) sum[i] = 0.f;
+  for (int64_t base = r0 + warp; base < r1; base += 8 * kDzUnroll) {
+    v8::Raw<__nv_bfloat16> raw[kDzUnroll];
+    uint2 codes[kDzUnroll];
+    uint32_t scale[kDzUnroll];
+#pragma unroll
+    for (int u = 0; u < kDzUnroll; ++u) {
+      const int64_t r = base + 8 * u;
+      raw[u] = v8::zero<__nv_bfloat16>();
+      codes[u] = make_uint2(0, 0);
+      scale[u] = 0;
+      if (!in || r >= r1) continue;
+      raw[u] = v8::load(dy + r * p.ld_dy + col);
+      if (ACT) {
+        codes[u] = __ldcs(reinterpret_cast<const uint2 *>(p.codes + size_t(r) * (32 * size_t(p.nb)) + col));
+        scale[u] = __ldg(p.scales + size_t(r) * p.ns + col / 32);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kDzUnroll; ++u) {
+      const int64_t r = base + 8 * u;
+      float d[8];
+      v8::unpack(raw[u], d);
+      if (ACT) {
+        float zv[8], sl[8];
+        const float unit = ck::unit_of(scale[u]);
+        ck::unpack_codes4(codes[u].x, unit, zv[0], zv[1], zv[2], zv[3]);
+        ck::unpack_codes4(codes[u].y, unit, zv[4], zv[5], zv[6], zv[7]);
+        lin::act_all<true>(p.act, zv, sl);
+        if (!in || r >= r1) continue;  // (zero codes of a row that is not there)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) d[i] *= sl[i];
+        v8::Raw<__nv_bfloat16> o;
+        v8::pack(d, o);
+        *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.dz) + size_t(r) * p.C + col) = o.a;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum[i] += d[i];
+    }
+  }
+  if (!p.partial) return;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) red[warp][8 * lane + i] = sum[i];
+  __syncthreads();
+  const int32_t c = int32_t(blockIdx.x) * 256 + int32_t(threadIdx.x);
+  if (c >= p.C) return;
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s += red[i][threadIdx.x];
+  p.partial[size_t(blockIdx.y) * p.C + c] = s;
+}
+
+// Sums the chunks' columns in a fixed order: 8 slices of the chunks, then the slices.
+__global__ void __launch_bounds__(256) column_sum_kernel(const float *part, int32_t chunks, int32_t C, float *out) {
+  __shared__ float s[8][32];
+  const int32_t c = int32_t(blockIdx.x) * 32 + int32_t(threadIdx.x & 31), slice = int32_t(threadIdx.x >> 5);
+  float acc = 0.f;
+  if (c < C) {
+#pragma unroll 8
+    for (int32_t b = slice; b < chunks; b += 8) acc += part[size_t(b) * C + c];
+  }
+  s[slice][threadIdx.x & 31] = acc;
+  __syncthreads();
+  if (slice == 0 && c < C) {
+#pragma unroll
+    for (int i = 1; i < 8; ++i) acc += s[i][threadIdx.x & 31];
+    out[c] = acc;
+  }
+}
+
+template <bool JVP, bool AMN, bool BMN, bool EPI>
+cudaError_t launch_tiles(const LinearParams &p, cudaStream_t stream) {
+  auto kernel = linear_sm100_kernel<JVP, AMN, BMN, EPI>;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Lay<JVP>::SMEM;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cfg.gridDim = dim3(2);
+  // per device, once: the shared-memory limit and how many pairs fit at a time
+  static std::atomic<uint64_t> set_up{0};
+  static std::atomic<int> max_pairs_of[64];
+  e = once_per_device(set_up, [&] {
+    cudaError_t r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<JVP>::SMEM);
+    int sms = 0, pairs = 0;
+    if (r == cudaSuccess) r = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (r == cudaSuccess) r = cudaOccupancyMaxActiveClusters(&pairs, kernel, &cfg);
+    if (r == cudaSuccess && dev < 64) max_pairs_of[dev].store(pairs >= 1 ? pairs : sms / 2);
+    return r;
+  });
+  if (e != cudaSuccess) return e;
+  const int64_t max_pairs = dev < 64 ? max_pairs_of[dev].load() : 74;
+  const int64_t units = int64_t(p.m_tiles) * p.n_tiles * p.splits;
+  cfg.gridDim = dim3(unsigned(2 * (units < max_pairs ? units : max_pairs)));
+  e = cudaLaunchKernelEx(&cfg, kernel, p);
+  if (e == cudaSuccess) e = cudaGetLastError();
+  if (e != cudaSuccess || p.splits == 1) return e;
+  const int64_t threads = int64_t(p.M) * ck::blocks_of(p.N) * 4;
+  linear_finish_kernel<JVP, EPI><<<unsigned((threads + 255) / 256), 256, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+template <int R>
+cudaError_t launch_rows(const LinearParams &p, cudaStream_t stream) {
+  // columns a warp: more reuse x, fewer give more blocks; a checkpoint needs blocks of 32
+  if (p.codes || p.N >= 32 * 148) {
+    linear_rows_kernel<R, 4><<<unsigned((p.N + 31) / 32), 256, 0, stream>>>(p);
+  } else if (p.N >= 16 * 148) {
+    linear_rows_kernel<R, 2><<<unsigned((p.N + 15) / 16), 256, 0, stream>>>(p);
+  } else {
+    linear_rows_kernel<R, 1><<<unsigned((p.N + 7) / 8), 256, 0, stream>>>(p);
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_linear_fwd(const LinearParams &p, cudaStream_t stream) {
+  const int32_t rows = p.tx ? 2 * p.M : p.M;
+  if (rows <= kLinearFewRows) {
+    if (rows == 1) return launch_rows<1>(p, stream);
+    if (rows == 2) return launch_rows<2>(p, stream);
+    return rows <= 4 ? launch_rows<4>(p, stream) : launch_rows<8>(p, stream);
+  }
+  return p.tx ? launch_tiles<true, false, false, true>(p, stream) : launch_tiles<false, false, false, true>(p, stream);
+}
+cudaError_t launch_linear_dx(const LinearParams &p, cudaStream_t stream) {
+  return launch_tiles<false, false, true, false>(p, stream);
+}
+cudaError_t launch_linear_dw(const LinearParams &p, cudaStream_t stream) {
+  return launch_tiles<false, true, true, false>(p, stream);
+}
+
+// Chunks of rows of the dz pass: about eight blocks an SM, at least 32 rows each.
+int32_t linear_dz_chunk_rows(int64_t M, int32_t C) {
+  const int64_t strips = (C + 255) / 256, want = (148 * 8 + strips - 1) / strips;
+  const int64_t rows = (M + want - 1) / want;
+  return int32_t(rows < 32 ? 32 : (rows + 31) & ~int64_t(31));
+}
+cudaError_t launch_linear_dz(const LinearDzParams &p, float *db, cudaStream_t stream) {
+  const int64_t chunks = (p.M + p.chunk_rows - 1) / p.chunk_rows;
+  const dim3 grid(unsigned((p.C + 255) / 256), unsigned(chunks));
+  if (p.act != lin::kActNone)
+    linear_dz_kernel<true><<<grid, 256, 0, stream>>>(p);
+  else
+    linear_dz_kernel<false><<<grid, 256, 0, stream>>>(p);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || !db) return e;
+  column_sum_kernel<<<unsigned((p.C + 31) / 32), 256, 0, stream>>>(p.partial, int32_t(chunks), p.C, db);
+  return cudaGetLastError();
+}
+
+cudaError_t read_and_clear_linear_error(uint32_t *out) {
+  uint32_t v = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(&v, g_linear_error, sizeof(v));
+  if (e == cudaSuccess && v) {
+    const uint32_t zero = 0;
+    e = cudaMemcpyToSymbol(g_linear_error, &zero, sizeof(zero));
+  }
+  *out = v;
+  return e;
+}
+
+}  // namespace caj

@@ -1,0 +1,133 @@
+// Inline-PTX wrappers for kernels that run as clusters of two CTAs sharing their
+// tensor-core products (tcgen05 cta_group::2), for TMA tile stores, and for
+// bounded mbarrier waits. One instruction (or one and its wait) each.
+#pragma once
+#include <cuda.h>
+#include <stdint.h>
+
+#include "ptx_sm100.cuh"
+
+namespace caj {
+namespace pair {
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_id() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%clusterid.x;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t clusters() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%nclusterid.x;" : "=r"(r));
+  return r;
+}
+// The shared::cluster address of this CTA's shared-memory word `saddr` in CTA `rank`.
+__device__ __forceinline__ uint32_t at_rank(uint32_t saddr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void sync_cluster() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void arrive_remote(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+// 2-D tile load into this CTA's shared memory, completion counted on an mbarrier
+// of either CTA of the pair. x * element size must be a multiple of 16 bytes.
+__device__ __forceinline__ void load_2d(uint32_t pred, uint32_t dst, const CUtensorMap *m, uint32_t bar, int32_t x,
+                                        int32_t y) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %0, 0;\n\t"
+      "@p cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%1], [%2, {%4, %5}], [%3];\n\t}" ::"r"(pred),
+      "r"(dst), "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(x), "r"(y)
+      : "memory");
+}
+// 2-D tile store; rows and columns past the tensor are not written.
+__device__ __forceinline__ void store_2d(const CUtensorMap *m, uint32_t src, int32_t x, int32_t y) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(m)),
+               "r"(src), "r"(x), "r"(y)
+               : "memory");
+}
+__device__ __forceinline__ void store_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void store_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void store_wait() {
+  asm volatile("cp.async.bulk.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+__device__ __forceinline__ void mma(uint32_t pred, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                    uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "setp.ne.b32 q, %0, 0;\n\t"
+      "@q tcgen05.mma.cta_group::2.kind::f16 [%1], %2, %3, %4, p;\n\t}" ::"r"(pred),
+      "r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Arrive once on the mbarrier at offset `bar` of both CTAs when the pair's products
+// issued so far are done (a commit, not a copy).
+__device__ __forceinline__ void commit(uint32_t pred, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %0, 0;\n\t"
+      "@p tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%1], %2;\n\t}" ::"r"(
+          pred),
+      "r"(bar), "h"(uint16_t(3))
+      : "memory");
+}
+__device__ __forceinline__ void tmem_alloc(uint32_t slot, uint32_t cols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "r"(cols) : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc(uint32_t tmem, uint32_t cols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(cols) : "memory");
+}
+
+// Bounded wait on a phase. On expiry `code` goes to *error (the first one stays)
+// and the CTA's abort flag is raised; a raised flag ends the wait too.
+__device__ __noinline__ inline void give_up(uint32_t *error, volatile int *abort_flag, uint32_t code) {
+  atomicCAS(error, 0u, code);
+  *abort_flag = 1;
+}
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, uint32_t *error, volatile int *abort_flag,
+                                     uint64_t timeout_ns, uint32_t code) {
+  if (ptx::mbar_test_wait(bar, parity)) return true;
+  const uint64_t t0 = ptx::globaltimer_ns();
+  for (uint32_t it = 1; it < 0x40000000u; ++it) {
+    if (ptx::mbar_try_wait(bar, parity)) return true;
+    if ((it & 31u) == 0) {
+      if (*abort_flag) return false;
+      if (ptx::globaltimer_ns() - t0 > timeout_ns) break;
+    }
+  }
+  give_up(error, abort_flag, code);
+  return false;
+}
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, uint32_t *error, volatile int *abort_flag,
+                                          uint64_t timeout_ns, uint32_t code) {
+  return __all_sync(0xffffffffu, wait(bar, parity, error, abort_flag, timeout_ns, code));
+}
+// Waits for this CTA's own copies or products on the way out; ignores the abort flag.
+__device__ __forceinline__ void drain(uint32_t bar, uint32_t parity, uint64_t timeout_ns) {
+  if (ptx::mbar_try_wait(bar, parity)) return;
+  const uint64_t t0 = ptx::globaltimer_ns();
+  for (uint32_t it = 1; it < 0x40000000u; ++it) {
+    if (ptx::mbar_try_wait(bar, parity)) return;
+    if ((it & 31u) == 0 && ptx::globaltimer_ns() - t0 > timeout_ns) return;
+  }
+}
+
+}  // namespace pair
+}  // namespace caj

@@ -123,3 +123,67 @@ def norm_rope_bwd(dy, x, g, cos, sin, eps, norm, layout):
     dg, adg = u * x / r, au * x.abs() / r
     keep = (0, 1, 2) if g.numel() == D else (0, 1)
     return (dx.reshape(B, N, H * D), dg.sum(keep).flatten(), adx.reshape(B, N, H * D), adg.sum(keep).flatten())
+
+
+# -------------------------------------------------------------------- linear layers
+
+def act(z, which):
+    """act(z) and its derivative, from the formulas."""
+    if which == "none":
+        return z, torch.ones_like(z)
+    if which == "silu":
+        s = torch.sigmoid(z)
+        return z * s, s + z * s * (1 - s)
+    if which == "gelu":
+        cdf = 0.5 * torch.erfc(-z / math.sqrt(2))
+        return z * cdf, cdf + z * torch.exp(-z * z / 2) / math.sqrt(2 * math.pi)
+    a, b = math.sqrt(2 / math.pi), 0.044715
+    t = torch.tanh(a * (z + b * z ** 3))
+    return 0.5 * z * (1 + t), 0.5 * (1 + t) + 0.5 * z * (1 - t * t) * a * (1 + 3 * b * z * z)
+
+
+def product_loss(depth):
+    """What a sum of `depth` products may lose, relative to the sum of their magnitudes:
+    products are exact, fp32 sums are truncated (2^-23), one after the other per 16 of them,
+    and up to 32 parts, a bias and a few more are added."""
+    return (depth / 16 + 40) * 2.0 ** -23
+
+
+ACT_LOSS = 2.0 ** -19  # exponential, reciprocal (2^-22 each, arguments below 2^3 amplify) and products
+
+
+def linear(x, w, bias, which, res, tx, tres):
+    """{"y": (value, bound without the output's own rounding), "ty": ..., "z": ...}."""
+    z, az = x @ w.t(), x.abs() @ w.abs().t()
+    if bias is not None:
+        z, az = z + bias, az + bias.abs()
+    ez = az * product_loss(x.shape[1])
+    y, slope = act(z, which)
+    ey = 1.2 * ez + ACT_LOSS * z.abs()  # |act'| < 1.13
+    if res is not None:
+        y, ey = y + res, ey + 2.0 ** -23 * (y.abs() + res.abs())
+    out = {"y": (y, ey), "z": (z, ez)}
+    if tx is not None:
+        tz, atz = tx @ w.t(), tx.abs() @ w.abs().t()
+        ty = slope * tz
+        ety = 1.2 * atz * product_loss(x.shape[1]) + (1.2 * ez + ACT_LOSS * (1 + z.abs())) * tz.abs()  # |act''| < 1.2
+        if which == "none":
+            ety = atz * product_loss(x.shape[1])
+        if tres is not None:
+            ty, ety = ty + tres, ety + 2.0 ** -23 * (ty.abs() + tres.abs())
+        out["ty"] = (ty, ety)
+    return out
+
+
+def linear_bwd(dy, x, w, z, which):
+    """dx, dw, db with bounds (without the outputs' own rounding)."""
+    dz, edz = dy, torch.zeros_like(dy)
+    if which != "none":
+        dz = dy * act(z, which)[1]
+        edz = dy.abs() * ACT_LOSS * (1 + z.abs())
+    rounded = dz.abs() * (2.0 ** -8 if which != "none" else 0.0) + edz
+    out = {"db": (dz.sum(0), edz.sum(0) + dz.abs().sum(0) * (dy.shape[0] / 8 + 64) * 2.0 ** -24)}
+    out["dx"] = (dz @ w, rounded @ w.abs() + dz.abs() @ w.abs() * product_loss(w.shape[0]))
+    if x is not None:
+        out["dw"] = (dz.t() @ x, rounded.t() @ x.abs() + dz.abs().t() @ x.abs() * product_loss(dy.shape[0]))
+    return out

@@ -201,3 +201,116 @@ def test_python_refuses_host_tensors():
     h = torch.zeros(1, 2, 4, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError):
         caj.qk_norm_rope_bwd(h, h, h, t, t, torch.ones(64), torch.ones(64), tab, tab)
+
+
+# --------------------------------------------------------------------- linear layers
+
+@pytest.mark.parametrize("which", ["none", "gelu_tanh", "gelu", "silu"])
+def test_linear_reference_against_differences(which):
+    g = torch.Generator().manual_seed(4)
+    rnd = lambda *s: torch.randn(*s, generator=g, dtype=torch.float64)  # noqa: E731
+    x, tx, w, b, dy = rnd(5, 8), rnd(5, 8), rnd(16, 8), rnd(16), rnd(5, 16)
+    f = lambda x_, w_, b_: ref.linear(x_, w_, b_, which, None, None, None)["y"][0]  # noqa: E731
+    h = 1e-5
+    num = (f(x + h * tx, w, b) - f(x - h * tx, w, b)) / (2 * h)
+    assert torch.allclose(ref.linear(x, w, b, which, None, tx, None)["ty"][0], num, rtol=0, atol=1e-7)
+    z = x @ w.t() + b
+    got = ref.linear_bwd(dy, x, w, z, which)
+    tw, tb = rnd(16, 8), rnd(16)
+    assert abs(float((got["dx"][0] * tx).sum() - (dy * num).sum())) < 1e-6
+    num_w = (f(x, w + h * tw, b) - f(x, w - h * tw, b)) / (2 * h)
+    assert abs(float((got["dw"][0] * tw).sum() - (dy * num_w).sum())) < 1e-6
+    num_b = (f(x, w, b + h * tb) - f(x, w, b - h * tb)) / (2 * h)
+    assert abs(float((got["db"][0] * tb).sum() - (dy * num_b).sum())) < 1e-6
+
+
+_LIN = ("x", "tx", "w", "bias", "res", "tres")
+_LOUT = ("y", "ty", "codes", "scales", "ws")
+
+
+def _lin_shape(**kw):
+    v = dict(M=100, K=64, C=128, act=1, ldx=64, ldtx=64, ldres=128, ldtres=128, ldy=128)
+    v.update(kw)
+    return _lib.LinearActShapeC(*[v[n] for n, _ in _lib.LinearActShapeC._fields_])
+
+
+def _lfwd(ptrs=None, ws_bytes=1 << 40, **kw):
+    p = dict.fromkeys(_LIN + _LOUT, A)
+    p.update(ptrs or {})
+    return _lib.lib().caj_linear_act_fwd(*[p[n] for n in _LIN], ctypes.byref(_lin_shape(**kw)),
+                                         *[p[n] for n in _LOUT], ws_bytes, None)
+
+
+_LBWD = ("dy", "x", "xs", "w", "codes", "scales")
+_LBOUT = ("dx", "dw", "db", "ws")
+
+
+def _lbwd(ptrs=None, ws_bytes=1 << 40, **kw):
+    p = dict.fromkeys(_LBWD + _LBOUT, A)
+    p.update(ptrs or {})
+    return _lib.lib().caj_linear_act_bwd(*[p[n] for n in _LBWD], ctypes.byref(_lin_shape(**kw)),
+                                         *[p[n] for n in _LBOUT], ws_bytes, None)
+
+
+_LIN_SHAPES = [(dict(M=0), INVALID), (dict(M=-5), INVALID), (dict(K=0), INVALID), (dict(C=0), INVALID),
+               (dict(act=4), INVALID), (dict(act=-1), INVALID), (dict(K=60), UNSUPPORTED), (dict(C=129), UNSUPPORTED),
+               (dict(M=1 << 31), UNSUPPORTED), (dict(K=1 << 25), UNSUPPORTED),
+               (dict(M=1 << 30, C=1 << 20), UNSUPPORTED)]
+
+
+@pytest.mark.parametrize("kw,want", _LIN_SHAPES)
+def test_linear_shape_refusals(kw, want):
+    size = ctypes.c_size_t(0)
+    assert _lfwd(**kw) == want and _lbwd(**kw) == want
+    assert _lib.lib().caj_linear_act_fwd_workspace(ctypes.byref(_lin_shape(**kw)), 0, ctypes.byref(size)) == want
+    assert _lib.lib().caj_linear_act_bwd_workspace(ctypes.byref(_lin_shape(**kw)), 0, ctypes.byref(size)) == want
+
+
+@pytest.mark.parametrize("kw", [dict(ldx=56), dict(ldx=68), dict(ldtx=63), dict(ldres=120), dict(ldtres=130),
+                                dict(ldx=-64)])
+def test_linear_fwd_row_refusals(kw):
+    assert _lfwd(**kw) == INVALID
+
+
+@pytest.mark.parametrize("ptrs", [dict(x=0), dict(w=0), dict(y=0), dict(x=A + 8), dict(tx=A + 2), dict(w=A + 8),
+                                  dict(bias=A + 2), dict(res=A + 8), dict(tres=A + 8), dict(tx=0), dict(ty=0),
+                                  dict(codes=0), dict(scales=0), dict(scales=A + 2), dict(codes=A + 8),
+                                  dict(tx=0, ty=0)])
+def test_linear_fwd_pointer_refusals(ptrs):
+    assert _lfwd(ptrs) == INVALID  # the last: tres without tx
+
+
+@pytest.mark.parametrize("ptrs", [dict(dy=0), dict(dy=A + 8), dict(w=0), dict(x=0), dict(x=A + 8), dict(xs=A + 1),
+                                  dict(codes=0), dict(scales=0), dict(dx=A + 8), dict(dw=A + 8), dict(db=A + 2),
+                                  dict(ws=0), dict(ws=A + 128), dict(dx=0, dw=0, db=0)])
+def test_linear_bwd_pointer_refusals(ptrs):
+    assert _lbwd(ptrs) == INVALID
+
+
+def test_linear_workspaces():
+    L, size = _lib.lib(), ctypes.c_size_t(0)
+    assert L.caj_linear_act_fwd_workspace(ctypes.byref(_lin_shape(M=4)), 1, ctypes.byref(size)) == 0 and size.value == 0
+    big = dict(M=256, K=8192, ldx=8192, ldtx=8192)
+    assert L.caj_linear_act_fwd_workspace(ctypes.byref(_lin_shape(**big)), 0, ctypes.byref(size)) == 0
+    assert size.value > 0  # one tile of a long contraction is split
+    assert _lfwd(ws_bytes=size.value - 1, ptrs=dict(tx=0, ty=0, tres=0), **big) == INVALID
+    assert L.caj_linear_act_fwd_workspace(ctypes.byref(_lin_shape()), 2, ctypes.byref(size)) == INVALID
+    assert L.caj_linear_act_bwd_workspace(ctypes.byref(_lin_shape()), 1, None) == INVALID
+    assert L.caj_linear_act_bwd_workspace(ctypes.byref(_lin_shape()), 1, ctypes.byref(size)) == 0
+    assert _lbwd(ws_bytes=size.value - 1) == INVALID
+
+
+@pytest.mark.skipif(not _NO_GPU, reason="valid calls with fake pointers must not launch")
+def test_valid_linear_calls_reach_the_device_check():
+    assert _lfwd() == _lbwd() == CUDA
+    assert _lfwd(dict.fromkeys(("tx", "ty", "tres", "res", "bias", "codes", "scales"), 0)) == CUDA
+    assert _lbwd(dict(xs=0)) == _lbwd(dict(xs=0, codes=0, scales=0), act=0) == CUDA
+    assert _lbwd(dict(dx=0, w=0)) == _lbwd(dict(dw=0, x=0, xs=0)) == CUDA
+
+
+def test_linear_python_refuses_host_tensors():
+    x, w = torch.zeros(4, 64, dtype=torch.bfloat16), torch.zeros(8, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        caj.linear_act_fwd(x, w)
+    with pytest.raises(ValueError):
+        caj.linear_act_bwd(torch.zeros(4, 8, dtype=torch.bfloat16), x, w)
