@@ -14,7 +14,6 @@ empty outputs (and zero gradients) without a launch.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 from typing import NamedTuple, Optional, Sequence, Tuple, Union
@@ -29,21 +28,30 @@ __all__ = ["Ckpt8", "ckpt8_pack", "ckpt8_unpack", "rope_frequencies", "rope_tabl
 _DTYPES = {torch.float32: _lib.CAJ_DTYPE_F32, torch.bfloat16: _lib.CAJ_DTYPE_BF16}
 
 
-def _ptr(t: Optional[torch.Tensor]) -> ctypes.c_void_p:
-    return ctypes.c_void_p(t.data_ptr() if t is not None else 0)
+# The calls are short, so what surrounds them is kept short too: addresses go to ctypes as plain
+# ints, the current stream comes as a raw handle, and the device is switched only where it differs.
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-@contextlib.contextmanager
-def _on(t: torch.Tensor):
-    """Makes t's device current for the call; gives its current stream."""
-    with torch.cuda.device(t.device):
-        yield ctypes.c_void_p(torch.cuda.current_stream(t.device).cuda_stream)
+def _ptr(t: Optional[torch.Tensor]) -> int:
+    return 0 if t is None else t.data_ptr()
 
 
-def _same_device(what: str, *tensors):
-    first = tensors[0]
+def _run(name: str, device: torch.device, *args):
+    """Calls the library's `name` on `device`'s current stream, with that device current."""
+    fn, index = getattr(_lib.lib(), name), device.index
+    if index == torch.cuda.current_device():
+        st = fn(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            st = fn(*args, _raw_stream(index))
+    if st:
+        _lib.check(st, name)
+
+
+def _same_device(what: str, device: torch.device, *tensors):
     for t in tensors:
-        if t is not None and not (t.is_cuda and t.device == first.device):
+        if t is not None and t.device != device:
             raise ValueError(f"{what}: all tensors must be CUDA tensors on one device")
 
 
@@ -71,16 +79,20 @@ def _ckpt_widths(C: int) -> Tuple[int, int]:
 
 def _check_ckpt(what: str, c: Ckpt8):
     w, ns = _ckpt_widths(c.shape[-1])
-    for t, dtype, width in ((c.codes, torch.int8, w), (c.scales, torch.uint8, ns)):
-        if not (t.is_cuda and t.is_contiguous() and t.dtype == dtype and tuple(t.shape) == (c.rows, width)):
-            raise ValueError(f"{what}: a checkpoint's codes are int8 [rows, {w}] and its scales uint8 "
-                             f"[rows, {ns}], contiguous CUDA tensors")
+    rows, codes, scales = c.rows, c.codes, c.scales
+    if not (codes.is_cuda and codes.dtype == torch.int8 and codes.shape == (rows, w) and codes.is_contiguous()
+            and scales.is_cuda and scales.dtype == torch.uint8 and scales.shape == (rows, ns)
+            and scales.is_contiguous()):
+        raise ValueError(f"{what}: a checkpoint's codes are int8 [rows, {w}] and its scales uint8 "
+                         f"[rows, {ns}], contiguous CUDA tensors")
 
 
 def _rows(t: torch.Tensor) -> Optional[Tuple[int, int]]:
     """(rows, elements between rows) of t seen as rows of its last axis; None if its strides
     do not allow it."""
     rows = math.prod(t.shape[:-1])
+    if t.is_contiguous():
+        return rows, max(t.shape[-1], 1)
     if t.numel() == 0:
         return rows, max(t.shape[-1], 1)
     if t.shape[-1] > 1 and t.stride(-1) != 1:
@@ -112,11 +124,9 @@ def ckpt8_pack(x: torch.Tensor) -> Ckpt8:
     rows, ld = at
     C = x.shape[-1]
     w, ns = _ckpt_widths(C)
-    codes = torch.empty((rows, w), dtype=torch.int8, device=x.device)
-    scales = torch.empty((rows, ns), dtype=torch.uint8, device=x.device)
-    with _on(x) as s:
-        st = _lib.lib().caj_ckpt_pack(_ptr(x), rows, C, ld, _DTYPES[x.dtype], _ptr(codes), _ptr(scales), s)
-    _lib.check(st, "caj_ckpt_pack")
+    codes = x.new_empty((rows, w), dtype=torch.int8)
+    scales = x.new_empty((rows, ns), dtype=torch.uint8)
+    _run("caj_ckpt_pack", x.device, x.data_ptr(), rows, C, ld, _DTYPES[x.dtype], codes.data_ptr(), scales.data_ptr())
     return Ckpt8(codes, scales, tuple(x.shape))
 
 
@@ -125,12 +135,11 @@ def ckpt8_unpack(c: Ckpt8, dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
     _check_ckpt("ckpt8_unpack", c)
     if dtype not in _DTYPES:
         raise ValueError("ckpt8_unpack: dtype must be bf16 or fp32")
-    _same_device("ckpt8_unpack", c.codes, c.scales)
-    x = torch.empty(c.shape, dtype=dtype, device=c.codes.device)
-    with _on(x) as s:
-        st = _lib.lib().caj_ckpt_unpack(_ptr(c.codes), _ptr(c.scales), c.rows, c.shape[-1], c.shape[-1],
-                                        _DTYPES[dtype], _ptr(x), s)
-    _lib.check(st, "caj_ckpt_unpack")
+    device, C = c.codes.device, c.shape[-1]
+    _same_device("ckpt8_unpack", device, c.scales)
+    x = c.codes.new_empty(c.shape, dtype=dtype)
+    _run("caj_ckpt_unpack", device, c.codes.data_ptr(), c.scales.data_ptr(), c.rows, C, C, _DTYPES[dtype],
+         x.data_ptr())
     return x
 
 
@@ -174,19 +183,18 @@ def rope_table(pos: torch.Tensor, freq: torch.Tensor, axis: Optional[torch.Tenso
         raise ValueError("rope_table: freq must be a contiguous fp64 tensor [P]")
     if axis is not None and not (axis.dtype == torch.int32 and axis.shape == freq.shape and axis.is_contiguous()):
         raise ValueError("rope_table: axis must be a contiguous int32 tensor [P]")
-    _same_device("rope_table", pos, freq, axis)
-    N, P, A = pos.shape[0], freq.numel(), pos.shape[1] if pos.dim() == 2 else 1
-    cos, sin = (torch.empty((N, P), dtype=torch.float32, device=pos.device) for _ in range(2))
-    with _on(pos) as s:
-        st = _lib.lib().caj_rope_table(_ptr(pos), int(pos.dtype == torch.int64), _ptr(freq), _ptr(axis), N, A, P,
-                                       float(mscale), _ptr(cos), _ptr(sin), s)
-    _lib.check(st, "caj_rope_table")
+    _same_device("rope_table", pos.device, freq, axis)
+    N, P, A = pos.shape[0], freq.shape[0], pos.shape[1] if pos.dim() == 2 else 1
+    cos = pos.new_empty((N, P), dtype=torch.float32)
+    sin = pos.new_empty((N, P), dtype=torch.float32)
+    _run("caj_rope_table", pos.device, pos.data_ptr(), pos.dtype == torch.int64, freq.data_ptr(), _ptr(axis), N, A, P,
+         mscale, cos.data_ptr(), sin.data_ptr())
     return cos, sin
 
 
 def _token_rows(what: str, name: str, t: torch.Tensor, B: int, N: int, width: int, like: torch.Tensor):
     """t [B, N, width] with one distance between tokens: that distance. Raises otherwise."""
-    if not (t.is_cuda and t.dtype == like.dtype and tuple(t.shape) == (B, N, width)):
+    if not (t.is_cuda and t.dtype == like.dtype and t.shape == (B, N, width)):
         raise ValueError(f"{what}: {name} must be a {like.dtype} CUDA tensor [{B}, {N}, {width}]")
     at = _rows(t)
     if at is None or at[1] * t.element_size() % 16 or t.data_ptr() % 16:
@@ -236,23 +244,23 @@ def qk_norm_rope_fwd(xq, xk, xv, gq, gk, rope_cos, rope_sin, H: int, Hk: Optiona
     tan = txq is not None
     if (txk is None) == tan or (txv is not None) != (tan and xv is not None):
         raise ValueError(f"{what}: give the tangents of all inputs or of none")
-    _same_device(what, xq, xk, xv, *tangents, gq, gk, rope_cos, rope_sin)
+    _same_device(what, xq.device, xk, xv, *tangents, gq, gk, rope_cos, rope_sin)
     shape = _rope_shape(what, B, N, H, Hk, D, xq.dtype, gq, gk, rope_cos, rope_sin, eps, norm, layout)
-    for name, t, heads in (("q", xq, H), ("k", xk, Hk), ("v", xv, Hk), ("tq", txq, H), ("tk", txk, Hk),
-                           ("tv", txv, Hk)):
-        if t is not None:
-            setattr(shape, "ld" + name, _token_rows(what, "x" + name if len(name) == 1 else "tx" + name[1], t, B, N,
-                                                    heads * D, xq))
-
-    def out(t, heads):
-        return None if t is None else torch.empty((B, heads, N, D), dtype=xq.dtype, device=xq.device)
-    outs = [out(t, h) for t, h in zip((xq, xk, xv) + tangents, (H, Hk, Hk) * 2)]
+    shape.ldq = _token_rows(what, "xq", xq, B, N, H * D, xq)
+    shape.ldk = _token_rows(what, "xk", xk, B, N, Hk * D, xq)
+    if xv is not None:
+        shape.ldv = _token_rows(what, "xv", xv, B, N, Hk * D, xq)
+    if tan:
+        shape.ldtq = _token_rows(what, "txq", txq, B, N, H * D, xq)
+        shape.ldtk = _token_rows(what, "txk", txk, B, N, Hk * D, xq)
+        if xv is not None:
+            shape.ldtv = _token_rows(what, "txv", txv, B, N, Hk * D, xq)
+    outs = [None if t is None else xq.new_empty((B, h, N, D))
+            for t, h in ((xq, H), (xk, Hk), (xv, Hk), (txq, H), (txk, Hk), (txv, Hk))]
     if B * N:
-        with _on(xq) as s:
-            st = _lib.lib().caj_qk_rope_fwd(*[_ptr(t) for t in (xq, xk, xv) + tangents], _ptr(gq), _ptr(gk),
-                                            _ptr(rope_cos), _ptr(rope_sin), ctypes.byref(shape),
-                                            *[_ptr(t) for t in outs], s)
-        _lib.check(st, "caj_qk_rope_fwd")
+        _run("caj_qk_rope_fwd", xq.device, xq.data_ptr(), xk.data_ptr(), _ptr(xv), _ptr(txq), _ptr(txk), _ptr(txv),
+             _ptr(gq), _ptr(gk), rope_cos.data_ptr(), rope_sin.data_ptr(), ctypes.byref(shape),
+             *[_ptr(t) for t in outs])
     return tuple(t for t in outs if t is not None)
 
 
@@ -271,7 +279,7 @@ def qk_norm_rope_bwd(dq, dk, dv, xq, xk, gq, gk, rope_cos, rope_sin, eps: float 
     Hk = dk.shape[1]
     for t, h in ((dq, H), (dk, Hk), (dv, Hk)):
         if t is not None and not (t.is_cuda and t.is_contiguous() and t.dtype == dq.dtype
-                                  and tuple(t.shape) == (B, h, N, D)):
+                                  and t.shape == (B, h, N, D)):
             raise ValueError(f"{what}: dq, dk, dv must be contiguous CUDA tensors [B, heads, N, D] of one dtype")
     shape = _rope_shape(what, B, N, H, Hk, D, dq.dtype, gq, gk, rope_cos, rope_sin, eps, norm, layout)
     ckpt = isinstance(xq, Ckpt8)
@@ -293,23 +301,17 @@ def qk_norm_rope_bwd(dq, dk, dv, xq, xk, gq, gk, rope_cos, rope_sin, eps: float 
                     raise ValueError(f"{what}: {name} is needed")
                 setattr(shape, ("ldq", "ldk")[i], _token_rows(what, name, x, B, N, h * D, dq))
                 xs[i] = x
-    _same_device(what, dq, dk, dv, *xs, *scales, gq, gk, rope_cos, rope_sin)
-
-    def out(t, h):
-        return None if t is None else torch.empty((B, N, h * D), dtype=dq.dtype, device=dq.device)
-    dx = [out(dq, H), out(dk, Hk), out(dv, Hk)]
+    _same_device(what, dq.device, dk, dv, *xs, *scales, gq, gk, rope_cos, rope_sin)
+    dx = [None if t is None else dq.new_empty((B, N, h * D)) for t, h in ((dq, H), (dk, Hk), (dv, Hk))]
     dg = [None if g is None else torch.zeros_like(g) if B * N == 0 else torch.empty_like(g) for g in (gq, gk)]
     if B * N:
         nbytes = ctypes.c_size_t(0)
         _lib.check(_lib.lib().caj_qk_rope_bwd_workspace(ctypes.byref(shape), ctypes.byref(nbytes)),
                    "caj_qk_rope_bwd_workspace")
-        with _on(dq) as s:
-            ws = torch.empty(nbytes.value, dtype=torch.uint8, device=dq.device)
-            st = _lib.lib().caj_qk_rope_bwd(_ptr(dq), _ptr(dk), _ptr(dv), _ptr(xs[0]), _ptr(xs[1]), _ptr(scales[0]),
-                                            _ptr(scales[1]), _ptr(gq), _ptr(gk), _ptr(rope_cos), _ptr(rope_sin),
-                                            ctypes.byref(shape), *[_ptr(t) for t in dx], _ptr(dg[0]), _ptr(dg[1]),
-                                            _ptr(ws), nbytes.value, s)
-        _lib.check(st, "caj_qk_rope_bwd")
+        ws = dq.new_empty(nbytes.value, dtype=torch.uint8)
+        _run("caj_qk_rope_bwd", dq.device, dq.data_ptr(), dk.data_ptr(), _ptr(dv), _ptr(xs[0]), _ptr(xs[1]),
+             _ptr(scales[0]), _ptr(scales[1]), _ptr(gq), _ptr(gk), rope_cos.data_ptr(), rope_sin.data_ptr(),
+             ctypes.byref(shape), *[_ptr(t) for t in dx], _ptr(dg[0]), _ptr(dg[1]), ws.data_ptr(), nbytes.value)
     return (*dx, *dg)
 
 
@@ -365,25 +367,21 @@ def linear_act_fwd(x, w, bias=None, act: str = "none", residual=None, tx=None, t
         shape.ldres = _matrix(what, "residual", residual, M, C)
     if tresidual is not None:
         shape.ldtres = _matrix(what, "tresidual", tresidual, M, C)
-    _same_device(what, x, w, bias, residual, tx, tresidual)
-    y = torch.empty(lead + (C,), dtype=torch.bfloat16, device=x.device)
-    ty = torch.empty_like(y) if tx is not None else None
+    _same_device(what, x.device, w, bias, residual, tx, tresidual)
+    y = x.new_empty(lead + (C,))
+    ty = x.new_empty(lead + (C,)) if tx is not None else None
     pre = None
     if save_pre:
         cw, sw = _ckpt_widths(C)
-        pre = Ckpt8(torch.empty((M, cw), dtype=torch.int8, device=x.device),
-                    torch.empty((M, sw), dtype=torch.uint8, device=x.device), lead + (C,))
+        pre = Ckpt8(x.new_empty((M, cw), dtype=torch.int8), x.new_empty((M, sw), dtype=torch.uint8), lead + (C,))
     if M:
         nbytes = ctypes.c_size_t(0)
         _lib.check(_lib.lib().caj_linear_act_fwd_workspace(ctypes.byref(shape), int(tx is not None),
                                                            ctypes.byref(nbytes)), "caj_linear_act_fwd_workspace")
-        with _on(x) as s:
-            ws = torch.empty(nbytes.value, dtype=torch.uint8, device=x.device) if nbytes.value else None
-            st = _lib.lib().caj_linear_act_fwd(
-                _ptr(x), _ptr(tx), _ptr(w), _ptr(bias), _ptr(residual), _ptr(tresidual), ctypes.byref(shape), _ptr(y),
-                _ptr(ty), _ptr(pre.codes if pre else None), _ptr(pre.scales if pre else None), _ptr(ws),
-                nbytes.value, s)
-        _lib.check(st, "caj_linear_act_fwd")
+        ws = x.new_empty(nbytes.value, dtype=torch.uint8) if nbytes.value else None
+        _run("caj_linear_act_fwd", x.device, x.data_ptr(), _ptr(tx), w.data_ptr(), _ptr(bias), _ptr(residual),
+             _ptr(tresidual), ctypes.byref(shape), y.data_ptr(), _ptr(ty), _ptr(pre.codes if pre else None),
+             _ptr(pre.scales if pre else None), _ptr(ws), nbytes.value)
     return y, ty, pre
 
 
@@ -423,21 +421,19 @@ def linear_act_bwd(dy, x, w, act: str = "none", pre: Optional[Ckpt8] = None, bia
             raise ValueError(f"{what}: an activation needs the checkpoint of z, {M} rows of {C}")
         _check_ckpt(what, pre)
     xs = x.codes if ckpt else x
-    _same_device(what, dy, w, *(t for t in (xs if need[1] else None, x.scales if ckpt else None,
-                                            *(pre[:2] if pre else ()))))
-    dx = torch.empty(lead + (K,), dtype=torch.bfloat16, device=dy.device) if need[0] else None
-    make = torch.empty if M else torch.zeros
-    dw = make((C, K), dtype=torch.bfloat16, device=dy.device) if need[1] else None
-    db = make((C,), dtype=torch.float32, device=dy.device) if bias else None
+    _same_device(what, dy.device, w, *(t for t in (xs if need[1] else None, x.scales if ckpt else None,
+                                                   *(pre[:2] if pre else ()))))
+    dx = dy.new_empty(lead + (K,)) if need[0] else None
+    make = dy.new_empty if M else dy.new_zeros
+    dw = make((C, K)) if need[1] else None
+    db = make((C,), dtype=torch.float32) if bias else None
     if M:
         nbytes = ctypes.c_size_t(0)
         _lib.check(_lib.lib().caj_linear_act_bwd_workspace(ctypes.byref(shape), int(ckpt), ctypes.byref(nbytes)),
                    "caj_linear_act_bwd_workspace")
-        with _on(dy) as s:
-            ws = torch.empty(nbytes.value, dtype=torch.uint8, device=dy.device) if nbytes.value else None
-            st = _lib.lib().caj_linear_act_bwd(
-                _ptr(dy), _ptr(xs if need[1] else None), _ptr(x.scales if ckpt and need[1] else None), _ptr(w),
-                _ptr(pre.codes if pre else None), _ptr(pre.scales if pre else None), ctypes.byref(shape), _ptr(dx),
-                _ptr(dw), _ptr(db), _ptr(ws), nbytes.value, s)
-        _lib.check(st, "caj_linear_act_bwd")
+        ws = dy.new_empty(nbytes.value, dtype=torch.uint8) if nbytes.value else None
+        _run("caj_linear_act_bwd", dy.device, dy.data_ptr(), _ptr(xs if need[1] else None),
+             _ptr(x.scales if ckpt and need[1] else None), w.data_ptr(), _ptr(pre.codes if pre else None),
+             _ptr(pre.scales if pre else None), ctypes.byref(shape), _ptr(dx), _ptr(dw), _ptr(db), _ptr(ws),
+             nbytes.value)
     return dx, dw, db
