@@ -258,6 +258,7 @@ caj_status caj_linear_act_bwd(const void *dy, const void *x, const uint8_t *x_sc
       c.nb = caj::ck::blocks_of(shape->K);
       c.ns = caj::ck::scale_bytes(shape->K);
       c.total = uint32_t(M * c.nb);
+      c.rows = uint32_t(M);
       st = done(caj::launch_ckpt8(c, true, true, s));
       if (st != CAJ_OK) return st;
       x = x_values;

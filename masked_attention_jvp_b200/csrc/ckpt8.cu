@@ -9,6 +9,8 @@
 // Rows whose 16-byte vectors do not line up (C not a multiple of 8, or a base or
 // row stride that is not 16-byte aligned) take the lane form: one lane per value,
 // coalesced 2- or 4-byte accesses, the maximum by one redux instruction.
+// 32760 x 1536 bf16 on B200: PACKED us packed, UNPACKED us unpacked in the vector form;
+// 32760 x 1545 ODDP and ODDU us in the lane form.
 #include <cuda_runtime.h>
 
 #include "ckpt8.cuh"
@@ -105,74 +107,68 @@ __global__ void __launch_bounds__(kThreads) unpack_vec_kernel(const Ckpt8Params 
   }
 }
 
-// One lane per value: blocks are dealt to warps a grid apart, kLaneUnroll at a time.
-constexpr int kLaneUnroll = 8;
+// One lane per value: a warp takes a run of up to eight blocks of one row.
+constexpr int kRun = 8;
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads) pack_lane_kernel(const Ckpt8Params p) {
-  const uint32_t nb = uint32_t(p.nb), total = p.total;
-  const uint32_t step = gridDim.x * (kThreads / 32);
-  const uint32_t first = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  const uint32_t runs = (uint32_t(p.nb) + kRun - 1) / kRun;
+  const uint32_t unit = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
-  float v[kLaneUnroll];
-  uint32_t row[kLaneUnroll], blk[kLaneUnroll];
+  const uint32_t row = unit / runs;
+  if (row >= p.rows) return;
+  const int32_t blk0 = int32_t(unit - row * runs) * kRun;
+  const T *x = static_cast<const T *>(p.x) + size_t(row) * p.ld + blk0 * ck::kBlock + lane;
+  int8_t *codes = p.codes + (size_t(row) * p.nb + blk0) * ck::kBlock + lane;
+  const int32_t left = p.cols - blk0 * ck::kBlock - lane, blocks = min(kRun, p.nb - blk0);
+  float v[kRun];
 #pragma unroll
-  for (int u = 0; u < kLaneUnroll; ++u) {
-    const uint64_t g = uint64_t(first) + uint64_t(u) * step;
-    row[u] = g < total ? uint32_t(g) / nb : 0xFFFFFFFFu;
-    blk[u] = uint32_t(g) - row[u] * nb;
-    const int32_t c = int32_t(blk[u]) * ck::kBlock + lane;
-    v[u] = 0.f;
-    if (g < total && c < p.cols) v[u] = v8::to_float(static_cast<const T *>(p.x)[size_t(row[u]) * p.ld + c]);
-  }
+  for (int j = 0; j < kRun; ++j) v[j] = 32 * j < left ? v8::to_float(x[32 * j]) : 0.f;
+  uint32_t mine = 0;  // lane j keeps the scale of block j
 #pragma unroll
-  for (int u = 0; u < kLaneUnroll; ++u) {
-    const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, ck::mag_bits(v[u]));
-    if (row[u] == 0xFFFFFFFFu) continue;
-    const uint32_t s = ck::scale_of(m);
-    float f[1] = {v[u]};
+  for (int j = 0; j < kRun; ++j) {
+    const uint32_t s = ck::scale_of(__reduce_max_sync(0xFFFFFFFFu, ck::mag_bits(v[j])));
+    if (lane == j) mine = s;
+    if (j >= blocks) continue;
+    float f[1] = {v[j]};
     ck::saturate(f, s);
-    const uint32_t code = s == 255u ? 0u : ck::code_word(f[0], ck::up_of(s));
-    p.codes[(size_t(row[u]) * nb + blk[u]) * ck::kBlock + lane] = int8_t(code & 0xFFu);
-    if (lane == 0) store_scale(p.scales + size_t(row[u]) * p.ns, int32_t(blk[u]), p.nb, p.ns, s);
+    codes[32 * j] = s == 255u ? int8_t(0) : int8_t(ck::code_word(f[0], ck::up_of(s)) & 0xFFu);
   }
+  if (lane < kRun && blk0 + lane < p.ns)  // runs start at multiples of 8: padding bytes included
+    p.scales[size_t(row) * p.ns + blk0 + lane] = uint8_t(lane < blocks ? mine : 0u);
 }
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads) unpack_lane_kernel(const Ckpt8Params p) {
-  const uint32_t nb = uint32_t(p.nb), total = p.total;
-  const uint32_t step = gridDim.x * (kThreads / 32);
-  const uint32_t first = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  const uint32_t runs = (uint32_t(p.nb) + kRun - 1) / kRun;
+  const uint32_t unit = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
-  int8_t code[kLaneUnroll];
-  uint32_t row[kLaneUnroll], scale[kLaneUnroll];
-  int32_t col[kLaneUnroll];
+  const uint32_t row = unit / runs;
+  if (row >= p.rows) return;
+  const int32_t blk0 = int32_t(unit - row * runs) * kRun;
+  T *out = static_cast<T *>(p.out) + size_t(row) * p.ld + blk0 * ck::kBlock + lane;
+  const int8_t *codes = p.codes + (size_t(row) * p.nb + blk0) * ck::kBlock + lane;
+  const int32_t left = p.cols - blk0 * ck::kBlock - lane;
+  int8_t code[kRun];
 #pragma unroll
-  for (int u = 0; u < kLaneUnroll; ++u) {
-    const uint64_t g = uint64_t(first) + uint64_t(u) * step;
-    row[u] = g < total ? uint32_t(g) / nb : 0xFFFFFFFFu;
-    const uint32_t blk = uint32_t(g) - row[u] * nb;
-    col[u] = int32_t(blk) * ck::kBlock + lane;
-    code[u] = 0;
-    scale[u] = 0;
-    if (g < total) {
-      code[u] = p.codes[(size_t(row[u]) * nb + blk) * ck::kBlock + lane];
-      scale[u] = __ldg(p.scales + size_t(row[u]) * p.ns + blk);
-    }
-  }
+  for (int j = 0; j < kRun; ++j) code[j] = 32 * j < left ? codes[32 * j] : int8_t(0);
+  uint32_t scale = 0;
+  if (lane < kRun && blk0 + lane < p.nb) scale = p.scales[size_t(row) * p.ns + blk0 + lane];
 #pragma unroll
-  for (int u = 0; u < kLaneUnroll; ++u) {
-    if (row[u] == 0xFFFFFFFFu || col[u] >= p.cols) continue;
+  for (int j = 0; j < kRun; ++j) {
+    const float unit_j = ck::unit_of(__shfl_sync(0xFFFFFFFFu, scale, j));
+    if (32 * j >= left) continue;
     T o;
-    v8::from_float(float(code[u]) * ck::unit_of(scale[u]), o);
-    static_cast<T *>(p.out)[size_t(row[u]) * p.ld + col[u]] = o;
+    v8::from_float(float(code[j]) * unit_j, o);
+    out[32 * j] = o;
   }
 }
 
 template <typename T>
 cudaError_t launch(const Ckpt8Params &p, bool unpack, bool vec, cudaStream_t stream) {
-  const uint32_t per_cta = vec ? kThreads / 4 * kUnroll : kThreads / 32 * kLaneUnroll;
-  const unsigned grid = unsigned((uint64_t(p.total) + per_cta - 1) / per_cta);
+  const uint64_t units = vec ? p.total : uint64_t(p.rows) * ((p.nb + kRun - 1) / kRun);
+  const uint32_t per_cta = vec ? kThreads / 4 * kUnroll : kThreads / 32;
+  const unsigned grid = unsigned((units + per_cta - 1) / per_cta);
   if (unpack) {
     if (vec)
       unpack_vec_kernel<T><<<grid, kThreads, 0, stream>>>(p);

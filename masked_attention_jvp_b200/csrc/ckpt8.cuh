@@ -20,6 +20,8 @@
 #pragma once
 #include <stdint.h>
 
+#include "ptx_sm100.cuh"
+
 namespace caj {
 namespace ck {
 
@@ -53,26 +55,59 @@ __device__ __forceinline__ float up_of(uint32_t s) { return __uint_as_float((254
 // 2^(s - 127); infinity for s = 255, subnormal for s = 0.
 __device__ __forceinline__ float unit_of(uint32_t s) { return __uint_as_float(s ? s << 23 : 0x400000u); }
 
+// Largest magnitude of M values; NaN if one is NaN (max.NaN keeps it).
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+template <int M>
+__device__ __forceinline__ float max_mag(const float (&f)[M]) {
+  float m[4] = {0.f, 0.f, 0.f, 0.f};  // four chains
+#pragma unroll
+  for (int i = 0; i < M; ++i) m[i & 3] = max_nan(m[i & 3], fabsf(f[i]));
+  return max_nan(max_nan(m[0], m[1]), max_nan(m[2], m[3]));
+}
+
 // |x| as ordered bits (NaN above infinity above every number).
 __device__ __forceinline__ uint32_t mag_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
 
 // Code of x, |x * up| <= 127: adding 1.5 * 2^23 rounds to the nearest whole
-// number, ties to even, and leaves it in the low byte.
+// number, ties to even, and leaves it in the low byte (one fma: the product with a
+// power of two is exact, or too small to matter).
 __device__ __forceinline__ uint32_t code_word(float x, float up) {
-  return __float_as_uint(__fadd_rn(__fmul_rn(x, up), 12582912.f));
+  return __float_as_uint(__fmaf_rn(x, up, 12582912.f));
 }
 __device__ __forceinline__ uint32_t pack_codes4(float a, float b, float c, float d, float up) {
   const uint32_t ab = __byte_perm(code_word(a, up), code_word(b, up), 0x0040);
   const uint32_t cd = __byte_perm(code_word(c, up), code_word(d, up), 0x0040);
   return __byte_perm(ab, cd, 0x5410);
 }
-// Four codes -> values: byte ^ 0x80 under the exponent of 2^23 is 2^23 + 128 + c.
+// A block's codes at the largest scale, where values may saturate (rare: kept out of line).
+__device__ __noinline__ inline void pack_saturated_block(float *f, uint32_t *w) {
+  const float up = up_of(kMaxScale);
+  for (int i = 0; i < kBlock; ++i) f[i] = fminf(fmaxf(f[i], -kTop), kTop);
+  for (int i = 0; i < kBlock / 4; ++i) w[i] = pack_codes4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3], up);
+}
+__device__ __forceinline__ void pack_saturated(const float (&v)[kBlock], uint32_t (&w)[kBlock / 4]) {
+  float f[kBlock];
+  uint32_t o[kBlock / 4];
+#pragma unroll
+  for (int i = 0; i < kBlock; ++i) f[i] = v[i];
+  pack_saturated_block(f, o);
+#pragma unroll
+  for (int i = 0; i < kBlock / 4; ++i) w[i] = o[i];
+}
+// Four codes -> values: byte ^ 0x80 under the exponent of 2^23 is 2^23 + 128 + c; in
+// packed pairs. (One fma with -(2^23 + 128) * unit instead would overflow from unit
+// 2^105 on.) unit = infinity: 0 * infinity = NaN, as the format wants.
 __device__ __forceinline__ void unpack_codes4(uint32_t w, float unit, float &a, float &b, float &c, float &d) {
   const uint32_t u = w ^ 0x80808080u;
-  a = (__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7440)) - 8388736.f) * unit;
-  b = (__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7441)) - 8388736.f) * unit;
-  c = (__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7442)) - 8388736.f) * unit;
-  d = (__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7443)) - 8388736.f) * unit;
+  const uint64_t off = ptx::f2(8388736.f, 8388736.f), un = ptx::f2(unit, unit);
+  ptx::f2_split(ptx::mul2(ptx::sub2(ptx::f2(__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7440)),
+                                            __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7441))), off), un), a, b);
+  ptx::f2_split(ptx::mul2(ptx::sub2(ptx::f2(__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7442)),
+                                            __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7443))), off), un), c, d);
 }
 
 }  // namespace ck

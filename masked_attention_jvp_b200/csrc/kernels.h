@@ -184,6 +184,7 @@ struct QkRopeParams {
   int32_t B, N, Hq, Hk, D, P;
   float eps;
   int32_t norm, half, gain_full, blocks;
+  int32_t tensors;             // 3, or 2 without v
 };
 
 // Matrix products of the linear operators; the operands' maps have 128-byte-swizzled
@@ -225,7 +226,7 @@ struct Ckpt8Params {
   int8_t *codes;       // [rows, 32 nb]
   uint8_t *scales;     // [rows, ns]
   int64_t ld;
-  uint32_t total;
+  uint32_t total, rows;
   int32_t cols, nb, ns;
 };
 

@@ -47,11 +47,61 @@ __device__ __forceinline__ float act(float z, float &slope) {
   }
 }
 
+// The same for a pair of values in packed fp32 arithmetic: one instruction for both
+// halves of each step but the two approximations (GELU's erf stays scalar).
+template <int ACT, bool SLOPE>
+__device__ __forceinline__ uint64_t act2(uint64_t z, uint64_t &slope) {
+  using namespace ptx;
+  if constexpr (ACT == kActGelu || ACT == kActNone) {
+    float a, b, sa, sb;
+    f2_split(z, a, b);
+    a = act<ACT, SLOPE>(a, sa);
+    b = act<ACT, SLOPE>(b, sb);
+    if constexpr (SLOPE) slope = f2(sa, sb);
+    return f2(a, b);
+  } else {
+    constexpr float kLog2e = 1.44269504f, kA = 0.79788456f, kB = 0.044715f;
+    const uint64_t one = f2(1.f, 1.f);
+    uint64_t z2 = 0, arg;
+    if constexpr (ACT == kActSilu) {
+      arg = mul2(z, f2(-kLog2e, -kLog2e));
+    } else {
+      constexpr float c3 = -2.f * kA * kB * kLog2e, c1 = -2.f * kA * kLog2e;
+      z2 = mul2(z, z);
+      arg = mul2(z, fma2(z2, f2(c3, c3), f2(c1, c1)));
+    }
+    float a, b;
+    f2_split(arg, a, b);
+    f2_split(add2(f2(ex2(a), ex2(b)), one), a, b);
+    const uint64_t s = f2(rcp(a), rcp(b)), y = mul2(z, s);
+    if constexpr (SLOPE) {
+      const uint64_t t = mul2(y, sub2(one, s));
+      if constexpr (ACT == kActSilu) {
+        slope = add2(t, s);
+      } else {
+        constexpr float d2 = 6.f * kA * kB, d0 = 2.f * kA;
+        slope = fma2(t, fma2(z2, f2(d2, d2), f2(d0, d0)), s);
+      }
+    }
+    return y;
+  }
+}
+
 // v = act(v) for M values; with SLOPE sl = act'(v).
 template <int ACT, bool SLOPE, int M>
 __device__ __forceinline__ void act_of(float (&v)[M], float (&sl)[M]) {
+  if constexpr (M % 2 == 0) {
 #pragma unroll
-  for (int i = 0; i < M; ++i) v[i] = act<ACT, SLOPE>(v[i], sl[i]);
+    for (int i = 0; i < M; i += 2) {
+      uint64_t s = 0;
+      const uint64_t y = act2<ACT, SLOPE>(ptx::f2(v[i], v[i + 1]), s);
+      ptx::f2_split(y, v[i], v[i + 1]);
+      if constexpr (SLOPE) ptx::f2_split(s, sl[i], sl[i + 1]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < M; ++i) v[i] = act<ACT, SLOPE>(v[i], sl[i]);
+  }
 }
 template <bool SLOPE, int M>
 __device__ __forceinline__ void act_all(int32_t which, float (&v)[M], float (&sl)[M]) {

@@ -18,10 +18,11 @@
 //   Tangents: a tile holds 128 tokens. Each CTA's A rows are 64 tokens of x, then
 //   the same 64 of tx, so primal and tangent share every weight tile, the product
 //   shape and the copies stay those of the primal alone, and both halves of a
-//   token's result land in one CTA. The tangent's factor act'(z) crosses from the
-//   warps that hold the primal rows to those that hold the tangent rows through
-//   4 KiB of shared memory per pair of warps, 32 columns at a time. (Two products
-//   of N = 128 per weight tile would keep both in one thread, but copy 25% more.)
+//   token's result land in one CTA. z crosses from the warps that hold the primal
+//   rows to those that hold the tangent rows through 4 KiB of shared memory per pair
+//   of warps, 32 columns at a time; these take act'(z) themselves, so that both
+//   kinds of warp have about the same to do. (Two products of N = 128 per weight
+//   tile would keep both in one thread, but copy 25% more.)
 //   warp 0      TMA producer (both CTAs)
 //   warp 1      MMA issuer (the leader's)
 //   warps 2-9   epilogue: two warps per 32 rows, 128 columns each, so that an
@@ -262,6 +263,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_sm100_kernel(const __grid_
     }
   } else {
     // ---------------------------------------------------------- epilogue (both CTAs)
+    // Kept as loops of 32 columns: unrolled over a whole tile, the activations' code
+    // outgrows the instruction cache (see the note at the top).
     const int q = warp & 3, half = (warp - 2) >> 2;
     const int op = JVP ? q >> 1 : 0;  // 1: this warp's rows are tangents
     const uint32_t lane_taddr = tmem + (uint32_t(32 * q) << 16) + uint32_t(128 * half);
@@ -270,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_sm100_kernel(const __grid_
     const uint32_t ex = sbase + L::OFF_EX + ex_id * EX_BYTES;
     const uint32_t acc_empty_leader = pair::at_rank(bars + L::ACC_EMPTY, 0);
     const CUtensorMap *om = op ? &p.tm_y2 : &p.tm_y;
-    const uint16_t *res = static_cast<const uint16_t *>(op ? p.tres : p.res);
+    const uint16_t *res = EPI && p.splits == 1 ? static_cast<const uint16_t *>(op ? p.tres : p.res) : nullptr;
     const int64_t ld_res = op ? p.ld_tres : p.ld_res;
     uint32_t count = 0, exchanged = 0;
     bool ok = true;
@@ -279,50 +282,58 @@ __global__ void __launch_bounds__(kThreads, 1) linear_sm100_kernel(const __grid_
       const int32_t row0 = (t / p.n_tiles) * TM + int32_t(rank) * (TM / 2) + 32 * (JVP ? q & 1 : q);
       const int32_t n0 = (t % p.n_tiles) * TN + 128 * half;
       const uint32_t buf = count & 1u, use = count >> 1;
+      const bool rows_in = row0 < p.M;
+      // residual, 64 columns ahead, coalesced: eight lanes a row, four rows at a time
+      uint4 rv[8];
+      auto fetch_residual = [&](int32_t col0) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int32_t r = row0 + 4 * i + (lane >> 3), cc = col0 + 8 * (lane & 7);
+          rv[i] = make_uint4(0, 0, 0, 0);
+          if (r < p.M && cc < p.N) rv[i] = __ldcs(reinterpret_cast<const uint4 *>(res + r * ld_res + cc));
+        }
+      };
+      if (EPI && res) fetch_residual(n0);
       if (!wait(bars + L::ACC_FULL + 8 * buf, use & 1u, kSiteAccFull)) break;
       tc_fence_after();
-      const bool rows_in = row0 < p.M;
       uint32_t scale_word = 0;
 #pragma unroll 1
-      for (int c = 0; ok && c < 2; ++c) {
-        uint32_t acc[2][32];
-        tmem_ld32x2(lane_taddr + buf * TN + 64 * c, lane_taddr + buf * TN + 64 * c + 32, acc[0], acc[1]);
-        if (c == 1) {
+      for (int c = 0; c < 4; ++c) {
+        uint32_t acc[32];
+        tmem_ld32(lane_taddr + buf * TN + 32 * c, acc);
+        if (c == 3) {
           tc_fence_before();
           __syncwarp();
           if (lane == 0) pair::arrive_remote(acc_empty_leader + 8 * buf);
         }
-        const int32_t col0 = n0 + 64 * c;
-        if (!rows_in || col0 >= p.N) continue;
-        if (p.splits > 1) {  // fp32 partial tiles, 32 columns at a time
+        const int32_t cs = n0 + 32 * c;
+        // (the second half of a 64-column store goes on past the last column)
+        if (!rows_in || n0 + 64 * (c >> 1) >= p.N) continue;
+        if (p.splits > 1) {  // fp32 partial tiles
+          if (cs >= p.N) continue;
+          if (lane == 0) pair::store_wait_read<0>();
+          __syncwarp();
 #pragma unroll
-          for (int s = 0; s < 2; ++s) {
-            if (col0 + 32 * s >= p.N) continue;
-            if (lane == 0) pair::store_wait_read<0>();
-            __syncwarp();
-#pragma unroll
-            for (int g = 0; g < 8; ++g)
-              sts128(swz(sbuf, lane, g), acc[s][4 * g], acc[s][4 * g + 1], acc[s][4 * g + 2], acc[s][4 * g + 3]);
-            fence_async_smem_then_store(&p.tm_part, sbuf, col0 + 32 * s,
-                                        (split * (JVP ? 2 : 1) + op) * p.part_rows + row0, lane);
-          }
+          for (int g = 0; g < 8; ++g)
+            sts128(swz(sbuf, lane, g), acc[4 * g], acc[4 * g + 1], acc[4 * g + 2], acc[4 * g + 3]);
+          fence_async_smem_then_store(&p.tm_part, sbuf, cs, (split * (JVP ? 2 : 1) + op) * p.part_rows + row0, lane);
           continue;
         }
-        uint4 rv[8];
-        if (EPI && res) {  // coalesced: eight lanes a row, four rows at a time
+        if ((c & 1) == 0) {  // a new 64-column staging tile
+          if (lane == 0) pair::store_wait_read<0>();
+          __syncwarp();
+          if (EPI && res) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int32_t r = row0 + 4 * i + (lane >> 3), cc = col0 + 8 * (lane & 7);
-            rv[i] = make_uint4(0, 0, 0, 0);
-            if (r < p.M && cc < p.N) rv[i] = __ldcs(reinterpret_cast<const uint4 *>(res + r * ld_res + cc));
+            for (int i = 0; i < 8; ++i)
+              sts128(swz(sbuf, 4 * i + (lane >> 3), lane & 7), rv[i].x, rv[i].y, rv[i].z, rv[i].w);
+            __syncwarp();
+            if (c == 0) fetch_residual(n0 + 64);
           }
         }
+        float v[32];
 #pragma unroll
-        for (int s = 0; EPI && s < 2; ++s) {
-          float v[32];
-#pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(acc[s][i]);
-          const int32_t cs = col0 + 32 * s;
+        for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(acc[i]);
+        if (EPI) {
           if (op == 0) {
             if (p.bias) {
               const uint4 *bp = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.bias) + cs);
@@ -338,25 +349,54 @@ __global__ void __launch_bounds__(kThreads, 1) linear_sm100_kernel(const __grid_
                 }
               }
             }
-            if (p.codes && cs < 32 * p.nb) {
-              uint32_t m = 0;
+          }
+          if constexpr (JVP) {  // z crosses to the tangents' warp, which takes act'(z) itself
+            if (p.act != lin::kActNone) {
+              if (!wait(op ? bars + L::EX_FULL + 8 * ex_id : bars + L::EX_EMPTY + 8 * ex_id,
+                        (exchanged & 1u) ^ uint32_t(op ^ 1), op ? kSiteExFull : kSiteExEmpty)) {
+                ok = false;
+                break;
+              }
+              if (op == 0) {
 #pragma unroll
-              for (int i = 0; i < 32; ++i) m = max(m, ck::mag_bits(v[i]));
-              const uint32_t sc = ck::scale_of(m);
-              scale_word |= sc << (8 * (2 * c + s));
-              uint32_t w[8];
-              if (sc == 255u) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) w[i] = 0;
+                for (int g = 0; g < 8; ++g)
+                  sts128(swz(ex, lane, g), __float_as_uint(v[4 * g]), __float_as_uint(v[4 * g + 1]),
+                         __float_as_uint(v[4 * g + 2]), __float_as_uint(v[4 * g + 3]));
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bars + L::EX_FULL + 8 * ex_id);
               } else {
-                float f[32];
+                float z[32], sl[32];
 #pragma unroll
-                for (int i = 0; i < 32; ++i) f[i] = v[i];
-                ck::saturate(f, sc);
+                for (int g = 0; g < 8; ++g) {
+                  const uint4 w = lds128(swz(ex, lane, g));
+                  z[4 * g] = __uint_as_float(w.x);
+                  z[4 * g + 1] = __uint_as_float(w.y);
+                  z[4 * g + 2] = __uint_as_float(w.z);
+                  z[4 * g + 3] = __uint_as_float(w.w);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bars + L::EX_EMPTY + 8 * ex_id);
+                lin::act_all<true>(p.act, z, sl);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] *= sl[i];
+              }
+              ++exchanged;
+            }
+          }
+          if (op == 0) {
+            if (p.codes && cs < 32 * p.nb) {
+              const uint32_t sc = ck::scale_of(__float_as_uint(ck::max_mag(v)));
+              scale_word |= sc << (8 * c);
+              uint32_t w[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) w[i] = 0;
+              if (sc < ck::kMaxScale) {
                 const float up = ck::up_of(sc);
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                  w[i] = ck::pack_codes4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3], up);
+                  w[i] = ck::pack_codes4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3], up);
+              } else if (sc == ck::kMaxScale) {
+                ck::pack_saturated(v, w);
               }
               if (row0 + lane < p.M) {
                 uint4 *dst = reinterpret_cast<uint4 *>(p.codes + size_t(row0 + lane) * (32 * size_t(p.nb)) + cs);
@@ -364,62 +404,16 @@ __global__ void __launch_bounds__(kThreads, 1) linear_sm100_kernel(const __grid_
                 dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
               }
             }
-          }
-          if (p.act != lin::kActNone) {
-            if constexpr (JVP) {
-              if (op == 0) {
-                float sl[32];
-                lin::act_all<true>(p.act, v, sl);
-                if (!wait(bars + L::EX_EMPTY + 8 * ex_id, (exchanged & 1u) ^ 1u, kSiteExEmpty)) {
-                  ok = false;
-                  break;
-                }
-#pragma unroll
-                for (int g = 0; g < 8; ++g)
-                  sts128(swz(ex, lane, g), __float_as_uint(sl[4 * g]), __float_as_uint(sl[4 * g + 1]),
-                         __float_as_uint(sl[4 * g + 2]), __float_as_uint(sl[4 * g + 3]));
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bars + L::EX_FULL + 8 * ex_id);
-              } else {
-                if (!wait(bars + L::EX_FULL + 8 * ex_id, exchanged & 1u, kSiteExFull)) {
-                  ok = false;
-                  break;
-                }
-#pragma unroll
-                for (int g = 0; g < 8; ++g) {
-                  const uint4 w = lds128(swz(ex, lane, g));
-                  v[4 * g] *= __uint_as_float(w.x);
-                  v[4 * g + 1] *= __uint_as_float(w.y);
-                  v[4 * g + 2] *= __uint_as_float(w.z);
-                  v[4 * g + 3] *= __uint_as_float(w.w);
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bars + L::EX_EMPTY + 8 * ex_id);
-              }
-              ++exchanged;
-            } else {
+            if (p.act != lin::kActNone) {
               float sl[32];
               lin::act_all<false>(p.act, v, sl);
             }
           }
-#pragma unroll
-          for (int i = 0; i < 32; ++i) acc[s][i] = __float_as_uint(v[i]);
-        }
-        if (!ok) break;
-        if (lane == 0) pair::store_wait_read<0>();
-        __syncwarp();
-        if (EPI && res) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            sts128(swz(sbuf, 4 * i + (lane >> 3), lane & 7), rv[i].x, rv[i].y, rv[i].z, rv[i].w);
-          __syncwarp();
         }
 #pragma unroll
-        for (int g = 0; g < 8; ++g) {
-          float f[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(acc[g >> 2][8 * (g & 3) + e]);
-          const uint32_t a = swz(sbuf, lane, g);
+        for (int g = 0; g < 4; ++g) {
+          const uint32_t a = swz(sbuf, lane, 4 * (c & 1) + g);
+          float *f = v + 8 * g;
           if (EPI && res) {
             const uint4 w = lds128(a);
             const uint32_t w4[4] = {w.x, w.y, w.z, w.w};
@@ -431,9 +425,9 @@ __global__ void __launch_bounds__(kThreads, 1) linear_sm100_kernel(const __grid_
           }
           sts128(a, pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
         }
-        fence_async_smem_then_store(om, sbuf, col0, row0, lane);
+        if (c & 1) fence_async_smem_then_store(om, sbuf, cs - 32, row0, lane);
       }
-      if (EPI && p.codes && p.splits == 1 && op == 0 && rows_in && row0 + lane < p.M && n0 < 32 * p.nb)
+      if (EPI && ok && p.codes && p.splits == 1 && op == 0 && rows_in && row0 + lane < p.M && n0 < 32 * p.nb)
         *reinterpret_cast<uint32_t *>(p.scales + size_t(row0 + lane) * p.ns + n0 / 32) = scale_word;
     }
     if (lane == 0) pair::store_wait<0>();
@@ -628,9 +622,9 @@ __global__ void __launch_bounds__(256) linear_rows_kernel(const LinearParams p) 
 // bias, in one pass over dy. A warp's lanes hold 256 neighbouring columns, eight a
 // lane, and walk over the rows of their block's chunk; the eight warps' sums meet in
 // shared memory. ACT none: only the sums, dz is dy.
-constexpr int kDzUnroll = 4;
+constexpr int kDzUnroll = 2;
 template <bool ACT>
-__global__ void __launch_bounds__(256) linear_dz_kernel(const LinearDzParams p) {
+__global__ void __launch_bounds__(256, 4) linear_dz_kernel(const LinearDzParams p) {
   __shared__ float red[8][256];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int32_t col = int32_t(blockIdx.x) * 256 + 8 * lane;

@@ -58,18 +58,35 @@ __device__ __forceinline__ void cos_sin(double pos, double freq, float mscale, f
   c = ((quadrant + 1) & 2 ? -b : b) * mscale;
 }
 
-template <typename I>
+// A thread owns V neighbouring pairs (V = 4: 16-byte stores) and walks over the
+// positions, so frequencies and axes stay in registers.
+template <typename I, int V>
 __global__ void __launch_bounds__(256) rope_table_kernel(const RopeTableParams p) {
-  const int64_t total = p.N * p.P, step = int64_t(gridDim.x) * 256;
-  for (int64_t g = int64_t(blockIdx.x) * 256 + threadIdx.x; g < total; g += step) {
-    const int64_t n = total < (int64_t(1) << 32) ? int64_t(uint32_t(g) / uint32_t(p.P)) : g / p.P;
-    const int32_t i = int32_t(g - n * p.P);
-    const int32_t ax = p.axis ? __ldg(p.axis + i) : 0;
-    float c = __int_as_float(0x7FC00000), s = c;  // an axis that pos does not have: NaN
-    if (ax >= 0 && ax < p.A)
-      cos_sin(double(__ldg(static_cast<const I *>(p.pos) + n * p.A + ax)), __ldg(p.freq + i), p.mscale, c, s);
-    p.cos[g] = c;
-    p.sin[g] = s;
+  const int32_t cols = p.P / V;  // threads across a row of pairs
+  const int64_t id = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t row0 = id / cols, step = int64_t(gridDim.x) * 256 / cols;  // a whole number of rows
+  const int32_t i = int32_t(id - row0 * cols) * V;
+  double freq[V];
+  int32_t ax[V];
+#pragma unroll
+  for (int e = 0; e < V; ++e) {
+    freq[e] = __ldg(p.freq + i + e);
+    ax[e] = p.axis ? __ldg(p.axis + i + e) : 0;
+    if (ax[e] < 0 || ax[e] >= p.A) freq[e] = __longlong_as_double(0x7FF8000000000000ll), ax[e] = 0;  // NaN
+  }
+  for (int64_t n = row0; n < p.N; n += step) {
+    float c[V], s[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e)
+      cos_sin(double(__ldg(static_cast<const I *>(p.pos) + n * p.A + ax[e])), freq[e], p.mscale, c[e], s[e]);
+    const int64_t at = n * p.P + i;
+    if constexpr (V == 4) {
+      __stcs(reinterpret_cast<float4 *>(p.cos + at), make_float4(c[0], c[1], c[2], c[3]));
+      __stcs(reinterpret_cast<float4 *>(p.sin + at), make_float4(s[0], s[1], s[2], s[3]));
+    } else {
+      p.cos[at] = c[0];
+      p.sin[at] = s[0];
+    }
   }
 }
 
@@ -167,17 +184,19 @@ __device__ __forceinline__ void load_gain(const float *g, const QkRopeParams &p,
   load4(src + 4, o + 4);
 }
 
-// Forward. Grid: x token groups of T * U, y the tensor (q, k, v).
+// Forward. Grid: token groups of T * U, and for each the tensors q, k, v next to each
+// other, so that v's copies fill the memory's time while q and k are computed.
 template <typename T, bool TAN, int U>
 __global__ void __launch_bounds__(1024) qk_rope_fwd_kernel(const QkRopeParams p) {
   extern __shared__ float red[];
-  const int which = blockIdx.y;
+  const int which = int(blockIdx.x) % p.tensors;
+  const int32_t group = int32_t(blockIdx.x) / p.tensors;
   const int32_t H = which == 0 ? p.Hq : p.Hk, D = p.D;
   const Lane l = lane_of(H, D);
   const int32_t rows = p.B * p.N;
   const T *x = static_cast<const T *>(p.x[which]), *tx = static_cast<const T *>(p.tx[which]);
   T *y = static_cast<T *>(p.y[which]), *ty = static_cast<T *>(p.ty[which]);
-  const int64_t tok0 = int64_t(blockIdx.x) * l.T * U + l.t;
+  const int64_t tok0 = int64_t(group) * l.T * U + l.t;
 
   v8::Raw<T> raw[U], traw[U];
   bool on[U];
@@ -247,14 +266,15 @@ __global__ void __launch_bounds__(1024) qk_rope_fwd_kernel(const QkRopeParams p)
   }
 }
 
-// Backward. Grid: x blocks that walk over the token groups (so the gains' gradient
-// stays in registers for a block's whole run), y the tensor. Block (x, which) leaves
-// its partial dg in p.partial[which][x][p.gain_len[which]].
+// Backward. p.blocks blocks for each tensor (q, k, v next to each other) walk over the
+// token groups, so the gains' gradient stays in registers for a block's whole run; block
+// i leaves its partial dg in p.partial[which][i].
 // CK: x comes from an 8-bit checkpoint.
 template <typename T, bool CK, int U>
 __global__ void __launch_bounds__(1024) qk_rope_bwd_kernel(const QkRopeParams p) {
   extern __shared__ float red[];
-  const int which = blockIdx.y;
+  const int which = int(blockIdx.x) % p.tensors;
+  const int32_t group = int32_t(blockIdx.x) / p.tensors;
   const int32_t H = which == 0 ? p.Hq : p.Hk, D = p.D;
   const Lane l = lane_of(H, D);
   const int32_t rows = p.B * p.N;
@@ -270,7 +290,7 @@ __global__ void __launch_bounds__(1024) qk_rope_bwd_kernel(const QkRopeParams p)
   if (normed && l.on) load_gain(p.g[which], p, l, g);
   const float inv_len = 1.f / float(p.norm == kNormHead ? D : H * D);
 
-  for (int64_t base = int64_t(blockIdx.x) * l.T * U; base < rows; base += int64_t(gridDim.x) * l.T * U) {
+  for (int64_t base = int64_t(group) * l.T * U; base < rows; base += int64_t(p.blocks) * l.T * U) {
     v8::Raw<T> raw[U], xr[U];
     uint2 cw[U];
     uint32_t sc[U];
@@ -352,7 +372,7 @@ __global__ void __launch_bounds__(1024) qk_rope_bwd_kernel(const QkRopeParams p)
   }
   __syncthreads();
   const int32_t len = p.gain_full ? H * D : D, width = H * D;
-  float *part = p.partial[which] + size_t(blockIdx.x) * len;
+  float *part = p.partial[which] + size_t(group) * len;
   for (int32_t c = int32_t(threadIdx.x); c < len; c += int32_t(blockDim.x)) {
     float s = 0.f;
     for (int32_t t = 0; t < l.T; ++t)
@@ -395,7 +415,7 @@ cudaError_t launch_fwd(const QkRopeParams &p, cudaStream_t stream) {
   const int32_t U = tan ? 2 : 4;
   const int32_t Vmax = (p.Hq > p.Hk ? p.Hq : p.Hk) * p.D / 8;
   const int32_t per = threads / Vmax * U;  // the narrower tensor takes more tokens a block
-  const dim3 grid(unsigned((int64_t(p.B) * p.N + per - 1) / per), p.x[2] ? 3 : 2);
+  const unsigned grid = unsigned((int64_t(p.B) * p.N + per - 1) / per) * unsigned(p.tensors);
   const size_t smem = p.norm == kNormToken ? size_t(threads) / (p.D / 8) * (tan ? 2 : 1) * sizeof(float) : 0;
   if (tan)
     qk_rope_fwd_kernel<T, true, 2><<<grid, threads, smem, stream>>>(p);
@@ -407,7 +427,7 @@ cudaError_t launch_fwd(const QkRopeParams &p, cudaStream_t stream) {
 template <typename T>
 cudaError_t launch_bwd(const QkRopeParams &p, cudaStream_t stream) {
   const int32_t threads = threads_for(p);
-  const dim3 grid(unsigned(p.blocks), p.dy[2] ? 3 : 2);
+  const unsigned grid = unsigned(p.blocks * p.tensors);
   const size_t smem = p.norm == kNormNone ? 0 : size_t(threads) * 8 * sizeof(float);
   if (p.x_scales[0])
     qk_rope_bwd_kernel<T, true, 2><<<grid, threads, smem, stream>>>(p);
@@ -422,14 +442,23 @@ cudaError_t launch_bwd(const QkRopeParams &p, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t launch_rope_table(const RopeTableParams &p, bool pos64, cudaStream_t stream) {
-  const int64_t blocks = (p.N * p.P + 255) / 256;
-  const unsigned grid = unsigned(blocks < 148 * 64 ? blocks : 148 * 64);
-  if (pos64)
-    rope_table_kernel<int64_t><<<grid, 256, 0, stream>>>(p);
-  else
-    rope_table_kernel<int32_t><<<grid, 256, 0, stream>>>(p);
+namespace {
+// The grid's threads are a whole number of rows: a multiple of `cols` blocks.
+template <typename I, int V>
+cudaError_t launch_table(const RopeTableParams &p, cudaStream_t stream) {
+  const int64_t cols = p.P / V, most = 148 * 32;
+  const int64_t want = (p.N * cols + 255) / 256;
+  int64_t blocks = want < most ? want : most;
+  blocks = (blocks + cols - 1) / cols * cols;
+  rope_table_kernel<I, V><<<unsigned(blocks), 256, 0, stream>>>(p);
   return cudaGetLastError();
+}
+}  // namespace
+
+cudaError_t launch_rope_table(const RopeTableParams &p, bool pos64, cudaStream_t stream) {
+  const bool vec = p.P % 4 == 0 && ((reinterpret_cast<uintptr_t>(p.cos) | reinterpret_cast<uintptr_t>(p.sin)) & 15u) == 0;
+  if (vec) return pos64 ? launch_table<int64_t, 4>(p, stream) : launch_table<int32_t, 4>(p, stream);
+  return pos64 ? launch_table<int64_t, 1>(p, stream) : launch_table<int32_t, 1>(p, stream);
 }
 
 // Blocks of the backward a tensor: fixed by the sizes alone, so that the order of
