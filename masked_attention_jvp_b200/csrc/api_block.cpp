@@ -161,7 +161,6 @@ caj_status caj_qk_rope_fwd(const void *xq, const void *xk, const void *xv, const
     p.ld[i] = ld[i];
     p.tld[i] = tld[i];
   }
-  p.tensors = xv ? 3 : 2;
   st = caj::check_device();
   if (st != CAJ_OK) return st;
   return done(caj::launch_qk_rope_fwd(p, shape->dtype == CAJ_DTYPE_BF16, static_cast<cudaStream_t>(stream)));
@@ -219,7 +218,6 @@ caj_status caj_qk_rope_bwd(const void *dq, const void *dk, const void *dv, const
   if (need && (!workspace || !aligned_to(workspace, 16) || workspace_bytes < need)) return CAJ_ERR_INVALID_ARG;
   st = caj::check_device();
   if (st != CAJ_OK) return st;
-  p.tensors = dv ? 3 : 2;
   p.blocks = caj::qk_rope_bwd_blocks(shape->B, shape->N, shape->Hq, shape->Hk, shape->D);
   if (normed) {
     p.partial[0] = static_cast<float *>(workspace);

@@ -12,11 +12,13 @@
 //
 // Everything here moves data: each element is read and written once, in 16-byte
 // accesses, with fp32 arithmetic between (sums of squares, means and the gains'
-// gradients too). A thread owns eight channels of one head for a run of tokens, so
-// gains stay in registers; D/8 neighbouring lanes hold a head and reduce by
+// gradients too), packed two to an instruction where that applies. A thread owns the
+// same eight channels of q, k and v; D/8 neighbouring lanes hold a head and reduce by
 // shuffles. Pairs of the half layout (channels i and i + P) sit P/8 lanes apart and
 // meet by a shuffle; interleaved pairs (2i, 2i + 1) are in one thread.
 #include <cuda_runtime.h>
+
+#include <atomic>
 
 #include "ckpt8.cuh"
 #include "kernels.h"
@@ -91,293 +93,458 @@ __global__ void __launch_bounds__(256) rope_table_kernel(const RopeTableParams p
 }
 
 // ------------------------------------------------------------ norm + rotation
-struct Lane {       // a thread's place in its tensor
-  int32_t V, T;     // 8-channel vectors of a token, tokens a block takes at a time
-  int32_t t, vec;   // this thread's token among T, and its vector
-  bool on;
-  int32_t head, d0;
+using ptx::add2;
+using ptx::f2;
+using ptx::f2_split;
+using ptx::fma2;
+using ptx::mul2;
+
+struct Lane {        // a thread's place: eight channels of one head, one token of T
+  int32_t V, T;      // vectors of a token (of the wider tensor), tokens of a block
+  int32_t t, vec, head, d0;
 };
-__device__ __forceinline__ Lane lane_of(int32_t H, int32_t D) {
+__device__ __forceinline__ Lane lane_of(const QkRopeParams &p) {
   Lane l;
-  l.V = H * D / 8;
+  l.V = max(p.Hq, p.Hk) * p.D / 8;
   l.T = int32_t(blockDim.x) / l.V;
   l.t = int32_t(threadIdx.x) / l.V;
   l.vec = int32_t(threadIdx.x) - l.t * l.V;
-  l.on = l.t < l.T;
-  l.head = 8 * l.vec / D;
-  l.d0 = 8 * l.vec - l.head * D;
+  l.head = 8 * l.vec / p.D;
+  l.d0 = 8 * l.vec - l.head * p.D;
   return l;
 }
 
-// Cosines and sines for a thread's eight channels: interleaved four pairs (repeated
-// for nothing: only the first four are read), half eight.
-struct Angle {
-  float c[8], s[8];
-};
-__device__ __forceinline__ void load4(const float *p, float *f) {
-  const float4 a = __ldg(reinterpret_cast<const float4 *>(p));
-  f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-}
-__device__ __forceinline__ void load_angle(const QkRopeParams &p, int32_t n, int32_t d0, Angle &a) {
-  const size_t row = size_t(n) * p.P;
-  if (p.half) {
-    const int32_t i = d0 < p.P ? d0 : d0 - p.P;
-    load4(p.cos + row + i, a.c);
-    load4(p.cos + row + i + 4, a.c + 4);
-    load4(p.sin + row + i, a.s);
-    load4(p.sin + row + i + 4, a.s + 4);
-  } else {
-    load4(p.cos + row + d0 / 2, a.c);
-    load4(p.sin + row + d0 / 2, a.s);
-  }
-}
-// Rotates a thread's eight channels; `sign` -1 turns back. Every lane of the warp
-// comes here (the half layout shuffles), `turns` says whether its channels rotate.
-__device__ __forceinline__ void rotate(float (&x)[8], const Angle &a, bool half, bool turns, bool first,
-                                       int32_t hop, float sign) {
-  if (half) {
-    const int src = int(threadIdx.x & 31) + (turns ? (first ? hop : -hop) : 0);
-    const float sg = first ? -sign : sign;
+__device__ __forceinline__ void pairs_of(const float (&f)[8], uint64_t (&o)[4]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float other = __shfl_sync(0xFFFFFFFFu, x[i], src);
-      if (turns) x[i] = fmaf(x[i], a.c[i], sg * a.s[i] * other);
-    }
-  } else if (turns) {
+  for (int i = 0; i < 4; ++i) o[i] = f2(f[2 * i], f[2 * i + 1]);
+}
+__device__ __forceinline__ void singles_of(const uint64_t (&p)[4], float (&o)[8]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float u = x[2 * i], w = x[2 * i + 1], s = sign * a.s[i];
-      x[2 * i] = fmaf(u, a.c[i], -w * s);
-      x[2 * i + 1] = fmaf(u, s, w * a.c[i]);
-    }
-  }
+  for (int i = 0; i < 4; ++i) f2_split(p[i], o[2 * i], o[2 * i + 1]);
+}
+template <typename T>
+__device__ __forceinline__ void unpack(const v8::Raw<T> &r, uint64_t (&o)[4]) {
+  float f[8];
+  v8::unpack(r, f);
+  pairs_of(f, o);
+}
+template <typename T>
+__device__ __forceinline__ v8::Raw<T> pack(const uint64_t (&x)[4]) {
+  float f[8];
+  singles_of(x, f);
+  v8::Raw<T> r;
+  v8::pack(f, r);
+  return r;
+}
+__device__ __forceinline__ void load_pairs(const float *g, uint64_t (&o)[4]) {
+  const float4 a = __ldg(reinterpret_cast<const float4 *>(g)), b = __ldg(reinterpret_cast<const float4 *>(g) + 1);
+  o[0] = f2(a.x, a.y);
+  o[1] = f2(a.z, a.w);
+  o[2] = f2(b.x, b.y);
+  o[3] = f2(b.z, b.w);
+}
+// sum of a * b over a thread's eight channels
+__device__ __forceinline__ float dot(const uint64_t (&a)[4], const uint64_t (&b)[4]) {
+  uint64_t s = mul2(a[0], b[0]);
+#pragma unroll
+  for (int i = 1; i < 4; ++i) s = fma2(a[i], b[i], s);
+  float x, y;
+  f2_split(s, x, y);
+  return x + y;
 }
 
-// Sums of a thread's M values over the norm's group: the head's lanes, or all
-// vectors of the token through shared memory (`red`: [T][heads][M] floats).
+// A thread's rotation. Interleaved: (u, w) -> (u, w) (c, c) + (w, u) (-s, s). Half: the
+// partner's channels are `hop` lanes away, x -> x c + partner * (-s in the first half,
+// s in the second). BACK turns the other way. Channels past 2 P pass.
+template <bool HALF>
+struct Turn {
+  uint64_t c[4], s[4];
+  int hop;
+  bool on;
+  // Slots of 16 bytes that a thread's cosines and sines take in the tables.
+  static constexpr int kSlots = HALF ? 4 : 2;
+  // The table element of the thread's first angle at position n.
+  __device__ __forceinline__ static size_t place(const QkRopeParams &p, const Lane &l, int32_t n) {
+    if constexpr (HALF) return size_t(n) * p.P + (l.d0 < p.P ? l.d0 : l.d0 - p.P);
+    return size_t(n) * p.P + l.d0 / 2;
+  }
+  // raw: cosines, then sines. BACK turns the other way; lanes that do not turn get 1 and 0.
+  template <bool BACK>
+  __device__ __forceinline__ void set(const QkRopeParams &p, const Lane &l, const float4 (&raw)[kSlots]) {
+    on = l.d0 < 2 * p.P;
+    if constexpr (HALF) {
+      const bool first = l.d0 < p.P;
+      hop = on ? (first ? p.P / 8 : -(p.P / 8)) : 0;
+      const float sg = first != BACK ? -1.f : 1.f;
+      const uint64_t sign = f2(sg, sg);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float4 cc = raw[i], ss = raw[2 + i];
+        c[2 * i] = on ? f2(cc.x, cc.y) : f2(1.f, 1.f);
+        c[2 * i + 1] = on ? f2(cc.z, cc.w) : f2(1.f, 1.f);
+        s[2 * i] = on ? mul2(f2(ss.x, ss.y), sign) : 0;
+        s[2 * i + 1] = on ? mul2(f2(ss.z, ss.w), sign) : 0;
+      }
+    } else {
+      const float4 cc = raw[0];
+      const float4 ss = BACK ? make_float4(-raw[1].x, -raw[1].y, -raw[1].z, -raw[1].w) : raw[1];
+      c[0] = f2(cc.x, cc.x);
+      c[1] = f2(cc.y, cc.y);
+      c[2] = f2(cc.z, cc.z);
+      c[3] = f2(cc.w, cc.w);
+      s[0] = f2(-ss.x, ss.x);
+      s[1] = f2(-ss.y, ss.y);
+      s[2] = f2(-ss.z, ss.z);
+      s[3] = f2(-ss.w, ss.w);
+    }
+  }
+  // Every lane of the warp comes here (the half layout shuffles).
+  __device__ __forceinline__ void apply(uint64_t (&x)[4]) const {
+    if constexpr (HALF) {
+      const int src = int(threadIdx.x & 31) + hop;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float u, w;
+        f2_split(x[i], u, w);
+        const uint64_t other = f2(__shfl_sync(0xFFFFFFFFu, u, src), __shfl_sync(0xFFFFFFFFu, w, src));
+        x[i] = fma2(x[i], c[i], mul2(other, s[i]));
+      }
+    } else if (on) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float u, w;
+        f2_split(x[i], u, w);
+        x[i] = fma2(x[i], c[i], mul2(f2(w, u), s[i]));
+      }
+    }
+  }
+};
+
+// Sums of a thread's M values over the norm's group: the head's lanes, or all heads of
+// the token through shared memory (`red`: [T][heads][M] floats). Values whose tensor has
+// fewer heads are zero there.
 template <int M>
-__device__ __forceinline__ void group_sums(float (&v)[M], const Lane &l, int32_t norm, int32_t D, int32_t H,
-                                           float *red) {
-  for (int o = D / 16; o > 0; o >>= 1) {
+__device__ __forceinline__ void group_sums(float (&v)[M], const Lane &l, const QkRopeParams &p, float *red) {
+  for (int o = p.D / 16; o > 0; o >>= 1) {
 #pragma unroll
     for (int i = 0; i < M; ++i) v[i] += __shfl_xor_sync(0xFFFFFFFFu, v[i], o);
   }
-  if (norm != kNormToken) return;
+  if (p.norm != kNormToken) return;
+  const int32_t heads = max(p.Hq, p.Hk);
   __syncthreads();  // the sums of the round before have been read
-  if (l.on && l.d0 == 0) {
+  if (l.t < l.T && l.d0 == 0) {
 #pragma unroll
-    for (int i = 0; i < M; ++i) red[(l.t * H + l.head) * M + i] = v[i];
+    for (int i = 0; i < M; ++i) red[(l.t * heads + l.head) * M + i] = v[i];
   }
   __syncthreads();
-  if (!l.on) return;
+  if (l.t >= l.T) return;
 #pragma unroll
   for (int i = 0; i < M; ++i) v[i] = 0.f;
-  for (int h = 0; h < H; ++h) {
+  for (int h = 0; h < heads; ++h) {
 #pragma unroll
-    for (int i = 0; i < M; ++i) v[i] += red[(l.t * H + h) * M + i];
+    for (int i = 0; i < M; ++i) v[i] += red[(l.t * heads + h) * M + i];
   }
 }
 
-__device__ __forceinline__ void load_gain(const float *g, const QkRopeParams &p, const Lane &l, float (&o)[8]) {
-  const float *src = g + (p.gain_full ? 8 * l.vec : l.d0);
-  load4(src, o);
-  load4(src + 4, o + 4);
-}
-
-// Forward. Grid: token groups of T * U, and for each the tensors q, k, v next to each
-// other, so that v's copies fill the memory's time while q and k are computed.
-template <typename T, bool TAN, int U>
-__global__ void __launch_bounds__(1024) qk_rope_fwd_kernel(const QkRopeParams p) {
+// Forward: a thread has its eight channels of q, k and v of one token (and tangents), so
+// up to six 16-byte loads are in flight and the angles serve four vectors.
+// MAXT: 256 threads leave 80 registers each, 1024 (tokens wider than 2048 channels) 64.
+template <typename T, bool TAN, bool HALF, int MAXT>
+__global__ void __launch_bounds__(MAXT, MAXT == 256 ? 3 : 1) qk_rope_fwd_kernel(const QkRopeParams p) {
   extern __shared__ float red[];
-  const int which = int(blockIdx.x) % p.tensors;
-  const int32_t group = int32_t(blockIdx.x) / p.tensors;
-  const int32_t H = which == 0 ? p.Hq : p.Hk, D = p.D;
-  const Lane l = lane_of(H, D);
-  const int32_t rows = p.B * p.N;
-  const T *x = static_cast<const T *>(p.x[which]), *tx = static_cast<const T *>(p.tx[which]);
-  T *y = static_cast<T *>(p.y[which]), *ty = static_cast<T *>(p.ty[which]);
-  const int64_t tok0 = int64_t(group) * l.T * U + l.t;
-
-  v8::Raw<T> raw[U], traw[U];
-  bool on[U];
+  const Lane l = lane_of(p);
+  const int32_t tok = int32_t(min(int64_t(blockIdx.x) * l.T + l.t, int64_t(0x7FFFFFFF)));
+  const bool here = l.t < l.T && tok < p.B * p.N;
+  const int32_t b = here ? tok / p.N : 0, n = here ? tok - b * p.N : 0;
+  const int32_t heads[3] = {p.Hq, p.Hk, p.x[2] ? p.Hk : 0};
+  v8::Raw<T> raw[3], traw[3];
+  bool on[3];
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int64_t tok = tok0 + int64_t(u) * l.T;
-    on[u] = l.on && tok < rows;
-    raw[u] = v8::zero<T>();
-    traw[u] = v8::zero<T>();
-    if (on[u]) {
-      raw[u] = v8::load(x + tok * p.ld[which] + 8 * l.vec);
-      if (TAN) traw[u] = v8::load(tx + tok * p.tld[which] + 8 * l.vec);
+  for (int i = 0; i < 3; ++i) {
+    on[i] = here && l.head < heads[i];
+    raw[i] = v8::zero<T>();
+    if (TAN) traw[i] = v8::zero<T>();
+    if (on[i]) {
+      raw[i] = v8::load(static_cast<const T *>(p.x[i]) + tok * p.ld[i] + 8 * l.vec);
+      if (TAN) traw[i] = v8::load(static_cast<const T *>(p.tx[i]) + tok * p.tld[i] + 8 * l.vec);
     }
   }
-  float g[8];
-  const bool normed = which < 2 && p.norm != kNormNone;
-  if (normed && l.on) load_gain(p.g[which], p, l, g);
-  const bool turns = l.d0 < 2 * p.P, first = l.d0 < p.P;
+  Turn<HALF> turn;
+  float4 angles[Turn<HALF>::kSlots];
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int32_t tok = int32_t(tok0 + int64_t(u) * l.T);
-    const int32_t b = on[u] ? tok / p.N : 0, n = on[u] ? tok - b * p.N : 0;
-    const size_t out = ((size_t(b) * H + l.head) * p.N + n) * D + l.d0;
-    if (which == 2) {
-      if (on[u]) {
-        v8::store(y + out, raw[u]);
-        if (TAN) v8::store(ty + out, traw[u]);
-      }
-      continue;
+  for (int i = 0; i < Turn<HALF>::kSlots; ++i) angles[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (here && l.d0 < 2 * p.P) {
+    const size_t at = Turn<HALF>::place(p, l, n);
+#pragma unroll
+    for (int i = 0; i < Turn<HALF>::kSlots / 2; ++i) {
+      angles[i] = __ldg(reinterpret_cast<const float4 *>(p.cos + at) + i);
+      angles[Turn<HALF>::kSlots / 2 + i] = __ldg(reinterpret_cast<const float4 *>(p.sin + at) + i);
     }
-    float f[8], tf[8];
-    v8::unpack(raw[u], f);
-    if (TAN) v8::unpack(traw[u], tf);
-    if (normed) {
-      float sums[TAN ? 2 : 1];
-      sums[0] = 0.f;
-      if constexpr (TAN) sums[1] = 0.f;
+  }
+  turn.template set<false>(p, l, angles);
+  auto place = [&](int i) { return ((size_t(b) * heads[i] + l.head) * p.N + n) * p.D + l.d0; };
+  if (on[2]) {
+    v8::store(static_cast<T *>(p.y[2]) + place(2), raw[2]);
+    if (TAN) v8::store(static_cast<T *>(p.ty[2]) + place(2), traw[2]);
+  }
+  uint64_t x[2][4], tx[2][4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        sums[0] = fmaf(f[i], f[i], sums[0]);
-        if constexpr (TAN) sums[1] = fmaf(f[i], tf[i], sums[1]);
-      }
-      group_sums(sums, l, p.norm, D, H, red);
-      const float inv_len = 1.f / float(p.norm == kNormHead ? D : H * D);
-      const float inv = rsqrtf(fmaf(sums[0], inv_len, p.eps));
+  for (int i = 0; i < 2; ++i) {
+    unpack(raw[i], x[i]);
+    if (TAN) unpack(traw[i], tx[i]);
+  }
+  if (p.norm != kNormNone) {
+    float sums[TAN ? 4 : 2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      sums[i] = dot(x[i], x[i]);
+      if constexpr (TAN) sums[2 + i] = dot(x[i], tx[i]);
+    }
+    group_sums(sums, l, p, red);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float inv_len = 1.f / float(p.norm == kNormHead ? p.D : heads[i] * p.D);
+      const float inv = rsqrtf(fmaf(sums[i], inv_len, p.eps));
+      const uint64_t inv2 = f2(inv, inv);
+      uint64_t g[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) g[j] = 0;
+      if (on[i]) load_pairs(p.g[i] + (p.gain_full ? 8 * l.vec : l.d0), g);
       if constexpr (TAN) {
-        const float k3 = inv * inv * inv * (sums[1] * inv_len);
+        const float k3 = -(inv * inv * inv * (sums[2 + i] * inv_len));
+        const uint64_t k32 = f2(k3, k3);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) tf[i] = g[i] * fmaf(tf[i], inv, -f[i] * k3);
+        for (int j = 0; j < 4; ++j) tx[i][j] = mul2(g[j], fma2(tx[i][j], inv2, mul2(x[i][j], k32)));
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] *= g[i] * inv;
+      for (int j = 0; j < 4; ++j) x[i][j] = mul2(x[i][j], mul2(g[j], inv2));
     }
-    Angle a;
-    if (turns && on[u]) load_angle(p, n, l.d0, a);
-    rotate(f, a, p.half, turns, first, p.P / 8, 1.f);
-    if (TAN) rotate(tf, a, p.half, turns, first, p.P / 8, 1.f);
-    if (on[u]) {
-      v8::Raw<T> o;
-      v8::pack(f, o);
-      v8::store(y + out, o);
-      if (TAN) {
-        v8::pack(tf, o);
-        v8::store(ty + out, o);
-      }
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    turn.apply(x[i]);
+    if (TAN) turn.apply(tx[i]);
+    if (on[i]) {
+      v8::store(static_cast<T *>(p.y[i]) + place(i), pack<T>(x[i]));
+      if (TAN) v8::store(static_cast<T *>(p.ty[i]) + place(i), pack<T>(tx[i]));
     }
   }
 }
 
-// Backward. p.blocks blocks for each tensor (q, k, v next to each other) walk over the
-// token groups, so the gains' gradient stays in registers for a block's whole run; block
-// i leaves its partial dg in p.partial[which][i].
-// CK: x comes from an 8-bit checkpoint.
-template <typename T, bool CK, int U>
-__global__ void __launch_bounds__(1024) qk_rope_bwd_kernel(const QkRopeParams p) {
-  extern __shared__ float red[];
-  const int which = int(blockIdx.x) % p.tensors;
-  const int32_t group = int32_t(blockIdx.x) / p.tensors;
-  const int32_t H = which == 0 ? p.Hq : p.Hk, D = p.D;
-  const Lane l = lane_of(H, D);
-  const int32_t rows = p.B * p.N;
-  const T *dy = static_cast<const T *>(p.dy[which]);
-  T *dx = static_cast<T *>(p.dx[which]);
-  const bool normed = which < 2 && p.norm != kNormNone;
-  const int32_t ns = ck::scale_bytes(H * D);
-  const int8_t *codes = static_cast<const int8_t *>(p.x[which]);
-  const bool turns = l.d0 < 2 * p.P, first = l.d0 < p.P;
-  float g[8], dg[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) g[i] = dg[i] = 0.f;
-  if (normed && l.on) load_gain(p.g[which], p, l, g);
-  const float inv_len = 1.f / float(p.norm == kNormHead ? D : H * D);
+// ------------------------------------------------------------------- backward
+// Asynchronous copies from global to a thread's own slots of shared memory: only the
+// thread that issued them reads them, so waiting for its own groups is all it takes.
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy8(uint32_t dst, const void *src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void *src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+template <typename T>
+__device__ __forceinline__ void copy_vec(uint32_t dst, uint32_t stride, const T *src) {
+  copy16(dst, src);
+  if constexpr (sizeof(T) == 4) copy16(dst + stride, src + 4);
+}
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+template <typename T>
+__device__ __forceinline__ v8::Raw<T> lds_vec(uint32_t a, uint32_t stride) {
+  v8::Raw<T> r;
+  r.a = lds16(a);
+  if constexpr (sizeof(T) == 4) r.b = lds16(a + stride);
+  return r;
+}
 
-  for (int64_t base = int64_t(group) * l.T * U; base < rows; base += int64_t(p.blocks) * l.T * U) {
-    v8::Raw<T> raw[U], xr[U];
-    uint2 cw[U];
-    uint32_t sc[U];
-    bool on[U];
-    int32_t nn[U];
+constexpr int kRing = 3;  // tokens in a thread's ring: one worked on, two on their way (fewer if wide)
+constexpr size_t kMaxSmem = 232448;
+// 16-byte slots of a token: dq, dk and xq, xk (fp32: two each; a checkpoint: eight codes
+// and the word with the scale byte in one slot), and the angles. dv needs none of them
+// and goes through registers.
+template <typename T, bool CK, bool HALF>
+constexpr int bwd_slots() {
+  return 2 * int(sizeof(T) / 2) + (CK ? 2 : 2 * int(sizeof(T) / 2)) + Turn<HALF>::kSlots;
+}
+
+// p.blocks blocks walk over the tokens, T of them at a time each, so the gains' gradient
+// stays in registers for a block's whole run; block i leaves its partial dg in
+// p.partial[q or k][i]. What a token needs comes through a ring of asynchronous copies,
+// two tokens ahead: with plain loads the kernel waited for memory half of its time.
+// CK: xq and xk are 8-bit checkpoints.
+template <typename T, bool CK, bool HALF, int MAXT>
+__global__ void __launch_bounds__(MAXT, MAXT == 256 ? 3 : 1) qk_rope_bwd_kernel(const QkRopeParams p) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  constexpr int kVec = int(sizeof(T) / 2);  // slots of a vector of T
+  constexpr int kSlots = bwd_slots<T, CK, HALF>(), kAngles = kSlots - Turn<HALF>::kSlots;
+  float *red = reinterpret_cast<float *>(smem + size_t(p.ring) * kSlots * 16 * blockDim.x);
+  const Lane l = lane_of(p);
+  const int32_t rows = p.B * p.N, stride = 16 * int32_t(blockDim.x);
+  const uint32_t mine = ptx::smem_u32(smem) + 16 * threadIdx.x;
+  const int32_t heads[3] = {p.Hq, p.Hk, p.dy[2] ? p.Hk : 0};
+  const bool normed = p.norm != kNormNone, in_t = l.t < l.T;
+  uint64_t dg[2][4];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t tok = base + int64_t(u) * l.T + l.t;
-      on[u] = l.on && tok < rows;
-      raw[u] = v8::zero<T>();
-      if (!CK) xr[u] = v8::zero<T>();
-      cw[u] = make_uint2(0, 0);
-      sc[u] = 0;
-      nn[u] = 0;
-      if (on[u]) {
-        const int32_t b = int32_t(tok) / p.N;
-        nn[u] = int32_t(tok) - b * p.N;
-        raw[u] = v8::load(dy + ((size_t(b) * H + l.head) * p.N + nn[u]) * D + l.d0);
-        if (normed) {
-          if (CK) {
-            cw[u] = __ldcs(reinterpret_cast<const uint2 *>(codes + size_t(tok) * H * D + 8 * l.vec));
-            sc[u] = __ldg(p.x_scales[which] + size_t(tok) * ns + l.vec / 4);
-          } else {
-            xr[u] = v8::load(static_cast<const T *>(p.x[which]) + tok * p.ld[which] + 8 * l.vec);
-          }
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) dg[i][j] = 0;
+
+  const int32_t step = p.blocks * l.T;
+  auto fetch = [&](int64_t tok, uint32_t slot0) {
+    if (in_t && tok < rows) {
+      const int32_t b = int32_t(tok) / p.N, n = int32_t(tok) - b * p.N;
+      if (l.d0 < 2 * p.P) {
+        const size_t at = Turn<HALF>::place(p, l, n);
+#pragma unroll
+        for (int i = 0; i < Turn<HALF>::kSlots / 2; ++i) {
+          copy16(slot0 + (kAngles + i) * stride, p.cos + at + 4 * i);
+          copy16(slot0 + (kAngles + Turn<HALF>::kSlots / 2 + i) * stride, p.sin + at + 4 * i);
         }
       }
-    }
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      T *out = dx + (base + int64_t(u) * l.T + l.t) * int64_t(H) * D + 8 * l.vec;
-      if (which == 2) {
-        if (on[u]) v8::store(out, raw[u]);
-        continue;
+      for (int i = 0; i < 2; ++i) {
+        if (l.head >= heads[i]) continue;
+        copy_vec(slot0 + i * kVec * stride, stride,
+                 static_cast<const T *>(p.dy[i]) + ((size_t(b) * heads[i] + l.head) * p.N + n) * p.D + l.d0);
       }
-      float f[8];
-      v8::unpack(raw[u], f);
-      Angle a;
-      if (turns && on[u]) load_angle(p, nn[u], l.d0, a);
-      rotate(f, a, p.half, turns, first, p.P / 8, -1.f);
       if (normed) {
-        float xv[8], sums[2] = {0.f, 0.f};
-        if (CK) {
-          const float unit = ck::unit_of(sc[u]);
-          ck::unpack_codes4(cw[u].x, unit, xv[0], xv[1], xv[2], xv[3]);
-          ck::unpack_codes4(cw[u].y, unit, xv[4], xv[5], xv[6], xv[7]);
-        } else {
-          v8::unpack(xr[u], xv);
-        }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          sums[0] = fmaf(xv[i], xv[i], sums[0]);
-          sums[1] = fmaf(xv[i], g[i] * f[i], sums[1]);
-        }
-        group_sums(sums, l, p.norm, D, H, red);
-        const float inv = rsqrtf(fmaf(sums[0], inv_len, p.eps));
-        const float k3 = inv * inv * inv * (sums[1] * inv_len);
-        if (on[u]) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            dg[i] = fmaf(f[i], xv[i] * inv, dg[i]);
-            f[i] = fmaf(g[i] * f[i], inv, -xv[i] * k3);
+        for (int i = 0; i < 2; ++i) {
+          if (l.head >= heads[i]) continue;
+          const uint32_t at = slot0 + (2 * kVec + i * (CK ? 1 : kVec)) * stride;
+          if constexpr (CK) {
+            const int32_t width = heads[i] * p.D;
+            copy8(at, static_cast<const int8_t *>(p.x[i]) + size_t(tok) * width + 8 * l.vec);
+            copy4(at + 8, p.x_scales[i] + size_t(tok) * ck::scale_bytes(width) + (l.vec / 16) * 4);
+          } else {
+            copy_vec(at, stride, static_cast<const T *>(p.x[i]) + tok * p.ld[i] + 8 * l.vec);
           }
         }
       }
-      if (on[u]) {
-        v8::Raw<T> o;
-        v8::pack(f, o);
-        v8::store(out, o);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+
+  int64_t tok = int64_t(blockIdx.x) * l.T + l.t;
+  const int64_t last = (int64_t(rows) - int64_t(blockIdx.x) * l.T + step - 1) / step;  // rounds of this block
+  for (int i = 0; i < p.ring - 1; ++i) fetch(tok + int64_t(i) * step, mine + i * kSlots * stride);
+  int at = 0, to = p.ring - 1;  // ring positions
+  for (int64_t round = 0; round < last; ++round, tok += step) {
+    fetch(tok + int64_t(p.ring - 1) * step, mine + to * kSlots * stride);
+    const uint32_t slot0 = mine + at * kSlots * stride;
+    const bool here = in_t && tok < rows;
+    v8::Raw<T> dv = v8::zero<T>();
+    const bool on_v = here && l.head < heads[2];
+    if (on_v) {
+      const int32_t b = int32_t(tok) / p.N, n = int32_t(tok) - b * p.N;
+      dv = v8::load(static_cast<const T *>(p.dy[2]) + ((size_t(b) * heads[2] + l.head) * p.N + n) * p.D + l.d0);
+    }
+    if (p.ring == 3)
+      asm volatile("cp.async.wait_group 2;" ::: "memory");
+    else if (p.ring == 2)
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+    else
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+    Turn<HALF> turn;
+    {
+      float4 angles[Turn<HALF>::kSlots];
+#pragma unroll
+      for (int i = 0; i < Turn<HALF>::kSlots; ++i) {
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (here && l.d0 < 2 * p.P) w = lds16(slot0 + (kAngles + i) * stride);
+        angles[i] = make_float4(__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w));
+      }
+      turn.template set<true>(p, l, angles);
+    }
+    uint64_t u[2][4], x[2][4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const bool on = here && l.head < heads[i];
+      v8::Raw<T> r = v8::zero<T>();
+      if (on) r = lds_vec<T>(slot0 + i * kVec * stride, stride);
+      unpack(r, u[i]);
+      turn.apply(u[i]);
+      if (!normed) continue;
+      const uint32_t xs = slot0 + (2 * kVec + i * (CK ? 1 : kVec)) * stride;
+      if constexpr (CK) {
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (on) w = lds16(xs);
+        const float unit = ck::unit_of((w.z >> (8 * ((l.vec >> 2) & 3))) & 0xFFu);
+        float f[8];
+        ck::unpack_codes4(w.x, unit, f[0], f[1], f[2], f[3]);
+        ck::unpack_codes4(w.y, unit, f[4], f[5], f[6], f[7]);
+        pairs_of(f, x[i]);
+      } else {
+        v8::Raw<T> rx = v8::zero<T>();
+        if (on) rx = lds_vec<T>(xs, stride);
+        unpack(rx, x[i]);
       }
     }
+    if (normed) {
+      uint64_t gu[2][4];
+      float sums[4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) gu[i][j] = 0;
+        if (here && l.head < heads[i]) {
+          load_pairs(p.g[i] + (p.gain_full ? 8 * l.vec : l.d0), gu[i]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) gu[i][j] = mul2(gu[i][j], u[i][j]);
+        }
+        sums[i] = dot(x[i], x[i]);
+        sums[2 + i] = dot(x[i], gu[i]);
+      }
+      group_sums(sums, l, p, red);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float inv_len = 1.f / float(p.norm == kNormHead ? p.D : heads[i] * p.D);
+        const float inv = rsqrtf(fmaf(sums[i], inv_len, p.eps));
+        const float k3 = -(inv * inv * inv * (sums[2 + i] * inv_len));
+        const uint64_t inv2 = f2(inv, inv), k32 = f2(k3, k3);
+        if (here && l.head < heads[i]) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            dg[i][j] = fma2(u[i][j], mul2(x[i][j], inv2), dg[i][j]);
+            u[i][j] = fma2(gu[i][j], inv2, mul2(x[i][j], k32));
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (here && l.head < heads[i])
+        v8::store(static_cast<T *>(p.dx[i]) + tok * (int64_t(heads[i]) * p.D) + 8 * l.vec, pack<T>(u[i]));
+    if (on_v) v8::store(static_cast<T *>(p.dx[2]) + tok * (int64_t(heads[2]) * p.D) + 8 * l.vec, dv);
+    at = at + 1 == p.ring ? 0 : at + 1;
+    to = to + 1 == p.ring ? 0 : to + 1;
   }
+  asm volatile("cp.async.wait_all;" ::: "memory");
   if (!normed) return;
   // this block's dg: over its T tokens a round, and over the heads where they share a gain
-  __syncthreads();
-  if (l.on) {
+  float *sum = reinterpret_cast<float *>(smem);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) red[(l.t * l.V + l.vec) * 8 + i] = dg[i];
-  }
-  __syncthreads();
-  const int32_t len = p.gain_full ? H * D : D, width = H * D;
-  float *part = p.partial[which] + size_t(group) * len;
-  for (int32_t c = int32_t(threadIdx.x); c < len; c += int32_t(blockDim.x)) {
-    float s = 0.f;
-    for (int32_t t = 0; t < l.T; ++t)
-      for (int32_t i = c; i < width; i += len) s += red[t * width + i];
-    part[c] = s;
+  for (int i = 0; i < 2; ++i) {
+    __syncthreads();
+    if (in_t) {
+      float f[8];
+      singles_of(dg[i], f);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum[(l.t * l.V + l.vec) * 8 + j] = f[j];
+    }
+    __syncthreads();
+    const int32_t width = heads[i] * p.D, len = p.gain_full ? width : p.D;
+    float *part = p.partial[i] + size_t(blockIdx.x) * len;
+    for (int32_t c = int32_t(threadIdx.x); c < len; c += int32_t(blockDim.x)) {
+      float s = 0.f;
+      for (int32_t t = 0; t < l.T; ++t)
+        for (int32_t k = c; k < width; k += len) s += sum[t * l.V * 8 + k];
+      part[c] = s;
+    }
   }
 }
 
@@ -408,36 +575,57 @@ int32_t threads_for(const QkRopeParams &p) {
   return (V * t + 31) & ~31;
 }
 
-template <typename T>
-cudaError_t launch_fwd(const QkRopeParams &p, cudaStream_t stream) {
-  const int32_t threads = threads_for(p);
-  const bool tan = p.tx[0] != nullptr;
-  const int32_t U = tan ? 2 : 4;
-  const int32_t Vmax = (p.Hq > p.Hk ? p.Hq : p.Hk) * p.D / 8;
-  const int32_t per = threads / Vmax * U;  // the narrower tensor takes more tokens a block
-  const unsigned grid = unsigned((int64_t(p.B) * p.N + per - 1) / per) * unsigned(p.tensors);
-  const size_t smem = p.norm == kNormToken ? size_t(threads) / (p.D / 8) * (tan ? 2 : 1) * sizeof(float) : 0;
-  if (tan)
-    qk_rope_fwd_kernel<T, true, 2><<<grid, threads, smem, stream>>>(p);
-  else
-    qk_rope_fwd_kernel<T, false, 4><<<grid, threads, smem, stream>>>(p);
-  return cudaGetLastError();
+int32_t vectors(const QkRopeParams &p) { return (p.Hq > p.Hk ? p.Hq : p.Hk) * p.D / 8; }
+int64_t groups_for(const QkRopeParams &p) {  // blocks that hold all tokens, T each
+  const int32_t T = threads_for(p) / vectors(p);
+  return (int64_t(p.B) * p.N + T - 1) / T;
+}
+size_t token_norm_bytes(const QkRopeParams &p, int32_t values) {  // group_sums' shared memory
+  return p.norm == kNormToken ? size_t(threads_for(p)) / (p.D / 8) * values * sizeof(float) : 0;
 }
 
-template <typename T>
-cudaError_t launch_bwd(const QkRopeParams &p, cudaStream_t stream) {
+template <typename T, bool TAN, int MAXT>
+cudaError_t launch_fwd(const QkRopeParams &p, cudaStream_t stream) {
   const int32_t threads = threads_for(p);
-  const unsigned grid = unsigned(p.blocks * p.tensors);
-  const size_t smem = p.norm == kNormNone ? 0 : size_t(threads) * 8 * sizeof(float);
-  if (p.x_scales[0])
-    qk_rope_bwd_kernel<T, true, 2><<<grid, threads, smem, stream>>>(p);
+  const unsigned grid = unsigned(groups_for(p));
+  const size_t smem = token_norm_bytes(p, TAN ? 4 : 2);
+  if (p.half)
+    qk_rope_fwd_kernel<T, TAN, true, MAXT><<<grid, threads, smem, stream>>>(p);
   else
-    qk_rope_bwd_kernel<T, false, 2><<<grid, threads, smem, stream>>>(p);
-  cudaError_t e = cudaGetLastError();
+    qk_rope_fwd_kernel<T, TAN, false, MAXT><<<grid, threads, smem, stream>>>(p);
+  return cudaGetLastError();
+}
+template <typename T>
+cudaError_t launch_fwd(const QkRopeParams &p, cudaStream_t stream) {
+  if (threads_for(p) <= 256) return p.tx[0] ? launch_fwd<T, true, 256>(p, stream) : launch_fwd<T, false, 256>(p, stream);
+  return p.tx[0] ? launch_fwd<T, true, 1024>(p, stream) : launch_fwd<T, false, 1024>(p, stream);
+}
+
+template <typename T, bool CK, bool HALF, int MAXT>
+cudaError_t launch_bwd(const QkRopeParams &params, cudaStream_t stream) {
+  auto kernel = qk_rope_bwd_kernel<T, CK, HALF, MAXT>;
+  QkRopeParams p = params;
+  const int32_t threads = threads_for(p);
+  const size_t token = size_t(bwd_slots<T, CK, HALF>()) * 16 * threads, extra = token_norm_bytes(p, 4);
+  p.ring = kRing;
+  while (p.ring > 1 && p.ring * token + extra > kMaxSmem) --p.ring;
+  static std::atomic<uint64_t> set_up{0};
+  cudaError_t e = once_per_device(set_up, [&] {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kMaxSmem));
+  });
+  if (e != cudaSuccess) return e;
+  kernel<<<unsigned(p.blocks), threads, p.ring * token + extra, stream>>>(p);
+  e = cudaGetLastError();
   if (e != cudaSuccess || p.norm == kNormNone) return e;
-  const int32_t len = p.gain_full ? (p.Hq > p.Hk ? p.Hq : p.Hk) * p.D : p.D;
+  const int32_t len = p.gain_full ? vectors(p) * 8 : p.D;
   gain_grad_kernel<<<dim3(unsigned((len + 31) / 32), 2), 256, 0, stream>>>(p);
   return cudaGetLastError();
+}
+template <typename T, bool CK>
+cudaError_t launch_bwd(const QkRopeParams &p, cudaStream_t stream) {
+  if (threads_for(p) <= 256)
+    return p.half ? launch_bwd<T, CK, true, 256>(p, stream) : launch_bwd<T, CK, false, 256>(p, stream);
+  return p.half ? launch_bwd<T, CK, true, 1024>(p, stream) : launch_bwd<T, CK, false, 1024>(p, stream);
 }
 
 }  // namespace
@@ -461,14 +649,16 @@ cudaError_t launch_rope_table(const RopeTableParams &p, bool pos64, cudaStream_t
   return pos64 ? launch_table<int64_t, 1>(p, stream) : launch_table<int32_t, 1>(p, stream);
 }
 
-// Blocks of the backward a tensor: fixed by the sizes alone, so that the order of
-// the gains' sums is too. Four blocks an SM for the three tensors together.
+// Blocks of the backward: fixed by the sizes alone, so that the order of the gains'
+// sums is too. About as many as are resident on 148 SMs at once.
 int32_t qk_rope_bwd_blocks(int32_t B, int32_t N, int32_t Hq, int32_t Hk, int32_t D) {
   QkRopeParams p{};
-  p.Hq = Hq; p.Hk = Hk; p.D = D;
-  const int32_t V = (Hq > Hk ? Hq : Hk) * D / 8;
-  const int64_t groups = (int64_t(B) * N + threads_for(p) / V * 2 - 1) / (threads_for(p) / V * 2);
-  const int64_t most = 148 * 4;
+  p.B = B;
+  p.N = N;
+  p.Hq = Hq;
+  p.Hk = Hk;
+  p.D = D;
+  const int64_t groups = groups_for(p), most = 148 * int64_t(768 / threads_for(p) < 1 ? 1 : 768 / threads_for(p));
   return int32_t(groups < most ? groups : most);
 }
 
@@ -476,7 +666,8 @@ cudaError_t launch_qk_rope_fwd(const QkRopeParams &p, bool bf16, cudaStream_t st
   return bf16 ? launch_fwd<__nv_bfloat16>(p, stream) : launch_fwd<float>(p, stream);
 }
 cudaError_t launch_qk_rope_bwd(const QkRopeParams &p, bool bf16, cudaStream_t stream) {
-  return bf16 ? launch_bwd<__nv_bfloat16>(p, stream) : launch_bwd<float>(p, stream);
+  if (p.x_scales[0]) return bf16 ? launch_bwd<__nv_bfloat16, true>(p, stream) : launch_bwd<float, true>(p, stream);
+  return bf16 ? launch_bwd<__nv_bfloat16, false>(p, stream) : launch_bwd<float, false>(p, stream);
 }
 
 }  // namespace caj
