@@ -1,4 +1,5 @@
-"""Builds libcausaljvp.so in-tree with nvcc for sm_100a.
+"""Builds libcausaljvp.so in-tree with nvcc for sm_100a, and the Python extension
+_block.so over it with the host compiler.
 
 Run as `python -m masked_attention_jvp_b200.build` (or call `build()`). The
 library is written next to this file so it travels with the source tree; no
@@ -10,6 +11,7 @@ import os
 import shutil
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -21,6 +23,10 @@ SOURCES = ["api.cpp", "api_block.cpp", "api_linear.cpp", "fwd_jvp_sm100.cu", "fw
            "qk_rope.cu", "ckpt8.cu", "linear_sm100.cu"]
 HEADERS = ["api_internal.h", "kernels.h", "mask_schedule.h", "ptx_sm100.cuh", "vec8.cuh", "ckpt8.cuh",
            "linear_act.cuh", "pair_sm100.cuh"]
+
+# Python entry of the block operators (torch tensors in, the library's calls below)
+BIND = "bind.cpp"
+EXT = os.path.join(PKG, "_block.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2", "--expt-relaxed-constexpr",
@@ -35,11 +41,37 @@ def _nvcc():
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    if not (os.path.exists(LIB) and os.path.exists(EXT)):
         return True
-    t = os.path.getmtime(LIB)
-    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS] + [os.path.join(INCLUDE, "causaljvp.h")]
+    t = min(os.path.getmtime(LIB), os.path.getmtime(EXT))
+    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS + [BIND]] + [os.path.join(INCLUDE, "causaljvp.h")]
     return any(os.path.getmtime(d) > t for d in deps)
+
+
+def _build_ext() -> None:
+    """_block.so: a CPython extension against this interpreter's torch, linked to the library
+    beside it."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+
+    torch_lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cuda_inc = os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")
+    incs = [INCLUDE, *cpp_extension.include_paths(), sysconfig.get_path("include"), cuda_inc]
+    tmp = EXT + f".tmp{os.getpid()}"
+    # the system's g++, as nvcc uses: a compiler that links its own static libstdc++ would put
+    # a second, uninitialised C++ runtime beside torch's, and the first formatted error crashes
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-w",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    for i in incs:
+        cmd += ["-isystem", i]
+    cmd += [os.path.join(CSRC, BIND), "-o", tmp, LIB, f"-L{torch_lib}", "-lc10", "-lc10_cuda", "-ltorch_cpu",
+            "-ltorch_cuda", "-ltorch_python", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{torch_lib}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"building _block.so failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, EXT)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -48,25 +80,29 @@ def build(force: bool = False, verbose: bool = False) -> str:
     nvcc = _nvcc()
     objdir = os.path.join(PKG, "_build")
     os.makedirs(objdir, exist_ok=True)
-    objs = []
-    logs = []
-    for src in SOURCES:
+    objs = [os.path.join(objdir, src + ".o") for src in SOURCES]
+
+    def compile_one(src: str) -> str:
         obj = os.path.join(objdir, src + ".o")
         cmd = [nvcc, *ARCH, *NVCC_FLAGS, "-I", INCLUDE, "-I", CSRC, "-c", os.path.join(CSRC, src), "-o", obj]
         if src.endswith(".cpp"):
             cmd.insert(1, "-x")
             cmd.insert(2, "cu")
         r = subprocess.run(cmd, capture_output=True, text=True)
-        logs.append(r.stdout + r.stderr)
         if r.returncode != 0:
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
-        objs.append(obj)
+        return r.stdout + r.stderr
+
+    with ThreadPoolExecutor(max_workers=os.cpu_count() or 1) as pool:
+        logs = list(pool.map(compile_one, SOURCES))
     tmp = LIB + f".tmp{os.getpid()}"
-    r = subprocess.run([nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static"],
+    r = subprocess.run([nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static", "-Xlinker",
+                        "-soname=libcausaljvp.so"],
                        capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _build_ext()
     with open(os.path.join(objdir, "ptxas.log"), "w") as f:
         f.write("\n".join(logs))
     if verbose:

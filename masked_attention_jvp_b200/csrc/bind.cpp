@@ -1,0 +1,510 @@
+// Python entry of the block operators: checks torch tensors, allocates outputs and
+// workspaces from torch's allocator and calls the C-ABI library (causaljvp.h) on the
+// tensors' device and its current stream. The same work through ctypes took 10 to 28 us
+// a call on the host, more than the smallest kernels (2 to 5 us); here it takes 3 to 6.
+// Arguments come in the order that block.py passes them; the errors are ValueError for
+// arguments and CajError (raised by _lib.check) for the library's statuses.
+#include <Python.h>
+
+#include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDAGuard.h>
+#include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
+#include <torch/csrc/autograd/python_variable.h>
+
+#include <initializer_list>
+#include <optional>
+#include <string>
+#include <utility>
+#include <vector>
+
+#include "causaljvp.h"
+
+namespace {
+
+using at::Tensor;
+using OptTensor = std::optional<Tensor>;
+
+// ------------------------------------------------------------------ arguments
+const Tensor &tensor(PyObject *o, const char *what, const char *name) {
+  TORCH_CHECK_VALUE(THPVariable_Check(o), what, ": ", name, " must be a tensor");
+  return THPVariable_Unpack(o);
+}
+OptTensor maybe(PyObject *o, const char *what, const char *name) {
+  if (o == Py_None) return std::nullopt;
+  return tensor(o, what, name);
+}
+int64_t integer(PyObject *o) {
+  const long long v = PyLong_AsLongLong(o);
+  if (v == -1 && PyErr_Occurred()) throw python_error();
+  return v;
+}
+double number(PyObject *o) {
+  const double v = PyFloat_AsDouble(o);
+  if (v == -1.0 && PyErr_Occurred()) throw python_error();
+  return v;
+}
+void expect(Py_ssize_t got, Py_ssize_t want) {
+  TORCH_CHECK_VALUE(got == want, "wrong number of arguments");
+}
+
+void *ptr(const Tensor &t) { return t.data_ptr(); }
+void *ptr(const OptTensor &t) { return t ? t->data_ptr() : nullptr; }
+float *fptr(const OptTensor &t) { return static_cast<float *>(ptr(t)); }
+uint8_t *bptr(const OptTensor &t) { return static_cast<uint8_t *>(ptr(t)); }
+
+bool value_type(const Tensor &t) { return t.scalar_type() == at::kBFloat16 || t.scalar_type() == at::kFloat; }
+int32_t dtype_of(const Tensor &t) { return t.scalar_type() == at::kBFloat16 ? CAJ_DTYPE_BF16 : CAJ_DTYPE_F32; }
+
+void same_device(const char *what, const Tensor &first, std::initializer_list<const OptTensor *> others) {
+  for (const OptTensor *t : others)
+    TORCH_CHECK_VALUE(!*t || (**t).device() == first.device(), what, ": all tensors must be CUDA tensors on one device");
+}
+
+Tensor make(at::IntArrayRef sizes, at::ScalarType type, const Tensor &like) {
+  return at::detail::empty_cuda(sizes, type, like.device(), std::nullopt);
+}
+std::vector<int64_t> with_last(const Tensor &t, int64_t last) {
+  std::vector<int64_t> s = t.sizes().vec();
+  s.back() = last;
+  return s;
+}
+
+// t seen as rows of its last axis: their number and distance; nothing if the strides do
+// not allow it.
+std::optional<std::pair<int64_t, int64_t>> rows_of(const Tensor &t) {
+  const auto sizes = t.sizes(), strides = t.strides();
+  const int64_t n = t.dim(), width = sizes[n - 1];
+  int64_t rows = 1;
+  for (int64_t i = 0; i + 1 < n; ++i) rows *= sizes[i];
+  if (t.is_contiguous() || t.numel() == 0) return std::make_pair(rows, width > 1 ? width : int64_t(1));
+  if (width > 1 && strides[n - 1] != 1) return std::nullopt;
+  int64_t ld = -1, inner = 1;  // the distance of the innermost axis with more than one row; rows below
+  for (int64_t i = n - 2; i >= 0; --i) {
+    if (sizes[i] == 1) continue;
+    if (ld < 0)
+      ld = strides[i];
+    else if (strides[i] != ld * inner)
+      return std::nullopt;
+    inner *= sizes[i];
+  }
+  if (ld < 0) ld = width;
+  if (ld < width) return std::nullopt;
+  return std::make_pair(rows, ld);
+}
+
+// ---------------------------------------------------------------- results, errors
+PyObject *wrap(const OptTensor &t) {
+  if (!t) Py_RETURN_NONE;
+  return THPVariable_Wrap(*t);
+}
+PyObject *tuple_of(std::initializer_list<OptTensor> ts) {
+  PyObject *r = PyTuple_New(Py_ssize_t(ts.size()));
+  if (!r) throw python_error();
+  Py_ssize_t i = 0;
+  for (const OptTensor &t : ts) {
+    PyObject *o = wrap(t);
+    if (!o) {
+      Py_DECREF(r);
+      throw python_error();
+    }
+    PyTuple_SET_ITEM(r, i++, o);
+  }
+  return r;
+}
+// Raises what _lib.check raises for a status that is not CAJ_OK.
+void check(caj_status st, const char *name) {
+  if (st == CAJ_OK) return;
+  PyObject *lib = PyImport_ImportModule("masked_attention_jvp_b200._lib");
+  if (lib) {
+    Py_XDECREF(PyObject_CallMethod(lib, "check", "is", int(st), name));
+    Py_DECREF(lib);
+  }
+  if (!PyErr_Occurred()) PyErr_SetString(PyExc_RuntimeError, name);
+  throw python_error();
+}
+
+// The device of `t` is current while this lives.
+struct On {
+  explicit On(const Tensor &t) : guard(t.device()), stream(c10::cuda::getCurrentCUDAStream(t.device().index()).stream()) {}
+  c10::cuda::CUDAGuard guard;
+  void *stream;
+};
+
+int64_t code_width(int64_t C) { return (C + 31) / 32 * 32; }
+int64_t scale_width(int64_t C) { return (code_width(C) / 32 + 3) / 4 * 4; }
+void check_ckpt(const char *what, const Tensor &codes, const Tensor &scales, int64_t rows, int64_t C) {
+  auto good = [&](const Tensor &t, at::ScalarType type, int64_t width) {
+    return t.is_cuda() && t.scalar_type() == type && t.dim() == 2 && t.size(0) == rows && t.size(1) == width &&
+           t.is_contiguous();
+  };
+  TORCH_CHECK_VALUE(good(codes, at::kChar, code_width(C)) && good(scales, at::kByte, scale_width(C)), what,
+                    ": a checkpoint's codes are int8 [", rows, ", ", code_width(C), "] and its scales uint8 [", rows,
+                    ", ", scale_width(C), "], contiguous CUDA tensors");
+}
+
+// ------------------------------------------------------------------- checkpoints
+PyObject *ckpt8_pack(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  const char *what = "ckpt8_pack";
+  expect(n, 1);
+  Tensor x = tensor(a[0], what, "x");
+  TORCH_CHECK_VALUE(x.is_cuda() && value_type(x) && x.dim() >= 1 && x.size(-1) >= 1, what,
+                    ": x must be a bf16 or fp32 CUDA tensor with at least one column");
+  auto at = rows_of(x);
+  if (!at) {
+    x = x.contiguous();
+    at = rows_of(x);
+  }
+  const int64_t C = x.size(-1);
+  TORCH_CHECK_VALUE(C < (int64_t(1) << 31) - 64, what, ": rows are too wide");
+  Tensor codes = make({at->first, code_width(C)}, at::kChar, x), scales = make({at->first, scale_width(C)}, at::kByte, x);
+  On on(x);
+  check(caj_ckpt_pack(ptr(x), at->first, int32_t(C), at->second, dtype_of(x), static_cast<int8_t *>(ptr(codes)),
+                      static_cast<uint8_t *>(ptr(scales)), on.stream),
+        "caj_ckpt_pack");
+  return tuple_of({codes, scales});
+  END_HANDLE_TH_ERRORS
+}
+
+// codes, scales, shape, bf16
+PyObject *ckpt8_unpack(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  const char *what = "ckpt8_unpack";
+  expect(n, 4);
+  const Tensor &codes = tensor(a[0], what, "codes"), &scales = tensor(a[1], what, "scales");
+  TORCH_CHECK_VALUE(PyTuple_Check(a[2]) && PyTuple_GET_SIZE(a[2]) >= 1, what, ": the shape must be a tuple");
+  std::vector<int64_t> shape;
+  int64_t rows = 1;
+  for (Py_ssize_t i = 0; i < PyTuple_GET_SIZE(a[2]); ++i) {
+    shape.push_back(integer(PyTuple_GET_ITEM(a[2], i)));
+    TORCH_CHECK_VALUE(shape.back() >= 0, what, ": the shape must not be negative");
+    if (i + 1 < PyTuple_GET_SIZE(a[2])) rows *= shape.back();
+  }
+  const int64_t C = shape.back();
+  TORCH_CHECK_VALUE(C >= 1 && C < (int64_t(1) << 31) - 64, what, ": rows hold at least one value");
+  check_ckpt(what, codes, scales, rows, C);
+  const OptTensor os = scales;
+  same_device(what, codes, {&os});
+  Tensor x = make(shape, a[3] == Py_True ? at::kBFloat16 : at::kFloat, codes);
+  On on(x);
+  check(caj_ckpt_unpack(static_cast<const int8_t *>(ptr(codes)), static_cast<const uint8_t *>(ptr(scales)), rows,
+                        int32_t(C), C, dtype_of(x), ptr(x), on.stream),
+        "caj_ckpt_unpack");
+  return THPVariable_Wrap(x);
+  END_HANDLE_TH_ERRORS
+}
+
+// -------------------------------------------------------------------- rotary tables
+// pos, freq, axis, mscale
+PyObject *rope_table(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  const char *what = "rope_table";
+  expect(n, 4);
+  const Tensor &pos = tensor(a[0], what, "pos"), &freq = tensor(a[1], what, "freq");
+  const OptTensor axis = maybe(a[2], what, "axis");
+  const bool wide = pos.scalar_type() == at::kLong;
+  TORCH_CHECK_VALUE(pos.is_cuda() && (wide || pos.scalar_type() == at::kInt) && (pos.dim() == 1 || pos.dim() == 2) &&
+                        pos.is_contiguous(),
+                    what, ": pos must be a contiguous int32 or int64 CUDA tensor [N] or [N, axes]");
+  TORCH_CHECK_VALUE(freq.scalar_type() == at::kDouble && freq.dim() == 1 && freq.is_contiguous() && freq.numel() > 0, what,
+                    ": freq must be a contiguous fp64 tensor [P]");
+  TORCH_CHECK_VALUE(!axis || (axis->scalar_type() == at::kInt && axis->sizes() == freq.sizes() && axis->is_contiguous()), what,
+                    ": axis must be a contiguous int32 tensor [P]");
+  const OptTensor f = freq;
+  same_device(what, pos, {&f, &axis});
+  const int64_t N = pos.size(0), P = freq.size(0), A = pos.dim() == 2 ? pos.size(1) : 1;
+  TORCH_CHECK_VALUE(P < (int64_t(1) << 31) && A >= 1 && A < (int64_t(1) << 31), what, ": too many pairs, or no axis");
+  Tensor cos = make({N, P}, at::kFloat, pos), sin = make({N, P}, at::kFloat, pos);
+  On on(pos);
+  check(caj_rope_table(ptr(pos), wide, static_cast<const double *>(ptr(freq)), static_cast<const int32_t *>(ptr(axis)), N,
+                       int32_t(A), int32_t(P), float(number(a[3])), static_cast<float *>(ptr(cos)),
+                       static_cast<float *>(ptr(sin)), on.stream),
+        "caj_rope_table");
+  return tuple_of({cos, sin});
+  END_HANDLE_TH_ERRORS
+}
+
+// ----------------------------------------------------------------- norm and rotation
+int64_t token_rows(const char *what, const char *name, const Tensor &t, int64_t B, int64_t N, int64_t width,
+                   at::ScalarType type) {
+  TORCH_CHECK_VALUE(t.is_cuda() && t.scalar_type() == type && t.dim() == 3 && t.size(0) == B && t.size(1) == N &&
+                        t.size(2) == width,
+                    what, ": ", name, " must be a ", c10::toString(type), " CUDA tensor [", B, ", ", N, ", ", width, "]");
+  const auto at = rows_of(t);
+  TORCH_CHECK_VALUE(at && at->second * t.element_size() % 16 == 0 && reinterpret_cast<uintptr_t>(t.data_ptr()) % 16 == 0, what,
+                    ": ", name, "'s tokens must lie at one distance, a multiple of 16 bytes, 16-byte aligned, with "
+                    "neighbouring channels side by side");
+  return at->second;
+}
+
+caj_qk_rope_shape rope_shape(const char *what, int64_t B, int64_t N, int64_t Hq, int64_t Hk, int64_t D, const Tensor &like,
+                             const OptTensor &gq, const OptTensor &gk, const Tensor &cos, const Tensor &sin, double eps,
+                             int64_t norm, int64_t layout) {
+  for (const Tensor *t : {&cos, &sin})
+    TORCH_CHECK_VALUE(t->is_cuda() && t->scalar_type() == at::kFloat && t->is_contiguous() && t->dim() == 2 &&
+                          t->size(0) == N && t->sizes() == cos.sizes(),
+                      what, ": rope tables must be contiguous fp32 CUDA tensors [N, pairs]");
+  caj_qk_rope_shape s{};
+  if (norm == CAJ_NORM_NONE) {
+    TORCH_CHECK_VALUE(!gq && !gk, what, ": norm 'none' takes no gains");
+  } else {
+    for (const OptTensor *t : {&gq, &gk})
+      TORCH_CHECK_VALUE(*t && (*t)->is_cuda() && (*t)->scalar_type() == at::kFloat && (*t)->is_contiguous() && (*t)->dim() == 1,
+                        what, ": gains must be contiguous fp32 CUDA tensors");
+    s.gain_full = norm == CAJ_NORM_TOKEN || gq->numel() != D || gk->numel() != D;
+    TORCH_CHECK_VALUE(!s.gain_full || (gq->numel() == Hq * D && gk->numel() == Hk * D), what,
+                      ": gains hold D values (norm 'head', shared by the heads) or heads * D");
+  }
+  const int64_t limit = (int64_t(1) << 31) - 1;
+  TORCH_CHECK_VALUE(B <= limit && N <= limit && Hq <= limit && Hk <= limit && D <= limit && cos.size(1) <= limit, what,
+                    ": a size is too large");
+  s.B = int32_t(B);
+  s.N = int32_t(N);
+  s.Hq = int32_t(Hq);
+  s.Hk = int32_t(Hk);
+  s.D = int32_t(D);
+  s.pairs = int32_t(cos.size(1));
+  s.dtype = dtype_of(like);
+  s.norm = int32_t(norm);
+  s.layout = int32_t(layout);
+  s.eps = float(eps);
+  return s;
+}
+
+// xq, xk, xv, gq, gk, cos, sin, H, Hk, eps, norm, layout, txq, txk, txv
+PyObject *qk_norm_rope_fwd(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  const char *what = "qk_norm_rope_fwd";
+  expect(n, 15);
+  const Tensor &xq = tensor(a[0], what, "xq"), &xk = tensor(a[1], what, "xk");
+  const OptTensor xv = maybe(a[2], what, "xv"), gq = maybe(a[3], what, "gq"), gk = maybe(a[4], what, "gk");
+  const Tensor &cos = tensor(a[5], what, "rope_cos"), &sin = tensor(a[6], what, "rope_sin");
+  const int64_t H = integer(a[7]), Hk = integer(a[8]);
+  const OptTensor txq = maybe(a[12], what, "txq"), txk = maybe(a[13], what, "txk"), txv = maybe(a[14], what, "txv");
+  TORCH_CHECK_VALUE(xq.dim() == 3 && H > 0 && Hk > 0 && xq.size(2) % H == 0 && value_type(xq), what,
+                    ": xq must be a bf16 or fp32 tensor [B, N, H*D]");
+  const int64_t B = xq.size(0), N = xq.size(1), D = xq.size(2) / H;
+  const bool tan = txq.has_value();
+  TORCH_CHECK_VALUE(tan == txk.has_value() && txv.has_value() == (tan && xv.has_value()), what,
+                    ": give the tangents of all inputs or of none");
+  caj_qk_rope_shape s = rope_shape(what, B, N, H, Hk, D, xq, gq, gk, cos, sin, number(a[9]), integer(a[10]), integer(a[11]));
+  const auto type = xq.scalar_type();
+  s.ldq = token_rows(what, "xq", xq, B, N, H * D, type);
+  s.ldk = token_rows(what, "xk", xk, B, N, Hk * D, type);
+  if (xv) s.ldv = token_rows(what, "xv", *xv, B, N, Hk * D, type);
+  if (tan) {
+    s.ldtq = token_rows(what, "txq", *txq, B, N, H * D, type);
+    s.ldtk = token_rows(what, "txk", *txk, B, N, Hk * D, type);
+    if (txv) s.ldtv = token_rows(what, "txv", *txv, B, N, Hk * D, type);
+  }
+  const OptTensor okx = xk, oc = cos, os = sin;
+  same_device(what, xq, {&okx, &xv, &txq, &txk, &txv, &gq, &gk, &oc, &os});
+  auto out = [&](bool wanted, int64_t heads) { return wanted ? OptTensor(make({B, heads, N, D}, type, xq)) : std::nullopt; };
+  OptTensor y[6] = {out(true, H), out(true, Hk), out(xv.has_value(), Hk), out(tan, H), out(tan, Hk), out(txv.has_value(), Hk)};
+  if (B * N > 0) {
+    On on(xq);
+    check(caj_qk_rope_fwd(ptr(xq), ptr(xk), ptr(xv), ptr(txq), ptr(txk), ptr(txv), fptr(gq), fptr(gk),
+                          static_cast<const float *>(ptr(cos)), static_cast<const float *>(ptr(sin)), &s, ptr(y[0]),
+                          ptr(y[1]), ptr(y[2]), ptr(y[3]), ptr(y[4]), ptr(y[5]), on.stream),
+          "caj_qk_rope_fwd");
+  }
+  if (!tan) return xv ? tuple_of({y[0], y[1], y[2]}) : tuple_of({y[0], y[1]});
+  return xv ? tuple_of({y[0], y[1], y[2], y[3], y[4], y[5]}) : tuple_of({y[0], y[1], y[3], y[4]});
+  END_HANDLE_TH_ERRORS
+}
+
+// dq, dk, dv, xq, xk (or codes), xq scales, xk scales, gq, gk, cos, sin, eps, norm, layout
+PyObject *qk_norm_rope_bwd(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  const char *what = "qk_norm_rope_bwd";
+  expect(n, 14);
+  const Tensor &dq = tensor(a[0], what, "dq"), &dk = tensor(a[1], what, "dk");
+  const OptTensor dv = maybe(a[2], what, "dv");
+  const OptTensor x[2] = {maybe(a[3], what, "xq"), maybe(a[4], what, "xk")};
+  const OptTensor scales[2] = {maybe(a[5], what, "xq's scales"), maybe(a[6], what, "xk's scales")};
+  const OptTensor g[2] = {maybe(a[7], what, "gq"), maybe(a[8], what, "gk")};
+  const Tensor &cos = tensor(a[9], what, "rope_cos"), &sin = tensor(a[10], what, "rope_sin");
+  TORCH_CHECK_VALUE(dq.dim() == 4 && dk.dim() == 4 && value_type(dq), what,
+                    ": dq, dk must be bf16 or fp32 tensors [B, heads, N, D]");
+  const int64_t B = dq.size(0), H = dq.size(1), N = dq.size(2), D = dq.size(3), Hk = dk.size(1), norm = integer(a[12]);
+  const auto type = dq.scalar_type();
+  auto good = [&](const Tensor &t, int64_t heads) {
+    return t.is_cuda() && t.is_contiguous() && t.scalar_type() == type && t.dim() == 4 && t.size(0) == B &&
+           t.size(1) == heads && t.size(2) == N && t.size(3) == D;
+  };
+  TORCH_CHECK_VALUE(good(dq, H) && good(dk, Hk) && (!dv || good(*dv, Hk)), what,
+                    ": dq, dk, dv must be contiguous CUDA tensors [B, heads, N, D] of one dtype");
+  caj_qk_rope_shape s = rope_shape(what, B, N, H, Hk, D, dq, g[0], g[1], cos, sin, number(a[11]), norm, integer(a[13]));
+  if (norm == CAJ_NORM_NONE) {
+    TORCH_CHECK_VALUE(!x[0] && !x[1], what, ": norm 'none' reads no inputs: give None");
+  } else {
+    TORCH_CHECK_VALUE(x[0] && x[1], what, ": xq and xk are needed");
+    if (scales[0]) {
+      check_ckpt(what, *x[0], *scales[0], B * N, H * D);
+      check_ckpt(what, *x[1], *scales[1], B * N, Hk * D);
+    } else {
+      s.ldq = token_rows(what, "xq", *x[0], B, N, H * D, type);
+      s.ldk = token_rows(what, "xk", *x[1], B, N, Hk * D, type);
+    }
+  }
+  const OptTensor odk = dk, oc = cos, os = sin;
+  same_device(what, dq, {&odk, &dv, &x[0], &x[1], &scales[0], &scales[1], &g[0], &g[1], &oc, &os});
+  auto out = [&](bool wanted, int64_t heads) { return wanted ? OptTensor(make({B, N, heads * D}, type, dq)) : std::nullopt; };
+  OptTensor dx[3] = {out(true, H), out(true, Hk), out(dv.has_value(), Hk)}, dg[2];
+  for (int i = 0; i < 2; ++i)
+    if (g[i]) dg[i] = make({g[i]->numel()}, at::kFloat, dq);
+  if (B * N > 0) {
+    size_t bytes = 0;
+    check(caj_qk_rope_bwd_workspace(&s, &bytes), "caj_qk_rope_bwd_workspace");
+    On on(dq);
+    OptTensor ws;
+    if (bytes) ws = make({int64_t(bytes)}, at::kByte, dq);
+    check(caj_qk_rope_bwd(ptr(dq), ptr(dk), ptr(dv), ptr(x[0]), ptr(x[1]), bptr(scales[0]), bptr(scales[1]), fptr(g[0]),
+                          fptr(g[1]), static_cast<const float *>(ptr(cos)), static_cast<const float *>(ptr(sin)), &s,
+                          ptr(dx[0]), ptr(dx[1]), ptr(dx[2]), fptr(dg[0]), fptr(dg[1]), ptr(ws), bytes, on.stream),
+          "caj_qk_rope_bwd");
+  } else {
+    for (OptTensor &t : dg)
+      if (t) t->zero_();
+  }
+  return tuple_of({dx[0], dx[1], dx[2], dg[0], dg[1]});
+  END_HANDLE_TH_ERRORS
+}
+
+// -------------------------------------------------------------------- linear layers
+int64_t matrix(const char *what, const char *name, const Tensor &t, int64_t rows, int64_t cols) {
+  TORCH_CHECK_VALUE(t.is_cuda() && t.scalar_type() == at::kBFloat16 && t.dim() >= 1 && t.size(-1) == cols &&
+                        (rows < 0 || t.numel() == rows * cols),
+                    what, ": ", name, " must be a bf16 CUDA tensor with rows of ", cols, " elements",
+                    rows < 0 ? std::string() : ", " + std::to_string(rows) + " of them");
+  const auto at = rows_of(t);
+  TORCH_CHECK_VALUE(at && at->second % 8 == 0 && reinterpret_cast<uintptr_t>(t.data_ptr()) % 16 == 0, what, ": ", name,
+                    "'s rows must lie at one distance, a multiple of 16 bytes, 16-byte aligned");
+  return at->second;
+}
+void check_weight(const char *what, const Tensor &w, const OptTensor &bias) {
+  TORCH_CHECK_VALUE(w.is_cuda() && w.scalar_type() == at::kBFloat16 && w.dim() == 2 && w.is_contiguous(), what,
+                    ": w must be a contiguous bf16 CUDA tensor [C, K]");
+  const int64_t C = w.size(0), K = w.size(1), limit = (int64_t(1) << 31) - 1;
+  TORCH_CHECK_VALUE(C > 0 && K > 0 && C % 8 == 0 && K % 8 == 0 && C <= limit && K <= limit, what,
+                    ": C and K must be positive multiples of 8");
+  TORCH_CHECK_VALUE(!bias || (bias->is_cuda() && bias->scalar_type() == at::kBFloat16 && bias->is_contiguous() &&
+                              bias->dim() == 1 && bias->size(0) == C),
+                    what, ": bias must be a contiguous bf16 CUDA tensor [C]");
+}
+
+// x, w, bias, act, residual, tx, tresidual, save_pre
+PyObject *linear_act_fwd(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  const char *what = "linear_act_fwd";
+  expect(n, 8);
+  const Tensor &x = tensor(a[0], what, "x"), &w = tensor(a[1], what, "w");
+  const OptTensor bias = maybe(a[2], what, "bias"), res = maybe(a[4], what, "residual"), tx = maybe(a[5], what, "tx"),
+                  tres = maybe(a[6], what, "tresidual");
+  check_weight(what, w, bias);
+  TORCH_CHECK_VALUE(!tres || tx, what, ": tresidual needs tx");
+  const int64_t C = w.size(0), K = w.size(1);
+  caj_linear_act_shape s{};
+  s.ldx = matrix(what, "x", x, -1, K);
+  s.M = x.numel() / K;
+  s.K = int32_t(K);
+  s.C = int32_t(C);
+  s.act = int32_t(integer(a[3]));
+  const auto lead = x.sizes().slice(0, x.dim() - 1);
+  auto like_x = [&](const char *name, const Tensor &t, int64_t cols) {
+    TORCH_CHECK_VALUE(t.dim() == x.dim() && t.sizes().slice(0, t.dim() - 1) == lead, what, ": ", name,
+                      " must have x's leading shape");
+    return matrix(what, name, t, s.M, cols);
+  };
+  if (tx) s.ldtx = like_x("tx", *tx, K);
+  if (res) s.ldres = like_x("residual", *res, C);
+  if (tres) s.ldtres = like_x("tresidual", *tres, C);
+  const OptTensor ow = w;
+  same_device(what, x, {&ow, &bias, &res, &tx, &tres});
+  const std::vector<int64_t> sizes = with_last(x, C);
+  OptTensor y = make(sizes, at::kBFloat16, x), ty, codes, scales;
+  if (tx) ty = make(sizes, at::kBFloat16, x);
+  if (a[7] == Py_True) {
+    codes = make({s.M, code_width(C)}, at::kChar, x);
+    scales = make({s.M, scale_width(C)}, at::kByte, x);
+  }
+  if (s.M > 0) {
+    size_t bytes = 0;
+    check(caj_linear_act_fwd_workspace(&s, tx.has_value(), &bytes), "caj_linear_act_fwd_workspace");
+    On on(x);
+    OptTensor ws;
+    if (bytes) ws = make({int64_t(bytes)}, at::kByte, x);
+    check(caj_linear_act_fwd(ptr(x), ptr(tx), ptr(w), ptr(bias), ptr(res), ptr(tres), &s, ptr(y), ptr(ty),
+                             static_cast<int8_t *>(ptr(codes)), bptr(scales), ptr(ws), bytes, on.stream),
+          "caj_linear_act_fwd");
+  }
+  return tuple_of({y, ty, codes, scales});
+  END_HANDLE_TH_ERRORS
+}
+
+// dy, x (or codes), x scales, w, act, z's codes, z's scales, want dx, want dw, want db
+PyObject *linear_act_bwd(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  const char *what = "linear_act_bwd";
+  expect(n, 10);
+  const Tensor &dy = tensor(a[0], what, "dy"), &w = tensor(a[3], what, "w");
+  const bool want_dx = a[7] == Py_True, want_dw = a[8] == Py_True, want_db = a[9] == Py_True;
+  const OptTensor x = want_dw ? maybe(a[1], what, "x") : std::nullopt;
+  const OptTensor x_scales = want_dw ? maybe(a[2], what, "x's scales") : std::nullopt;
+  const OptTensor codes = maybe(a[5], what, "pre"), scales = maybe(a[6], what, "pre's scales");
+  check_weight(what, w, std::nullopt);
+  TORCH_CHECK_VALUE(want_dx || want_dw || want_db, what, ": no gradient is wanted");
+  const int64_t C = w.size(0), K = w.size(1);
+  caj_linear_act_shape s{};
+  s.ldy = matrix(what, "dy", dy, -1, C);
+  s.M = dy.numel() / C;
+  s.K = int32_t(K);
+  s.C = int32_t(C);
+  s.act = int32_t(integer(a[4]));
+  if (want_dw) {
+    TORCH_CHECK_VALUE(x, what, ": dw needs x");
+    if (x_scales)
+      check_ckpt(what, *x, *x_scales, s.M, K);
+    else
+      s.ldx = matrix(what, "x", *x, s.M, K);
+  }
+  if (s.act == CAJ_ACT_NONE) {
+    TORCH_CHECK_VALUE(!codes, what, ": without an activation no checkpoint is read");
+  } else {
+    TORCH_CHECK_VALUE(codes && scales, what, ": an activation needs the checkpoint of z");
+    check_ckpt(what, *codes, *scales, s.M, C);
+  }
+  const OptTensor ow = w;
+  same_device(what, dy, {&ow, &x, &x_scales, &codes, &scales});
+  OptTensor dx, dw, db;
+  if (want_dx) dx = make(with_last(dy, K), at::kBFloat16, dy);
+  if (want_dw) dw = make({C, K}, at::kBFloat16, dy);
+  if (want_db) db = make({C}, at::kFloat, dy);
+  if (s.M > 0) {
+    size_t bytes = 0;
+    check(caj_linear_act_bwd_workspace(&s, x_scales.has_value(), &bytes), "caj_linear_act_bwd_workspace");
+    On on(dy);
+    OptTensor ws;
+    if (bytes) ws = make({int64_t(bytes)}, at::kByte, dy);
+    check(caj_linear_act_bwd(ptr(dy), ptr(x), bptr(x_scales), ptr(w), static_cast<const int8_t *>(ptr(codes)), bptr(scales),
+                             &s, ptr(dx), ptr(dw), fptr(db), ptr(ws), bytes, on.stream),
+          "caj_linear_act_bwd");
+  } else {
+    if (dw) dw->zero_();
+    if (db) db->zero_();
+  }
+  return tuple_of({dx, dw, db});
+  END_HANDLE_TH_ERRORS
+}
+
+#define FAST(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
+PyMethodDef methods[] = {FAST(ckpt8_pack),       FAST(ckpt8_unpack),     FAST(rope_table),     FAST(qk_norm_rope_fwd),
+                         FAST(qk_norm_rope_bwd), FAST(linear_act_fwd), FAST(linear_act_bwd), {nullptr, nullptr, 0, nullptr}};
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_block", "Block operators: tensor checks, outputs and the library calls.",
+                      -1, methods, nullptr, nullptr, nullptr, nullptr};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__block() { return PyModule_Create(&module); }
