@@ -54,11 +54,11 @@ def _build_ext() -> None:
     import sysconfig
 
     import torch
-    from torch.utils import cpp_extension
 
-    torch_lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    torch_dir = os.path.dirname(torch.__file__)
+    torch_lib, torch_inc = os.path.join(torch_dir, "lib"), os.path.join(torch_dir, "include")
     cuda_inc = os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")
-    incs = [INCLUDE, *cpp_extension.include_paths(), sysconfig.get_path("include"), cuda_inc]
+    incs = [INCLUDE, torch_inc, os.path.join(torch_inc, "torch", "csrc", "api", "include"), sysconfig.get_path("include"), cuda_inc]
     tmp = EXT + f".tmp{os.getpid()}"
     # the system's g++, as nvcc uses: a compiler that links its own static libstdc++ would put
     # a second, uninitialised C++ runtime beside torch's, and the first formatted error crashes

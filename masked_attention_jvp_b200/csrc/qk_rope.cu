@@ -153,49 +153,30 @@ __device__ __forceinline__ float dot(const uint64_t (&a)[4], const uint64_t (&b)
   return x + y;
 }
 
-// A thread's rotation. Interleaved: (u, w) -> (u, w) (c, c) + (w, u) (-s, s). Half: the
-// partner's channels are `hop` lanes away, x -> x c + partner * (-s in the first half,
-// s in the second). BACK turns the other way. Channels past 2 P pass.
-template <bool HALF>
+// A thread's rotation of its eight channels. Interleaved: pairs within the thread, one
+// float4 of cosines and one of sines. Half: the partner's channels are `hop` lanes away,
+// x -> x c + partner * (-s in the first half, s in the second), packed two by two. BACK
+// turns the other way. Lanes past 2 P channels do not turn (cosine 1, sine 0).
+template <bool HALF, bool BACK>
 struct Turn {
-  uint64_t c[4], s[4];
+  static constexpr int kSlots = HALF ? 4 : 2;  // 16-byte pieces of the tables: cosines, then sines
+  float4 raw[kSlots];
   int hop;
-  bool on;
-  // Slots of 16 bytes that a thread's cosines and sines take in the tables.
-  static constexpr int kSlots = HALF ? 4 : 2;
-  // The table element of the thread's first angle at position n.
-  __device__ __forceinline__ static size_t place(const QkRopeParams &p, const Lane &l, int32_t n) {
-    if constexpr (HALF) return size_t(n) * p.P + (l.d0 < p.P ? l.d0 : l.d0 - p.P);
-    return size_t(n) * p.P + l.d0 / 2;
+  // The table element of the thread's first angle at position 0.
+  __device__ __forceinline__ static int32_t offset(const QkRopeParams &p, const Lane &l) {
+    return HALF ? (l.d0 < p.P ? l.d0 : l.d0 - p.P) : l.d0 / 2;
   }
-  // raw: cosines, then sines. BACK turns the other way; lanes that do not turn get 1 and 0.
-  template <bool BACK>
-  __device__ __forceinline__ void set(const QkRopeParams &p, const Lane &l, const float4 (&raw)[kSlots]) {
-    on = l.d0 < 2 * p.P;
+  __device__ __forceinline__ void rest() {
+#pragma unroll
+    for (int i = 0; i < kSlots; ++i) raw[i] = i < kSlots / 2 ? make_float4(1.f, 1.f, 1.f, 1.f) : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  __device__ __forceinline__ void set(const QkRopeParams &p, const Lane &l) {
     if constexpr (HALF) {
       const bool first = l.d0 < p.P;
-      hop = on ? (first ? p.P / 8 : -(p.P / 8)) : 0;
+      hop = l.d0 < 2 * p.P ? (first ? p.P / 8 : -(p.P / 8)) : 0;
       const float sg = first != BACK ? -1.f : 1.f;
-      const uint64_t sign = f2(sg, sg);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float4 cc = raw[i], ss = raw[2 + i];
-        c[2 * i] = on ? f2(cc.x, cc.y) : f2(1.f, 1.f);
-        c[2 * i + 1] = on ? f2(cc.z, cc.w) : f2(1.f, 1.f);
-        s[2 * i] = on ? mul2(f2(ss.x, ss.y), sign) : 0;
-        s[2 * i + 1] = on ? mul2(f2(ss.z, ss.w), sign) : 0;
-      }
-    } else {
-      const float4 cc = raw[0];
-      const float4 ss = BACK ? make_float4(-raw[1].x, -raw[1].y, -raw[1].z, -raw[1].w) : raw[1];
-      c[0] = f2(cc.x, cc.x);
-      c[1] = f2(cc.y, cc.y);
-      c[2] = f2(cc.z, cc.z);
-      c[3] = f2(cc.w, cc.w);
-      s[0] = f2(-ss.x, ss.x);
-      s[1] = f2(-ss.y, ss.y);
-      s[2] = f2(-ss.z, ss.z);
-      s[3] = f2(-ss.w, ss.w);
+      for (int i = 2; i < kSlots; ++i) raw[i] = make_float4(sg * raw[i].x, sg * raw[i].y, sg * raw[i].z, sg * raw[i].w);
     }
   }
   // Every lane of the warp comes here (the half layout shuffles).
@@ -207,14 +188,17 @@ struct Turn {
         float u, w;
         f2_split(x[i], u, w);
         const uint64_t other = f2(__shfl_sync(0xFFFFFFFFu, u, src), __shfl_sync(0xFFFFFFFFu, w, src));
-        x[i] = fma2(x[i], c[i], mul2(other, s[i]));
+        const float4 cc = raw[i / 2], ss = raw[2 + i / 2];
+        x[i] = fma2(x[i], i & 1 ? f2(cc.z, cc.w) : f2(cc.x, cc.y), mul2(other, i & 1 ? f2(ss.z, ss.w) : f2(ss.x, ss.y)));
       }
-    } else if (on) {
+    } else {
+      const float c[4] = {raw[0].x, raw[0].y, raw[0].z, raw[0].w}, s[4] = {raw[1].x, raw[1].y, raw[1].z, raw[1].w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         float u, w;
         f2_split(x[i], u, w);
-        x[i] = fma2(x[i], c[i], mul2(f2(w, u), s[i]));
+        x[i] = BACK ? f2(fmaf(u, c[i], w * s[i]), fmaf(w, c[i], -u * s[i]))
+                    : f2(fmaf(u, c[i], -w * s[i]), fmaf(w, c[i], u * s[i]));
       }
     }
   }
@@ -269,19 +253,17 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 3 : 1) qk_rope_fwd_kernel(
       if (TAN) traw[i] = v8::load(static_cast<const T *>(p.tx[i]) + tok * p.tld[i] + 8 * l.vec);
     }
   }
-  Turn<HALF> turn;
-  float4 angles[Turn<HALF>::kSlots];
-#pragma unroll
-  for (int i = 0; i < Turn<HALF>::kSlots; ++i) angles[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  Turn<HALF, false> turn;
+  turn.rest();
   if (here && l.d0 < 2 * p.P) {
-    const size_t at = Turn<HALF>::place(p, l, n);
+    const size_t at = size_t(n) * p.P + turn.offset(p, l);
 #pragma unroll
-    for (int i = 0; i < Turn<HALF>::kSlots / 2; ++i) {
-      angles[i] = __ldg(reinterpret_cast<const float4 *>(p.cos + at) + i);
-      angles[Turn<HALF>::kSlots / 2 + i] = __ldg(reinterpret_cast<const float4 *>(p.sin + at) + i);
+    for (int i = 0; i < turn.kSlots / 2; ++i) {
+      turn.raw[i] = __ldg(reinterpret_cast<const float4 *>(p.cos + at) + i);
+      turn.raw[turn.kSlots / 2 + i] = __ldg(reinterpret_cast<const float4 *>(p.sin + at) + i);
     }
   }
-  turn.template set<false>(p, l, angles);
+  turn.set(p, l);
   auto place = [&](int i) { return ((size_t(b) * heads[i] + l.head) * p.N + n) * p.D + l.d0; };
   if (on[2]) {
     v8::store(static_cast<T *>(p.y[2]) + place(2), raw[2]);
@@ -368,120 +350,141 @@ constexpr size_t kMaxSmem = 232448;
 // and goes through registers.
 template <typename T, bool CK, bool HALF>
 constexpr int bwd_slots() {
-  return 2 * int(sizeof(T) / 2) + (CK ? 2 : 2 * int(sizeof(T) / 2)) + Turn<HALF>::kSlots;
+  return 2 * int(sizeof(T) / 2) + (CK ? 2 : 2 * int(sizeof(T) / 2)) + Turn<HALF, true>::kSlots;
 }
 
-// p.blocks blocks walk over the tokens, T of them at a time each, so the gains' gradient
-// stays in registers for a block's whole run; block i leaves its partial dg in
-// p.partial[q or k][i]. What a token needs comes through a ring of asynchronous copies,
-// two tokens ahead: with plain loads the kernel waited for memory half of its time.
-// CK: xq and xk are 8-bit checkpoints.
+// Each of p.blocks blocks walks over a run of neighbouring tokens, T at a time, so the
+// gains' gradient stays in registers for the whole run and addresses only step on; block
+// i leaves its partial dg in p.partial[q or k][i]. What a token needs comes through a
+// ring of asynchronous copies, up to two tokens ahead: with plain loads the kernel waited
+// for memory half of its time. CK: xq and xk are 8-bit checkpoints.
 template <typename T, bool CK, bool HALF, int MAXT>
-__global__ void __launch_bounds__(MAXT, MAXT == 256 ? 3 : 1) qk_rope_bwd_kernel(const QkRopeParams p) {
+__global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) qk_rope_bwd_kernel(const QkRopeParams p) {
   extern __shared__ __align__(16) uint8_t smem[];
+  using Rot = Turn<HALF, true>;
   constexpr int kVec = int(sizeof(T) / 2);  // slots of a vector of T
-  constexpr int kSlots = bwd_slots<T, CK, HALF>(), kAngles = kSlots - Turn<HALF>::kSlots;
+  constexpr int kSlots = bwd_slots<T, CK, HALF>(), kAngles = kSlots - Rot::kSlots;
   float *red = reinterpret_cast<float *>(smem + size_t(p.ring) * kSlots * 16 * blockDim.x);
   const Lane l = lane_of(p);
   const int32_t rows = p.B * p.N, stride = 16 * int32_t(blockDim.x);
   const uint32_t mine = ptx::smem_u32(smem) + 16 * threadIdx.x;
   const int32_t heads[3] = {p.Hq, p.Hk, p.dy[2] ? p.Hk : 0};
-  const bool normed = p.norm != kNormNone, in_t = l.t < l.T;
-  uint64_t dg[2][4];
+  const bool normed = p.norm != kNormNone, turns = l.d0 < 2 * p.P;
+  const bool has[3] = {l.t < l.T && l.head < heads[0], l.t < l.T && l.head < heads[1], l.t < l.T && l.head < heads[2]};
+  uint64_t dg[2][4], g[2][4];
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int i = 0; i < 2; ++i) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) dg[i][j] = 0;
+    for (int j = 0; j < 4; ++j) dg[i][j] = g[i][j] = 0;
+    if (normed && has[i]) load_pairs(p.g[i] + (p.gain_full ? 8 * l.vec : l.d0), g[i]);
+  }
 
-  const int32_t step = p.blocks * l.T;
-  auto fetch = [&](int64_t tok, uint32_t slot0) {
-    if (in_t && tok < rows) {
-      const int32_t b = int32_t(tok) / p.N, n = int32_t(tok) - b * p.N;
-      if (l.d0 < 2 * p.P) {
-        const size_t at = Turn<HALF>::place(p, l, n);
+  // this thread's tokens: tok0, tok0 + T, ... below end
+  const int32_t rounds = (rows + p.blocks * l.T - 1) / (p.blocks * l.T);
+  const int64_t tok0 = int64_t(blockIdx.x) * rounds * l.T + l.t;
+  const int64_t end = min(int64_t(rows), (int64_t(blockIdx.x) + 1) * rounds * l.T);
+  // A place in the walk: the token, its position, and its row in the [B, heads, N, D] tensors
+  // (the row of head 0, for the wider tensor's and the narrower one's number of heads).
+  struct Walk {
+    int64_t tok;
+    int32_t n, b;
+  };
+  auto start = [&](int64_t tok) {
+    Walk w;
+    w.tok = tok;
+    w.b = int32_t(tok / p.N);
+    w.n = int32_t(tok - int64_t(w.b) * p.N);
+    return w;
+  };
+  auto advance = [&](Walk &w) {
+    w.tok += l.T;
+    w.n += l.T;
+    while (w.n >= p.N) {
+      w.n -= p.N;
+      ++w.b;
+    }
+  };
+  auto head_row = [&](const Walk &w, int i) {  // element of (b, head, n, d0)
+    return (int64_t(w.b) * heads[i] + l.head) * p.N * p.D + int64_t(w.n) * p.D + l.d0;
+  };
+  auto fetch = [&](const Walk &w, uint32_t slot0) {
+    if (w.tok < end) {
+      if (turns && l.t < l.T) {
+        const int64_t at = int64_t(w.n) * p.P + Rot::offset(p, l);
 #pragma unroll
-        for (int i = 0; i < Turn<HALF>::kSlots / 2; ++i) {
+        for (int i = 0; i < Rot::kSlots / 2; ++i) {
           copy16(slot0 + (kAngles + i) * stride, p.cos + at + 4 * i);
-          copy16(slot0 + (kAngles + Turn<HALF>::kSlots / 2 + i) * stride, p.sin + at + 4 * i);
+          copy16(slot0 + (kAngles + Rot::kSlots / 2 + i) * stride, p.sin + at + 4 * i);
         }
       }
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        if (l.head >= heads[i]) continue;
-        copy_vec(slot0 + i * kVec * stride, stride,
-                 static_cast<const T *>(p.dy[i]) + ((size_t(b) * heads[i] + l.head) * p.N + n) * p.D + l.d0);
-      }
-      if (normed) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          if (l.head >= heads[i]) continue;
-          const uint32_t at = slot0 + (2 * kVec + i * (CK ? 1 : kVec)) * stride;
-          if constexpr (CK) {
-            const int32_t width = heads[i] * p.D;
-            copy8(at, static_cast<const int8_t *>(p.x[i]) + size_t(tok) * width + 8 * l.vec);
-            copy4(at + 8, p.x_scales[i] + size_t(tok) * ck::scale_bytes(width) + (l.vec / 16) * 4);
-          } else {
-            copy_vec(at, stride, static_cast<const T *>(p.x[i]) + tok * p.ld[i] + 8 * l.vec);
-          }
+        if (!has[i]) continue;
+        copy_vec(slot0 + i * kVec * stride, stride, static_cast<const T *>(p.dy[i]) + head_row(w, i));
+        if (!normed) continue;
+        const uint32_t at = slot0 + (2 * kVec + i * (CK ? 1 : kVec)) * stride;
+        if constexpr (CK) {
+          const int32_t width = heads[i] * p.D;
+          copy8(at, static_cast<const int8_t *>(p.x[i]) + w.tok * width + 8 * l.vec);
+          copy4(at + 8, p.x_scales[i] + w.tok * ck::scale_bytes(width) + (l.vec / 16) * 4);
+        } else {
+          copy_vec(at, stride, static_cast<const T *>(p.x[i]) + w.tok * p.ld[i] + 8 * l.vec);
         }
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
 
-  int64_t tok = int64_t(blockIdx.x) * l.T + l.t;
-  const int64_t last = (int64_t(rows) - int64_t(blockIdx.x) * l.T + step - 1) / step;  // rounds of this block
-  for (int i = 0; i < p.ring - 1; ++i) fetch(tok + int64_t(i) * step, mine + i * kSlots * stride);
+  Walk now = start(tok0), next = now;
+  for (int i = 0; i < p.ring - 1; ++i) {
+    fetch(next, mine + i * kSlots * stride);
+    advance(next);
+  }
+  const float inv_len[2] = {1.f / float(p.norm == kNormHead ? p.D : heads[0] * p.D),
+                            1.f / float(p.norm == kNormHead ? p.D : heads[1] * p.D)};
   int at = 0, to = p.ring - 1;  // ring positions
-  for (int64_t round = 0; round < last; ++round, tok += step) {
-    fetch(tok + int64_t(p.ring - 1) * step, mine + to * kSlots * stride);
+  for (int32_t round = 0; round < rounds; ++round) {
+    fetch(next, mine + to * kSlots * stride);
+    advance(next);
     const uint32_t slot0 = mine + at * kSlots * stride;
-    const bool here = in_t && tok < rows;
+    const bool here = now.tok < end;
+    const bool on[3] = {here && has[0], here && has[1], here && has[2]};
     v8::Raw<T> dv = v8::zero<T>();
-    const bool on_v = here && l.head < heads[2];
-    if (on_v) {
-      const int32_t b = int32_t(tok) / p.N, n = int32_t(tok) - b * p.N;
-      dv = v8::load(static_cast<const T *>(p.dy[2]) + ((size_t(b) * heads[2] + l.head) * p.N + n) * p.D + l.d0);
-    }
+    if (on[2]) dv = v8::load(static_cast<const T *>(p.dy[2]) + head_row(now, 2));
     if (p.ring == 3)
       asm volatile("cp.async.wait_group 2;" ::: "memory");
     else if (p.ring == 2)
       asm volatile("cp.async.wait_group 1;" ::: "memory");
     else
       asm volatile("cp.async.wait_group 0;" ::: "memory");
-    Turn<HALF> turn;
-    {
-      float4 angles[Turn<HALF>::kSlots];
+    // (slots of tokens or heads that are not there hold anything: nothing below lets it
+    // past the `on` conditions, and a head's lanes are all there or all not)
+    Rot turn;
+    turn.rest();
+    if (turns) {
 #pragma unroll
-      for (int i = 0; i < Turn<HALF>::kSlots; ++i) {
-        uint4 w = make_uint4(0, 0, 0, 0);
-        if (here && l.d0 < 2 * p.P) w = lds16(slot0 + (kAngles + i) * stride);
-        angles[i] = make_float4(__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w));
+      for (int i = 0; i < Rot::kSlots; ++i) {
+        const uint4 w = lds16(slot0 + (kAngles + i) * stride);
+        turn.raw[i] = make_float4(__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w));
       }
-      turn.template set<true>(p, l, angles);
     }
+    turn.set(p, l);
     uint64_t u[2][4], x[2][4];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const bool on = here && l.head < heads[i];
-      v8::Raw<T> r = v8::zero<T>();
-      if (on) r = lds_vec<T>(slot0 + i * kVec * stride, stride);
-      unpack(r, u[i]);
+      unpack(lds_vec<T>(slot0 + i * kVec * stride, stride), u[i]);
       turn.apply(u[i]);
       if (!normed) continue;
       const uint32_t xs = slot0 + (2 * kVec + i * (CK ? 1 : kVec)) * stride;
       if constexpr (CK) {
-        uint4 w = make_uint4(0, 0, 0, 0);
-        if (on) w = lds16(xs);
+        const uint4 w = lds16(xs);
         const float unit = ck::unit_of((w.z >> (8 * ((l.vec >> 2) & 3))) & 0xFFu);
         float f[8];
         ck::unpack_codes4(w.x, unit, f[0], f[1], f[2], f[3]);
         ck::unpack_codes4(w.y, unit, f[4], f[5], f[6], f[7]);
         pairs_of(f, x[i]);
       } else {
-        v8::Raw<T> rx = v8::zero<T>();
-        if (on) rx = lds_vec<T>(xs, stride);
-        unpack(rx, x[i]);
+        unpack(lds_vec<T>(xs, stride), x[i]);
       }
     }
     if (normed) {
@@ -490,23 +493,17 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 3 : 1) qk_rope_bwd_kernel(
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) gu[i][j] = 0;
-        if (here && l.head < heads[i]) {
-          load_pairs(p.g[i] + (p.gain_full ? 8 * l.vec : l.d0), gu[i]);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) gu[i][j] = mul2(gu[i][j], u[i][j]);
-        }
-        sums[i] = dot(x[i], x[i]);
-        sums[2 + i] = dot(x[i], gu[i]);
+        for (int j = 0; j < 4; ++j) gu[i][j] = mul2(g[i][j], u[i][j]);
+        sums[i] = on[i] ? dot(x[i], x[i]) : 0.f;
+        sums[2 + i] = on[i] ? dot(x[i], gu[i]) : 0.f;
       }
       group_sums(sums, l, p, red);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const float inv_len = 1.f / float(p.norm == kNormHead ? p.D : heads[i] * p.D);
-        const float inv = rsqrtf(fmaf(sums[i], inv_len, p.eps));
-        const float k3 = -(inv * inv * inv * (sums[2 + i] * inv_len));
+        const float inv = rsqrtf(fmaf(sums[i], inv_len[i], p.eps));
+        const float k3 = -(inv * inv * inv * (sums[2 + i] * inv_len[i]));
         const uint64_t inv2 = f2(inv, inv), k32 = f2(k3, k3);
-        if (here && l.head < heads[i]) {
+        if (on[i]) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             dg[i][j] = fma2(u[i][j], mul2(x[i][j], inv2), dg[i][j]);
@@ -517,9 +514,9 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 3 : 1) qk_rope_bwd_kernel(
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-      if (here && l.head < heads[i])
-        v8::store(static_cast<T *>(p.dx[i]) + tok * (int64_t(heads[i]) * p.D) + 8 * l.vec, pack<T>(u[i]));
-    if (on_v) v8::store(static_cast<T *>(p.dx[2]) + tok * (int64_t(heads[2]) * p.D) + 8 * l.vec, dv);
+      if (on[i]) v8::store(static_cast<T *>(p.dx[i]) + now.tok * (heads[i] * p.D) + 8 * l.vec, pack<T>(u[i]));
+    if (on[2]) v8::store(static_cast<T *>(p.dx[2]) + now.tok * (heads[2] * p.D) + 8 * l.vec, dv);
+    advance(now);
     at = at + 1 == p.ring ? 0 : at + 1;
     to = to + 1 == p.ring ? 0 : to + 1;
   }
@@ -530,7 +527,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 3 : 1) qk_rope_bwd_kernel(
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     __syncthreads();
-    if (in_t) {
+    if (l.t < l.T) {
       float f[8];
       singles_of(dg[i], f);
 #pragma unroll
@@ -575,6 +572,8 @@ int32_t threads_for(const QkRopeParams &p) {
   return (V * t + 31) & ~31;
 }
 
+// Blocks of the backward that an SM holds (registers: 512 threads).
+int32_t qk_rope_resident(int32_t threads) { return threads >= 512 ? 1 : 512 / threads; }
 int32_t vectors(const QkRopeParams &p) { return (p.Hq > p.Hk ? p.Hq : p.Hk) * p.D / 8; }
 int64_t groups_for(const QkRopeParams &p) {  // blocks that hold all tokens, T each
   const int32_t T = threads_for(p) / vectors(p);
@@ -607,8 +606,11 @@ cudaError_t launch_bwd(const QkRopeParams &params, cudaStream_t stream) {
   QkRopeParams p = params;
   const int32_t threads = threads_for(p);
   const size_t token = size_t(bwd_slots<T, CK, HALF>()) * 16 * threads, extra = token_norm_bytes(p, 4);
+  // the deepest ring with which the blocks that the grid counts on fit an SM (228 KB, 1 KB
+  // of it reserved a block); one block a SM for wide tokens
+  const size_t resident = size_t(qk_rope_resident(threads));
   p.ring = kRing;
-  while (p.ring > 1 && p.ring * token + extra > kMaxSmem) --p.ring;
+  while (p.ring > 1 && (p.ring * token + extra > kMaxSmem || resident * (p.ring * token + extra + 1024) > 233472)) --p.ring;
   static std::atomic<uint64_t> set_up{0};
   cudaError_t e = once_per_device(set_up, [&] {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kMaxSmem));
@@ -658,7 +660,7 @@ int32_t qk_rope_bwd_blocks(int32_t B, int32_t N, int32_t Hq, int32_t Hk, int32_t
   p.Hq = Hq;
   p.Hk = Hk;
   p.D = D;
-  const int64_t groups = groups_for(p), most = 148 * int64_t(768 / threads_for(p) < 1 ? 1 : 768 / threads_for(p));
+  const int64_t groups = groups_for(p), most = 148 * int64_t(qk_rope_resident(threads_for(p)));
   return int32_t(groups < most ? groups : most);
 }
 
