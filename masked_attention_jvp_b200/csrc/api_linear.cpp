@@ -13,48 +13,49 @@ namespace {
 
 caj_status done(cudaError_t e) { return e == cudaSuccess ? CAJ_OK : caj::cuda_fail(e); }
 
-constexpr int64_t kTileRows = 256, kTileCols = 256, kBlock = 64;
+constexpr int64_t kTileRows = 256, kBlock = 64;
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 size_t padded(int64_t bytes) { return size_t((bytes + 255) & ~int64_t(255)); }
 
-// In how many parts a contraction of k_blocks runs when there are `tiles` output
-// tiles and `elems` outputs. 74 pairs of SMs work at a time; a block of the
-// contraction takes a pair about 0.4 us and a tile 1.5 us besides, and the parts
-// are written and read again (about 5 TB/s) by one more launch (3 us). The least
-// estimate wins; the numbers only weigh one split against another.
-int32_t pick_splits(int64_t tiles, int64_t k_blocks, int64_t elems) {
-  int32_t best = 1;
+struct Plan {
+  int32_t m_tiles, n_tiles, k_blocks, splits, split_blocks, tile_cols;
+  int64_t part_rows, part_bytes;
+};
+// rows x cols outputs (and as many tangents), contraction of `depth`: the width of the
+// tiles and in how many parts the contraction runs, by the least estimate of
+//   waves * (blocks of a part * block time + tile time) + parts written and read again.
+// 74 pairs of SMs work at a time; a 64-wide block of the contraction takes a pair 0.40 us
+// at 256 columns and 0.23 us at 128, a tile 1.5 us (1.0) besides; parts cost 8 bytes an
+// output at about 5 TB/s and a launch (3 us). The figures only weigh one shape against
+// another. Measured on B200 (primal and tangent, 1560 tokens, 1536 x 1536): WIDE us with
+// 78 tiles of 256 columns, NARROW us with 156 of 128.
+Plan plan(int64_t rows, int64_t cols, int64_t depth, bool tangent) {
+  Plan best{};
   double best_us = 0;
-  for (int32_t s = 1; s <= 32 && s <= k_blocks; ++s) {
-    const int64_t per = ceil_div(k_blocks, s);
-    if (ceil_div(k_blocks, per) != s) continue;  // a part would be empty
-    const double us = double(ceil_div(tiles * s, 74)) * (0.4 * double(per) + 1.5) +
-                      (s > 1 ? 3.0 + 8.0 * s * double(elems) / 5e6 : 0.0);
-    if (s == 1 || us < best_us) {
-      best = s;
+  const int64_t tile_rows = tangent ? kTileRows / 2 : kTileRows, ops = tangent ? 2 : 1;
+  const int64_t m_tiles = ceil_div(rows, tile_rows), k_blocks = ceil_div(depth, kBlock);
+  for (const int32_t tile_cols : {256, 128}) {
+    const int64_t n_tiles = ceil_div(cols, tile_cols), tiles = m_tiles * n_tiles;
+    const double block_us = tile_cols == 256 ? 0.40 : 0.23, tile_us = tile_cols == 256 ? 1.5 : 1.0;
+    for (int32_t s = 1; s <= 32 && s <= k_blocks; ++s) {
+      const int64_t per = ceil_div(k_blocks, s);
+      if (ceil_div(k_blocks, per) != s) continue;  // a part would be empty
+      const double us = double(ceil_div(tiles * s, 74)) * (block_us * double(per) + tile_us) +
+                        (s > 1 ? 3.0 + 8.0 * s * double(rows * cols * ops) / 5e6 : 0.0);
+      if (best.splits && us >= best_us) continue;
       best_us = us;
+      best.m_tiles = int32_t(m_tiles);
+      best.n_tiles = int32_t(n_tiles);
+      best.k_blocks = int32_t(k_blocks);
+      best.splits = s;
+      best.split_blocks = int32_t(per);
+      best.tile_cols = tile_cols;
+      best.part_rows = m_tiles * tile_rows;
+      best.part_bytes = s > 1 ? int64_t(s) * ops * best.part_rows * cols * 4 : 0;
     }
   }
   return best;
-}
-
-struct Plan {
-  int32_t m_tiles, n_tiles, k_blocks, splits, split_blocks;
-  int64_t part_rows, part_bytes;
-};
-// rows x cols outputs (and as many tangents), contraction of `depth`.
-Plan plan(int64_t rows, int64_t cols, int64_t depth, bool tangent) {
-  Plan p{};
-  const int64_t tile_rows = tangent ? kTileRows / 2 : kTileRows, ops = tangent ? 2 : 1;
-  p.m_tiles = int32_t(ceil_div(rows, tile_rows));
-  p.n_tiles = int32_t(ceil_div(cols, kTileCols));
-  p.k_blocks = int32_t(ceil_div(depth, kBlock));
-  p.splits = pick_splits(int64_t(p.m_tiles) * p.n_tiles, p.k_blocks, rows * cols * ops);
-  p.split_blocks = int32_t(ceil_div(p.k_blocks, p.splits));
-  p.part_rows = p.m_tiles * tile_rows;
-  p.part_bytes = p.splits > 1 ? int64_t(p.splits) * ops * p.part_rows * cols * 4 : 0;
-  return p;
 }
 bool few_rows(int64_t M, bool tangent) { return (tangent ? 2 : 1) * M <= caj::kLinearFewRows; }
 
@@ -68,6 +69,7 @@ bool use_plan(caj::LinearParams *p, const Plan &pl, int64_t rows, int64_t cols, 
   p->k_blocks = pl.k_blocks;
   p->splits = pl.splits;
   p->split_blocks = pl.split_blocks;
+  p->tile_cols = pl.tile_cols;
   p->part_rows = pl.part_rows;
   p->part = static_cast<float *>(workspace);
   p->timeout_ns = caj::wait_timeout_ns();
@@ -83,7 +85,7 @@ caj_status check_shape(const caj_linear_act_shape *s) {
   // rows, tiles and parts are counted in 32 bits
   if (s->M > (int64_t(1) << 30) || s->K > (1 << 24) || s->C > (1 << 24)) return CAJ_ERR_UNSUPPORTED;
   const int64_t limit = (int64_t(1) << 31) - 1;
-  if (ceil_div(s->M, 128) * ceil_div(std::max(s->K, s->C), 256) > limit / 32) return CAJ_ERR_UNSUPPORTED;
+  if (ceil_div(s->M, 128) * ceil_div(std::max(s->K, s->C), 128) > limit / 32) return CAJ_ERR_UNSUPPORTED;
   if (s->M > limit / ceil_div(std::max(s->K, s->C), 32)) return CAJ_ERR_UNSUPPORTED;  // checkpoint blocks
   return CAJ_OK;
 }
@@ -169,7 +171,7 @@ caj_status caj_linear_act_fwd(const void *x, const void *tx, const void *w, cons
   } else {
     ok = use_plan(&p, pl, M, C, K, tan, workspace) &&
          caj::encode_map_2d_ld(&p.tm_a, x, M, K, shape->ldx, tan ? 64 : 128) &&
-         caj::encode_map_2d_ld(&p.tm_b, w, C, K, K, 128) && caj::encode_map_2d_ld(&p.tm_y, y, M, C, C, 32);
+         caj::encode_map_2d_ld(&p.tm_b, w, C, K, K, pl.tile_cols / 2) && caj::encode_map_2d_ld(&p.tm_y, y, M, C, C, 32);
     if (ok && tan)
       ok = caj::encode_map_2d_ld(&p.tm_a2, tx, M, K, shape->ldtx, 64) &&
            caj::encode_map_2d_ld(&p.tm_y2, ty, M, C, C, 32);

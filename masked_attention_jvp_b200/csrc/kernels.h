@@ -188,7 +188,8 @@ struct QkRopeParams {
 };
 
 // Matrix products of the linear operators; the operands' maps have 128-byte-swizzled
-// boxes of 64 bf16 columns (K-major operands: 128 rows, 64 with tangents; MN-major: 64).
+// boxes of 64 bf16 columns (K-major A: 128 rows, 64 with tangents; K-major B: half a
+// tile's columns; MN-major: 64).
 constexpr int32_t kLinearFewRows = 8;  // rows (tangents counted) up to which W is streamed
 struct LinearParams {
   CUtensorMap tm_a, tm_a2, tm_b;  // x (or dz), tx, W (or x)
@@ -203,7 +204,7 @@ struct LinearParams {
   int64_t ld_x, ld_tx, ld_res, ld_tres;
   int64_t part_rows;
   int32_t M, N, K;                // output rows and columns, contraction
-  int32_t m_tiles, n_tiles, k_blocks, splits, split_blocks;
+  int32_t m_tiles, n_tiles, k_blocks, splits, split_blocks, tile_cols;
   int32_t nb, ns;
   int32_t act;
   int32_t fault_mode;             // test hook: 1 = the producer issues no copies

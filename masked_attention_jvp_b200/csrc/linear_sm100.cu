@@ -27,6 +27,9 @@
 //   warp 1      MMA issuer (the leader's)
 //   warps 2-9   epilogue: two warps per 32 rows, 128 columns each, so that an
 //               activation costs less than the products of the next tile.
+// Where 256-column tiles would leave the last wave of pairs mostly empty (a frame of
+// tokens: 78 tiles on 74 pairs), tiles of 128 columns are used: half the work each, a
+// little slower per product (A is copied twice as often).
 // Column blocks run fastest, so the pairs work on one band of A at a time and it is
 // read from DRAM once; weights stay in L2.
 //
@@ -60,19 +63,21 @@ using namespace ptx;
 
 __device__ uint32_t g_linear_error = 0;
 
-constexpr int TN = 256, TK = 64;
+constexpr int TK = 64;
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 32 * (2 + kEpiWarps);
-constexpr uint32_t A_BYTES = 128 * TK * 2, B_BYTES = 128 * TK * 2, STAGE_BYTES = A_BYTES + B_BYTES;
+constexpr uint32_t A_BYTES = 128 * TK * 2;
 constexpr uint32_t OUT_BYTES = 32 * 128;  // a warp's staging tile: 32 rows of 128 bytes
 constexpr uint32_t EX_BYTES = 32 * 128;   // a pair of warps' act'(z): 32 rows x 32 columns
-constexpr uint32_t kTmemCols = 512;
 
 enum : uint32_t { kSiteEmpty = 0x21, kSiteFull, kSiteAccEmpty, kSiteAccFull, kSiteExEmpty, kSiteExFull };
 
-template <bool JVP>
+// TN: columns of a tile, 256 or 128.
+template <bool JVP, int TN>
 struct Lay {
-  static constexpr int STAGES = JVP ? 5 : 6;
+  static constexpr uint32_t B_BYTES = TN / 2 * TK * 2, STAGE_BYTES = A_BYTES + B_BYTES;
+  static constexpr int STAGES = TN == 256 ? (JVP ? 5 : 6) : (JVP ? 7 : 8);
+  static constexpr uint32_t TMEM_COLS = 2 * TN;
   static constexpr uint32_t OFF_OUT = STAGES * STAGE_BYTES;
   static constexpr uint32_t OFF_EX = OFF_OUT + kEpiWarps * OUT_BYTES;
   static constexpr uint32_t OFF_BAR = OFF_EX + (JVP ? 4 * EX_BYTES : 0);
@@ -110,11 +115,25 @@ __device__ __forceinline__ void fence_async_smem_then_store(const CUtensorMap *m
   __syncwarp();
 }
 
+// A row's N scale bytes of one warp's columns. Two of them (128-column tiles) leave the
+// padding that rounds a row up to four to whoever stores the row's last pair.
+template <int N>
+__device__ __forceinline__ void store_scales(uint8_t *at, uint32_t word, int32_t blk, const LinearParams &p) {
+  if constexpr (N == 4) {
+    *reinterpret_cast<uint32_t *>(at) = word;
+  } else {
+    *reinterpret_cast<uint16_t *>(at) = uint16_t(word);
+    if (blk + 2 >= p.nb && blk + 4 <= p.ns) *reinterpret_cast<uint16_t *>(at + 2) = 0;
+  }
+}
+
 // JVP: tangent rows beside the primal's. AMN, BMN: the operand is MN-major. EPI:
 // bias, activation, residual and checkpoint (otherwise the plain product).
-template <bool JVP, bool AMN, bool BMN, bool EPI>
+template <bool JVP, bool AMN, bool BMN, bool EPI, int TN>
 __global__ void __launch_bounds__(kThreads, 1) linear_sm100_kernel(const __grid_constant__ LinearParams p) {
-  using L = Lay<JVP>;
+  using L = Lay<JVP, TN>;
+  constexpr uint32_t STAGE_BYTES = L::STAGE_BYTES, B_BYTES = L::B_BYTES;
+  constexpr int HN = TN / 2;            // columns of an epilogue warp
   constexpr int TM = JVP ? 128 : 256;  // tokens (or output rows) of a tile
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -152,7 +171,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_sm100_kernel(const __grid_
     prefetch_tmap(&p.tm_y);
     if (JVP) prefetch_tmap(&p.tm_y2);
   }
-  if (warp == 1) pair::tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+  if (warp == 1) pair::tmem_alloc(smem_u32(tmem_slot), L::TMEM_COLS);
   tc_fence_before();
   pair::sync_cluster();  // barriers of both CTAs initialised, tensor memory allocated
   tc_fence_after();
@@ -191,7 +210,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_sm100_kernel(const __grid_
           }
           if (BMN) {
             pair::load_2d(leader, sb, &p.tm_b, fb, n0, kb * TK);
-            pair::load_2d(leader, sb + B_BYTES / 2, &p.tm_b, fb, n0 + 64, kb * TK);
+            if (TN == 256) pair::load_2d(leader, sb + B_BYTES / 2, &p.tm_b, fb, n0 + 64, kb * TK);
           } else {
             pair::load_2d(leader, sb, &p.tm_b, fb, kb * TK, n0);
           }
@@ -224,7 +243,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_sm100_kernel(const __grid_
       // per 16-wide step of the contraction: 32 bytes along a K-major row, 16 rows of
       // 128 bytes of an MN-major block
       constexpr uint64_t A_STEP = AMN ? 128 : 2, B_STEP = BMN ? 128 : 2;
-      constexpr uint32_t A_LBO = AMN ? A_BYTES / 2 : 16, B_LBO = BMN ? B_BYTES / 2 : 16;
+      constexpr uint32_t A_LBO = AMN ? A_BYTES / 2 : 16, B_LBO = BMN ? 64 * TK * 2 : 16;
       uint32_t stage = 0, phase = 0, count = 0;
       bool ok = true;
       for (int32_t u = first; ok && u < n_units; u += step, ++count) {
@@ -267,7 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_sm100_kernel(const __grid_
     // outgrows the instruction cache (see the note at the top).
     const int q = warp & 3, half = (warp - 2) >> 2;
     const int op = JVP ? q >> 1 : 0;  // 1: this warp's rows are tangents
-    const uint32_t lane_taddr = tmem + (uint32_t(32 * q) << 16) + uint32_t(128 * half);
+    const uint32_t lane_taddr = tmem + (uint32_t(32 * q) << 16) + uint32_t(HN * half);
     const uint32_t sbuf = sbase + L::OFF_OUT + uint32_t(warp - 2) * OUT_BYTES;
     const uint32_t ex_id = uint32_t((q & 1) + 2 * half);
     const uint32_t ex = sbase + L::OFF_EX + ex_id * EX_BYTES;
@@ -280,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_sm100_kernel(const __grid_
     for (int32_t u = first; ok && u < n_units; u += step, ++count) {
       const int32_t t = u % n_tiles, split = u / n_tiles;
       const int32_t row0 = (t / p.n_tiles) * TM + int32_t(rank) * (TM / 2) + 32 * (JVP ? q & 1 : q);
-      const int32_t n0 = (t % p.n_tiles) * TN + 128 * half;
+      const int32_t n0 = (t % p.n_tiles) * TN + HN * half;
       const uint32_t buf = count & 1u, use = count >> 1;
       const bool rows_in = row0 < p.M;
       // residual, 64 columns ahead, coalesced: eight lanes a row, four rows at a time
@@ -298,10 +317,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_sm100_kernel(const __grid_
       tc_fence_after();
       uint32_t scale_word = 0;
 #pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
+      for (int c = 0; c < HN / 32; ++c) {
         uint32_t acc[32];
         tmem_ld32(lane_taddr + buf * TN + 32 * c, acc);
-        if (c == 3) {
+        if (c == HN / 32 - 1) {
           tc_fence_before();
           __syncwarp();
           if (lane == 0) pair::arrive_remote(acc_empty_leader + 8 * buf);
@@ -327,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_sm100_kernel(const __grid_
             for (int i = 0; i < 8; ++i)
               sts128(swz(sbuf, 4 * i + (lane >> 3), lane & 7), rv[i].x, rv[i].y, rv[i].z, rv[i].w);
             __syncwarp();
-            if (c == 0) fetch_residual(n0 + 64);
+            if (HN > 64 && c == 0) fetch_residual(n0 + 64);
           }
         }
         float v[32];
@@ -428,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_sm100_kernel(const __grid_
         if (c & 1) fence_async_smem_then_store(om, sbuf, cs - 32, row0, lane);
       }
       if (EPI && ok && p.codes && p.splits == 1 && op == 0 && rows_in && row0 + lane < p.M && n0 < 32 * p.nb)
-        *reinterpret_cast<uint32_t *>(p.scales + size_t(row0 + lane) * p.ns + n0 / 32) = scale_word;
+        store_scales<HN / 32>(p.scales + size_t(row0 + lane) * p.ns + n0 / 32, scale_word, n0 / 32, p);
     }
     if (lane == 0) pair::store_wait<0>();
     __syncwarp();
@@ -440,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_sm100_kernel(const __grid_
   pair::sync_cluster();
   if (warp == 1) {
     tc_fence_after();
-    pair::tmem_dealloc(tmem, kTmemCols);
+    pair::tmem_dealloc(tmem, L::TMEM_COLS);
   }
 }
 
@@ -704,9 +723,9 @@ __global__ void __launch_bounds__(256) column_sum_kernel(const float *part, int3
   }
 }
 
-template <bool JVP, bool AMN, bool BMN, bool EPI>
+template <bool JVP, bool AMN, bool BMN, bool EPI, int TN>
 cudaError_t launch_tiles(const LinearParams &p, cudaStream_t stream) {
-  auto kernel = linear_sm100_kernel<JVP, AMN, BMN, EPI>;
+  auto kernel = linear_sm100_kernel<JVP, AMN, BMN, EPI, TN>;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -717,7 +736,7 @@ cudaError_t launch_tiles(const LinearParams &p, cudaStream_t stream) {
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = Lay<JVP>::SMEM;
+  cfg.dynamicSmemBytes = Lay<JVP, TN>::SMEM;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
@@ -726,7 +745,7 @@ cudaError_t launch_tiles(const LinearParams &p, cudaStream_t stream) {
   static std::atomic<uint64_t> set_up{0};
   static std::atomic<int> max_pairs_of[64];
   e = once_per_device(set_up, [&] {
-    cudaError_t r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<JVP>::SMEM);
+    cudaError_t r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<JVP, TN>::SMEM);
     int sms = 0, pairs = 0;
     if (r == cudaSuccess) r = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (r == cudaSuccess) r = cudaOccupancyMaxActiveClusters(&pairs, kernel, &cfg);
@@ -743,6 +762,12 @@ cudaError_t launch_tiles(const LinearParams &p, cudaStream_t stream) {
   const int64_t threads = int64_t(p.M) * ck::blocks_of(p.N) * 4;
   linear_finish_kernel<JVP, EPI><<<unsigned((threads + 255) / 256), 256, 0, stream>>>(p);
   return cudaGetLastError();
+}
+
+template <bool JVP, bool AMN, bool BMN, bool EPI>
+cudaError_t launch_tiles(const LinearParams &p, cudaStream_t stream) {
+  return p.tile_cols == 128 ? launch_tiles<JVP, AMN, BMN, EPI, 128>(p, stream)
+                            : launch_tiles<JVP, AMN, BMN, EPI, 256>(p, stream);
 }
 
 template <int R>
