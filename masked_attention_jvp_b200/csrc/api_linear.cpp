@@ -74,8 +74,8 @@ bool use_plan(caj::LinearParams *p, const Plan &pl, int64_t rows, int64_t cols, 
   p->part = static_cast<float *>(workspace);
   p->timeout_ns = caj::wait_timeout_ns();
   p->fault_mode = caj::fault_mode();
-  return pl.splits == 1 || caj::encode_map_2d_f32(&p->tm_part, workspace, int64_t(pl.splits) * (tangent ? 2 : 1) * pl.part_rows,
-                                                  cols, cols, 32);
+  return pl.splits == 1 || caj::encode_out_2d(&p->tm_part, workspace, int64_t(pl.splits) * (tangent ? 2 : 1) * pl.part_rows, cols,
+                                              true);
 }
 
 caj_status check_shape(const caj_linear_act_shape *s) {
@@ -171,10 +171,10 @@ caj_status caj_linear_act_fwd(const void *x, const void *tx, const void *w, cons
   } else {
     ok = use_plan(&p, pl, M, C, K, tan, workspace) &&
          caj::encode_map_2d_ld(&p.tm_a, x, M, K, shape->ldx, tan ? 64 : 128) &&
-         caj::encode_map_2d_ld(&p.tm_b, w, C, K, K, pl.tile_cols / 2) && caj::encode_map_2d_ld(&p.tm_y, y, M, C, C, 32);
+         caj::encode_map_2d_ld(&p.tm_b, w, C, K, K, pl.tile_cols / 2) && caj::encode_out_2d(&p.tm_y, y, M, C, false);
     if (ok && tan)
       ok = caj::encode_map_2d_ld(&p.tm_a2, tx, M, K, shape->ldtx, 64) &&
-           caj::encode_map_2d_ld(&p.tm_y2, ty, M, C, C, 32);
+           caj::encode_out_2d(&p.tm_y2, ty, M, C, false);
   }
   if (!ok) return caj::cuda_fail(cudaErrorInvalidValue);
   return done(caj::launch_linear_fwd(p, static_cast<cudaStream_t>(stream)));
@@ -243,7 +243,7 @@ caj_status caj_linear_act_bwd(const void *dy, const void *x, const uint8_t *x_sc
     caj::LinearParams p{};
     p.y = dx;
     if (!use_plan(&p, b.dx, M, K, C, false, parts) || !caj::encode_map_2d_ld(&p.tm_a, dz, M, C, ld_dz, 128) ||
-        !caj::encode_map_2d_ld(&p.tm_b, w, C, K, K, 64) || !caj::encode_map_2d_ld(&p.tm_y, dx, M, K, K, 32))
+        !caj::encode_map_2d_ld(&p.tm_b, w, C, K, K, 64) || !caj::encode_out_2d(&p.tm_y, dx, M, K, false))
       return caj::cuda_fail(cudaErrorInvalidValue);
     st = done(caj::launch_linear_dx(p, s));
     if (st != CAJ_OK) return st;
@@ -268,7 +268,7 @@ caj_status caj_linear_act_bwd(const void *dy, const void *x, const uint8_t *x_sc
     caj::LinearParams p{};
     p.y = dw;
     if (!use_plan(&p, b.dw, C, K, M, false, parts) || !caj::encode_map_2d_ld(&p.tm_a, dz, M, C, ld_dz, 64) ||
-        !caj::encode_map_2d_ld(&p.tm_b, x, M, K, ld_x, 64) || !caj::encode_map_2d_ld(&p.tm_y, dw, C, K, K, 32))
+        !caj::encode_map_2d_ld(&p.tm_b, x, M, K, ld_x, 64) || !caj::encode_out_2d(&p.tm_y, dw, C, K, false))
       return caj::cuda_fail(cudaErrorInvalidValue);
     st = done(caj::launch_linear_dw(p, s));
   }

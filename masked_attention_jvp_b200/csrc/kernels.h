@@ -193,8 +193,8 @@ struct QkRopeParams {
 constexpr int32_t kLinearFewRows = 8;  // rows (tangents counted) up to which W is streamed
 struct LinearParams {
   CUtensorMap tm_a, tm_a2, tm_b;  // x (or dz), tx, W (or x)
-  CUtensorMap tm_y, tm_y2;        // outputs, boxes of 64 x 32
-  CUtensorMap tm_part;            // splits > 1: fp32 parts, boxes of 32 x 32
+  CUtensorMap tm_y, tm_y2;        // outputs, 64-byte-swizzled boxes of 32 columns x 32 rows
+  CUtensorMap tm_part;            // splits > 1: fp32 parts, boxes of 16 x 32
   const void *x, *tx, *w;         // few rows: x, tx, W themselves; tx also says whether there are tangents
   const void *bias, *res, *tres;  // bf16 or null
   void *y, *ty;                   // [M, N] bf16

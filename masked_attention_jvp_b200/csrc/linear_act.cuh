@@ -115,6 +115,26 @@ __device__ __forceinline__ void act_all(int32_t which, float (&v)[M], float (&sl
     act_of<kActNone, SLOPE>(v, sl);
 }
 
+// v *= act'(z)
+template <int ACT, int M>
+__device__ __forceinline__ void times_slope_of(const float (&z)[M], float (&v)[M]) {
+#pragma unroll
+  for (int i = 0; i < M; i += 2) {
+    uint64_t s = 0;
+    act2<ACT, true>(ptx::f2(z[i], z[i + 1]), s);
+    ptx::f2_split(ptx::mul2(ptx::f2(v[i], v[i + 1]), s), v[i], v[i + 1]);
+  }
+}
+template <int M>
+__device__ __forceinline__ void times_slope(int32_t which, const float (&z)[M], float (&v)[M]) {
+  if (which == kActGeluTanh)
+    times_slope_of<kActGeluTanh>(z, v);
+  else if (which == kActSilu)
+    times_slope_of<kActSilu>(z, v);
+  else if (which == kActGelu)
+    times_slope_of<kActGelu>(z, v);
+}
+
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 

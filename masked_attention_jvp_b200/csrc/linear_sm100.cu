@@ -8,7 +8,7 @@
 //   dx       dz [M, C] along the rows, W [C, K] across them (MN-major B)
 //   dW       dz [M, C] and x [M, K], contraction over the tokens: both MN-major
 //
-// Design (clusters of two CTAs, one CTA per SM, 10 warps per CTA):
+// Design (clusters of two CTAs, one CTA per SM, 18 warps per CTA, 10 for narrow tiles):
 //   A pair computes 256 x 256 tiles with tcgen05 cta_group::2 (M = 256, N = 256):
 //   each CTA loads its 128 rows of A and its 128 of the tile's 256 rows of B, 32 KiB
 //   per 64-wide block of the contraction, and the leader issues four products that
@@ -25,8 +25,11 @@
 //   tile would keep both in one thread, but copy 25% more.)
 //   warp 0      TMA producer (both CTAs)
 //   warp 1      MMA issuer (the leader's)
-//   warps 2-9   epilogue: two warps per 32 rows, 128 columns each, so that an
-//               activation costs less than the products of the next tile.
+//   warps 2-17  epilogue: four warps per 32 rows, 64 columns each. What an epilogue
+//               warp does to 32 columns is a few hundred dependent instructions
+//               (about 1200 cycles alone on its scheduler), so it takes four warps a
+//               scheduler to stay ahead of the products: EPI8 us with eight, EPI16
+//               with sixteen (32760 x 1536 -> 6144, tangents, GELU, checkpoint).
 // Where 256-column tiles would leave the last wave of pairs mostly empty (a frame of
 // tokens: 78 tiles on 74 pairs), tiles of 128 columns are used: half the work each, a
 // little slower per product (A is copied twice as often).
@@ -64,32 +67,37 @@ using namespace ptx;
 __device__ uint32_t g_linear_error = 0;
 
 constexpr int TK = 64;
-constexpr int kEpiWarps = 8;
-constexpr int kThreads = 32 * (2 + kEpiWarps);
 constexpr uint32_t A_BYTES = 128 * TK * 2;
-constexpr uint32_t OUT_BYTES = 32 * 128;  // a warp's staging tile: 32 rows of 128 bytes
-constexpr uint32_t EX_BYTES = 32 * 128;   // a pair of warps' act'(z): 32 rows x 32 columns
+constexpr uint32_t OUT_BYTES = 32 * 64;   // a staging tile of a warp: 32 rows of 32 bf16 (or 16 fp32)
+constexpr uint32_t EX_BYTES = 32 * 128;   // z on its way to the tangents' warp: 32 rows x 32 columns
 
 enum : uint32_t { kSiteEmpty = 0x21, kSiteFull, kSiteAccEmpty, kSiteAccFull, kSiteExEmpty, kSiteExFull };
 
-// TN: columns of a tile, 256 or 128.
+// TN: columns of a tile, 256 or 128. An epilogue warp has 32 rows and 64 columns.
 template <bool JVP, int TN>
 struct Lay {
+  static constexpr int EPI_WARPS = TN / 16, THREADS = 32 * (2 + EPI_WARPS);
   static constexpr uint32_t B_BYTES = TN / 2 * TK * 2, STAGE_BYTES = A_BYTES + B_BYTES;
-  static constexpr int STAGES = TN == 256 ? (JVP ? 5 : 6) : (JVP ? 7 : 8);
+  static constexpr int STAGES = TN == 256 ? 5 : 8;
   static constexpr uint32_t TMEM_COLS = 2 * TN;
+  static constexpr int OUT_BUFS = JVP ? 1 : 2, PAIRS = JVP ? EPI_WARPS / 2 : 0;
   static constexpr uint32_t OFF_OUT = STAGES * STAGE_BYTES;
-  static constexpr uint32_t OFF_EX = OFF_OUT + kEpiWarps * OUT_BYTES;
-  static constexpr uint32_t OFF_BAR = OFF_EX + (JVP ? 4 * EX_BYTES : 0);
+  static constexpr uint32_t OFF_EX = OFF_OUT + EPI_WARPS * OUT_BUFS * OUT_BYTES;
+  static constexpr uint32_t OFF_BAR = OFF_EX + PAIRS * EX_BYTES;
   // offsets from OFF_BAR
   static constexpr uint32_t FULL = 0, EMPTY = 8 * STAGES, ACC_FULL = 16 * STAGES, ACC_EMPTY = ACC_FULL + 16,
-                            DRAIN = ACC_EMPTY + 16, EX_FULL = DRAIN + 8, EX_EMPTY = EX_FULL + 32,
-                            TMEM_SLOT = EX_EMPTY + 32, ABORT = TMEM_SLOT + 4, END = ABORT + 4;
+                            DRAIN = ACC_EMPTY + 16, EX_FULL = DRAIN + 8, EX_EMPTY = EX_FULL + 8 * PAIRS,
+                            TMEM_SLOT = EX_EMPTY + 8 * PAIRS, ABORT = TMEM_SLOT + 4, END = ABORT + 4;
   static constexpr uint32_t SMEM = OFF_BAR + END + 1024;  // + slack for the 1 KiB alignment
   static_assert(SMEM <= 232448, "shared memory per CTA");
 };
 
-// The 16-byte unit `u` of row `row` in a 128-byte-swizzled tile at `base`.
+// The 16-byte unit `u` of row `row` in a tile of 64-byte rows, 64-byte-swizzled as the
+// copy engine has it; and in the exchange tiles' 128-byte rows. Eight lanes with the same
+// u meet eight different bank groups in both.
+__device__ __forceinline__ uint32_t swz64(uint32_t base, uint32_t row, uint32_t u) {
+  return base + row * 64u + ((u ^ ((row >> 1) & 3u)) << 4);
+}
 __device__ __forceinline__ uint32_t swz(uint32_t base, uint32_t row, uint32_t u) {
   return base + row * 128u + ((u ^ (row & 7u)) << 4);
 }
@@ -115,25 +123,19 @@ __device__ __forceinline__ void fence_async_smem_then_store(const CUtensorMap *m
   __syncwarp();
 }
 
-// A row's N scale bytes of one warp's columns. Two of them (128-column tiles) leave the
-// padding that rounds a row up to four to whoever stores the row's last pair.
-template <int N>
+// The two scale bytes of a row in one warp's 64 columns; the row's last pair also stores
+// the padding that rounds a row up to four.
 __device__ __forceinline__ void store_scales(uint8_t *at, uint32_t word, int32_t blk, const LinearParams &p) {
-  if constexpr (N == 4) {
-    *reinterpret_cast<uint32_t *>(at) = word;
-  } else {
-    *reinterpret_cast<uint16_t *>(at) = uint16_t(word);
-    if (blk + 2 >= p.nb && blk + 4 <= p.ns) *reinterpret_cast<uint16_t *>(at + 2) = 0;
-  }
+  *reinterpret_cast<uint16_t *>(at) = uint16_t(word);
+  if (blk + 2 >= p.nb && blk + 4 <= p.ns) *reinterpret_cast<uint16_t *>(at + 2) = 0;
 }
 
 // JVP: tangent rows beside the primal's. AMN, BMN: the operand is MN-major. EPI:
 // bias, activation, residual and checkpoint (otherwise the plain product).
 template <bool JVP, bool AMN, bool BMN, bool EPI, int TN>
-__global__ void __launch_bounds__(kThreads, 1) linear_sm100_kernel(const __grid_constant__ LinearParams p) {
+__global__ void __launch_bounds__((Lay<JVP, TN>::THREADS), 1) linear_sm100_kernel(const __grid_constant__ LinearParams p) {
   using L = Lay<JVP, TN>;
   constexpr uint32_t STAGE_BYTES = L::STAGE_BYTES, B_BYTES = L::B_BYTES;
-  constexpr int HN = TN / 2;            // columns of an epilogue warp
   constexpr int TM = JVP ? 128 : 256;  // tokens (or output rows) of a tile
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -154,10 +156,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_sm100_kernel(const __grid_
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(bars + L::ACC_FULL + 8 * b, 1);
-      mbar_init(bars + L::ACC_EMPTY + 8 * b, 2 * kEpiWarps);  // both CTAs' epilogue warps
+      mbar_init(bars + L::ACC_EMPTY + 8 * b, 2 * L::EPI_WARPS);  // both CTAs' epilogue warps
     }
     mbar_init(bars + L::DRAIN, 1);
-    for (int b = 0; b < 4; ++b) {
+    for (int b = 0; b < L::PAIRS; ++b) {
       mbar_init(bars + L::EX_FULL + 8 * b, 1);
       mbar_init(bars + L::EX_EMPTY + 8 * b, 1);
     }
@@ -282,91 +284,84 @@ __global__ void __launch_bounds__(kThreads, 1) linear_sm100_kernel(const __grid_
     }
   } else {
     // ---------------------------------------------------------- epilogue (both CTAs)
-    // Kept as loops of 32 columns: unrolled over a whole tile, the activations' code
+    // Loops of 32 columns, not unrolled: over a whole tile, the activations' code
     // outgrows the instruction cache (see the note at the top).
-    const int q = warp & 3, half = (warp - 2) >> 2;
+    const int q = warp & 3, cols = (warp - 2) >> 2;
     const int op = JVP ? q >> 1 : 0;  // 1: this warp's rows are tangents
-    const uint32_t lane_taddr = tmem + (uint32_t(32 * q) << 16) + uint32_t(HN * half);
-    const uint32_t sbuf = sbase + L::OFF_OUT + uint32_t(warp - 2) * OUT_BYTES;
-    const uint32_t ex_id = uint32_t((q & 1) + 2 * half);
+    const uint32_t lane_taddr = tmem + (uint32_t(32 * q) << 16) + uint32_t(64 * cols);
+    const uint32_t sbuf0 = sbase + L::OFF_OUT + uint32_t(warp - 2) * L::OUT_BUFS * OUT_BYTES;
+    const uint32_t ex_id = uint32_t((q & 1) + 2 * cols);
     const uint32_t ex = sbase + L::OFF_EX + ex_id * EX_BYTES;
     const uint32_t acc_empty_leader = pair::at_rank(bars + L::ACC_EMPTY, 0);
     const CUtensorMap *om = op ? &p.tm_y2 : &p.tm_y;
     const uint16_t *res = EPI && p.splits == 1 ? static_cast<const uint16_t *>(op ? p.tres : p.res) : nullptr;
     const int64_t ld_res = op ? p.ld_tres : p.ld_res;
-    uint32_t count = 0, exchanged = 0;
+    uint32_t count = 0, exchanged = 0, stores = 0;
     bool ok = true;
+    // the staging tile whose turn it is, once the copy engine has read what it held
+    auto next_tile = [&]() {
+      if (lane == 0) pair::store_wait_read<L::OUT_BUFS - 1>();
+      __syncwarp();
+      return sbuf0 + (stores++ % L::OUT_BUFS) * OUT_BYTES;
+    };
     for (int32_t u = first; ok && u < n_units; u += step, ++count) {
       const int32_t t = u % n_tiles, split = u / n_tiles;
       const int32_t row0 = (t / p.n_tiles) * TM + int32_t(rank) * (TM / 2) + 32 * (JVP ? q & 1 : q);
-      const int32_t n0 = (t % p.n_tiles) * TN + HN * half;
+      const int32_t n0 = (t % p.n_tiles) * TN + 64 * cols;
       const uint32_t buf = count & 1u, use = count >> 1;
       const bool rows_in = row0 < p.M;
-      // residual, 64 columns ahead, coalesced: eight lanes a row, four rows at a time
-      uint4 rv[8];
-      auto fetch_residual = [&](int32_t col0) {
+      // residual, a chunk ahead, coalesced: four lanes a row, eight rows at a time
+      uint4 rv[4];
+      auto fetch_residual = [&](int32_t cs) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int32_t r = row0 + 4 * i + (lane >> 3), cc = col0 + 8 * (lane & 7);
+        for (int i = 0; i < 4; ++i) {
+          const int32_t r = row0 + 8 * i + (lane >> 2), cc = cs + 8 * (lane & 3);
           rv[i] = make_uint4(0, 0, 0, 0);
           if (r < p.M && cc < p.N) rv[i] = __ldcs(reinterpret_cast<const uint4 *>(res + r * ld_res + cc));
         }
       };
       if (EPI && res) fetch_residual(n0);
+      uint32_t bias2 = 0;  // the bias of this lane's two columns, zero past the last
+      if (EPI && p.bias && op == 0 && n0 + 2 * lane < p.N)
+        bias2 = __ldg(reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(p.bias) + n0) + lane);
       if (!wait(bars + L::ACC_FULL + 8 * buf, use & 1u, kSiteAccFull)) break;
       tc_fence_after();
       uint32_t scale_word = 0;
 #pragma unroll 1
-      for (int c = 0; c < HN / 32; ++c) {
+      for (int c = 0; c < 2; ++c) {
         uint32_t acc[32];
         tmem_ld32(lane_taddr + buf * TN + 32 * c, acc);
-        if (c == HN / 32 - 1) {
+        if (c == 1) {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) pair::arrive_remote(acc_empty_leader + 8 * buf);
+          if (lane == 0) pair::arrive_remote_relaxed(acc_empty_leader + 8 * buf);
         }
         const int32_t cs = n0 + 32 * c;
-        // (the second half of a 64-column store goes on past the last column)
-        if (!rows_in || n0 + 64 * (c >> 1) >= p.N) continue;
-        if (p.splits > 1) {  // fp32 partial tiles
-          if (cs >= p.N) continue;
-          if (lane == 0) pair::store_wait_read<0>();
-          __syncwarp();
+        if (!rows_in || cs >= p.N) continue;
+        if (p.splits > 1) {  // fp32 parts, 16 columns at a time
 #pragma unroll
-          for (int g = 0; g < 8; ++g)
-            sts128(swz(sbuf, lane, g), acc[4 * g], acc[4 * g + 1], acc[4 * g + 2], acc[4 * g + 3]);
-          fence_async_smem_then_store(&p.tm_part, sbuf, cs, (split * (JVP ? 2 : 1) + op) * p.part_rows + row0, lane);
-          continue;
-        }
-        if ((c & 1) == 0) {  // a new 64-column staging tile
-          if (lane == 0) pair::store_wait_read<0>();
-          __syncwarp();
-          if (EPI && res) {
+          for (int h = 0; h < 2; ++h) {
+            if (cs + 16 * h >= p.N) continue;
+            const uint32_t sbuf = next_tile();
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              sts128(swz(sbuf, 4 * i + (lane >> 3), lane & 7), rv[i].x, rv[i].y, rv[i].z, rv[i].w);
-            __syncwarp();
-            if (HN > 64 && c == 0) fetch_residual(n0 + 64);
+            for (int g = 0; g < 4; ++g)
+              sts128(swz64(sbuf, lane, g), acc[16 * h + 4 * g], acc[16 * h + 4 * g + 1], acc[16 * h + 4 * g + 2],
+                     acc[16 * h + 4 * g + 3]);
+            fence_async_smem_then_store(&p.tm_part, sbuf, cs + 16 * h,
+                                        (split * (JVP ? 2 : 1) + op) * p.part_rows + row0, lane);
           }
+          continue;
         }
         float v[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(acc[i]);
         if (EPI) {
-          if (op == 0) {
-            if (p.bias) {
-              const uint4 *bp = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.bias) + cs);
+          if (op == 0 && p.bias) {
 #pragma unroll
-              for (int g = 0; g < 4; ++g) {
-                if (cs + 8 * g >= p.N) continue;
-                const uint4 w = __ldg(bp + g);
-                const uint32_t w4[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  v[8 * g + 2 * e] += lin::bf_lo(w4[e]);
-                  v[8 * g + 2 * e + 1] += lin::bf_hi(w4[e]);
-                }
-              }
+            for (int j = 0; j < 16; ++j) {
+              const uint32_t w = __shfl_sync(0xffffffffu, bias2, 16 * c + j);
+              v[2 * j] += lin::bf_lo(w);
+              v[2 * j + 1] += lin::bf_hi(w);
             }
           }
           if constexpr (JVP) {  // z crosses to the tangents' warp, which takes act'(z) itself
@@ -384,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_sm100_kernel(const __grid_
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bars + L::EX_FULL + 8 * ex_id);
               } else {
-                float z[32], sl[32];
+                float z[32];
 #pragma unroll
                 for (int g = 0; g < 8; ++g) {
                   const uint4 w = lds128(swz(ex, lane, g));
@@ -395,9 +390,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_sm100_kernel(const __grid_
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bars + L::EX_EMPTY + 8 * ex_id);
-                lin::act_all<true>(p.act, z, sl);
-#pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] *= sl[i];
+                lin::times_slope(p.act, z, v);
               }
               ++exchanged;
             }
@@ -429,9 +422,17 @@ __global__ void __launch_bounds__(kThreads, 1) linear_sm100_kernel(const __grid_
             }
           }
         }
+        const uint32_t sbuf = next_tile();
+        if (EPI && res) {  // rows arrive four lanes each, and are read back a lane each
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            sts128(swz64(sbuf, 8 * i + (lane >> 2), lane & 3), rv[i].x, rv[i].y, rv[i].z, rv[i].w);
+          __syncwarp();
+          if (c == 0) fetch_residual(n0 + 32);
+        }
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-          const uint32_t a = swz(sbuf, lane, 4 * (c & 1) + g);
+          const uint32_t a = swz64(sbuf, lane, g);
           float *f = v + 8 * g;
           if (EPI && res) {
             const uint4 w = lds128(a);
@@ -444,10 +445,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_sm100_kernel(const __grid_
           }
           sts128(a, pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
         }
-        if (c & 1) fence_async_smem_then_store(om, sbuf, cs - 32, row0, lane);
+        fence_async_smem_then_store(om, sbuf, cs, row0, lane);
       }
       if (EPI && ok && p.codes && p.splits == 1 && op == 0 && rows_in && row0 + lane < p.M && n0 < 32 * p.nb)
-        store_scales<HN / 32>(p.scales + size_t(row0 + lane) * p.ns + n0 / 32, scale_word, n0 / 32, p);
+        store_scales(p.scales + size_t(row0 + lane) * p.ns + n0 / 32, scale_word, n0 / 32, p);
     }
     if (lane == 0) pair::store_wait<0>();
     __syncwarp();
@@ -735,7 +736,7 @@ cudaError_t launch_tiles(const LinearParams &p, cudaStream_t stream) {
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(Lay<JVP, TN>::THREADS);
   cfg.dynamicSmemBytes = Lay<JVP, TN>::SMEM;
   cfg.stream = stream;
   cfg.attrs = attr;

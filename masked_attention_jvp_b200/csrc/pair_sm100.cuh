@@ -38,6 +38,13 @@ __device__ __forceinline__ void arrive_remote(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
+// The same without ordering this thread's memory accesses: for handing back tensor memory,
+// whose reads tcgen05.wait::ld and the tcgen05 fence order. (The release waits for every
+// earlier store of the thread to be performed, some 1000 cycles after stores to global.)
+__device__ __forceinline__ void arrive_remote_relaxed(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
 // 2-D tile load into this CTA's shared memory, completion counted on an mbarrier
 // of either CTA of the pair. x * element size must be a multiple of 16 bytes.
 __device__ __forceinline__ void load_2d(uint32_t pred, uint32_t dst, const CUtensorMap *m, uint32_t bar, int32_t x,
