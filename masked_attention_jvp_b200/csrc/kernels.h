@@ -190,7 +190,7 @@ struct QkRopeParams {
 // Matrix products of the linear operators; the operands' maps have 128-byte-swizzled
 // boxes of 64 bf16 columns (K-major A: 128 rows, 64 with tangents; K-major B: half a
 // tile's columns; MN-major: 64).
-constexpr int32_t kLinearFewRows = 8;  // rows (tangents counted) up to which W is streamed
+constexpr int32_t kLinearFewRows = 32;  // rows (tangents counted) up to which W is streamed
 struct LinearParams {
   CUtensorMap tm_a, tm_a2, tm_b;  // x (or dz), tx, W (or x)
   CUtensorMap tm_y, tm_y2;        // outputs, 64-byte-swizzled boxes of 32 columns x 32 rows

@@ -40,9 +40,9 @@
 // contraction is split, each part stores fp32 partial tiles, and a second kernel
 // adds them in a fixed order and does the epilogue. The split goes by sizes alone,
 // so results do not depend on the device's state.
-// Up to 8 rows (tokens being decoded, and their tangents) a tile would be almost
-// empty and the weights' bytes are all there is: rows_kernel streams W once through
-// CUDA cores, 16 bytes a lane.
+// Up to 32 rows (tokens being decoded, and their tangents) a tile would be almost empty
+// and the weights' bytes are all there is: linear_rows_kernel streams W once, 16 bytes a
+// lane, into warp-level tensor instructions. On B200, 1536 -> 6144 (18.9 MB): ROWS
 //
 // Every wait is bounded: on expiry the kernel records an error code, drains its
 // copies, products and stores, frees tensor memory and returns.
@@ -546,95 +546,125 @@ __global__ void __launch_bounds__(256) linear_finish_kernel(const LinearParams p
 }
 
 // --------------------------------------------------------------------- a few rows
-// R rows (primal rows, then as many tangent rows) against all of W, which is read
-// once, 16 bytes a lane: a warp takes CPW rows of W at a time, its lanes 256
-// neighbouring elements of each, U such pieces in flight. x comes through L1.
-// The sums of a row of W are shuffled together; then one warp per token does the
-// epilogue of the block's 8 * CPW columns.
-template <int R, int CPW>
-__global__ void __launch_bounds__(256) linear_rows_kernel(const LinearParams p) {
-  constexpr int U = 8 / CPW;
-  __shared__ float z[R][8 * CPW];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int32_t base = int32_t(blockIdx.x) * 8 * CPW, c0 = base + warp * CPW;
-  const int32_t rows = p.M;  // primal rows
-  const uint16_t *w = static_cast<const uint16_t *>(p.w);
-  const bool jvp = p.tx != nullptr;
-  float acc[R][CPW];
-#pragma unroll
-  for (int r = 0; r < R; ++r)
-#pragma unroll
-    for (int c = 0; c < CPW; ++c) acc[r][c] = 0.f;
-  for (int32_t k0 = 8 * lane; k0 < p.K; k0 += 256 * U) {
-    v8::Raw<__nv_bfloat16> wr[U][CPW];
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int c = 0; c < CPW; ++c) {
-        wr[u][c] = v8::zero<__nv_bfloat16>();
-        const int32_t k = k0 + 256 * u;
-        if (k < p.K && c0 + c < p.N)
-          wr[u][c].a = __ldg(reinterpret_cast<const uint4 *>(w + size_t(c0 + c) * p.K + k));
-      }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int32_t k = k0 + 256 * u;
-      if (k >= p.K) break;
-      float wf[CPW][8];
-#pragma unroll
-      for (int c = 0; c < CPW; ++c) v8::unpack(wr[u][c], wf[c]);
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const bool tan = jvp && r >= rows;
-        if (r >= (jvp ? 2 * rows : rows)) break;
-        const uint16_t *src = tan ? static_cast<const uint16_t *>(p.tx) + (r - rows) * p.ld_tx
-                                  : static_cast<const uint16_t *>(p.x) + r * p.ld_x;
-        v8::Raw<__nv_bfloat16> xr;
-        xr.a = __ldg(reinterpret_cast<const uint4 *>(src + k));
-        float xf[8];
-        v8::unpack(xr, xf);
-#pragma unroll
-        for (int c = 0; c < CPW; ++c)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) acc[r][c] = fmaf(xf[i], wf[c][i], acc[r][c]);
+// Up to 32 rows (primal rows, then as many tangent rows): a tile of 256 would be mostly
+// empty and the weights' bytes are all there is to move, so W is streamed once, 16 bytes
+// a lane, and the next step's pieces are on their way while one is multiplied.
+
+// The epilogue of a block's columns base .. base + COLS, COLS <= 32: z[row][column] holds
+// the products. One warp per token, one lane per column.
+template <int COLS>
+__device__ __forceinline__ void rows_epilogue(const LinearParams &p, const float *z, int32_t ldz, int32_t base) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rows = p.M;
+  const int32_t col = base + lane;
+  const bool jvp = p.tx != nullptr, in = lane < COLS && col < p.N;
+  const float bias = in && p.bias ? __uint_as_float(uint32_t(static_cast<const uint16_t *>(p.bias)[col]) << 16) : 0.f;
+  for (int32_t r = warp; r < rows; r += int32_t(blockDim.x >> 5)) {
+    float v[1] = {in ? z[r * ldz + lane] + bias : 0.f}, sl[1];
+    if (COLS == 32 && p.codes) {
+      const uint32_t s = ck::scale_of(__reduce_max_sync(0xFFFFFFFFu, ck::mag_bits(v[0])));
+      float f[1] = {v[0]};
+      ck::saturate(f, s);
+      p.codes[size_t(r) * (32 * size_t(p.nb)) + col] = s == 255u ? 0 : int8_t(ck::code_word(f[0], ck::up_of(s)) & 0xFFu);
+      if (lane == 0) {
+        p.scales[size_t(r) * p.ns + base / 32] = uint8_t(s);
+        if (base / 32 == p.nb - 1)
+          for (int32_t i = p.nb; i < p.ns; ++i) p.scales[size_t(r) * p.ns + i] = 0;
       }
     }
+    if (!in) continue;
+    lin::act_all<true>(p.act, v, sl);
+    if (p.res) v[0] += __bfloat162float(static_cast<const __nv_bfloat16 *>(p.res)[r * p.ld_res + col]);
+    static_cast<__nv_bfloat16 *>(p.y)[size_t(r) * p.N + col] = __float2bfloat16_rn(v[0]);
+    if (jvp) {
+      float t = sl[0] * z[(r + rows) * ldz + lane];
+      if (p.tres) t += __bfloat162float(static_cast<const __nv_bfloat16 *>(p.tres)[r * p.ld_tres + col]);
+      static_cast<__nv_bfloat16 *>(p.ty)[size_t(r) * p.N + col] = __float2bfloat16_rn(t);
+    }
   }
+}
+
+// On the warp-level tensor instruction (m16n8k16: at these sizes the weights
+// bound, not the products): a block takes 16 MT columns of the output, its eight warps deal
+// the contraction out in steps of 32 and add their sums through shared memory. The order
+// of the contraction is free, so a lane's 16 bytes of a row (eight neighbouring elements)
+// serve as its fragments of two instructions, for W and x alike: both come straight from
+// global memory in 16-byte pieces. NT: groups of eight rows.
+template <int NT, int MT>
+__global__ void __launch_bounds__(256) linear_rows_kernel(const LinearParams p) {
+  extern __shared__ float red[];  // [8 warps][8 NT rows][columns + 1]
+  constexpr int kRows = 8 * NT, kCols = 16 * MT, kLd = kCols + 1;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int32_t base = int32_t(blockIdx.x) * kCols, rows = p.tx ? 2 * p.M : p.M;
+  const uint16_t *w = static_cast<const uint16_t *>(p.w);
+  const uint4 none = make_uint4(0, 0, 0, 0);
+  const uint16_t *wrow[2 * MT], *xrow[NT];
 #pragma unroll
-  for (int r = 0; r < R; ++r)
+  for (int i = 0; i < 2 * MT; ++i) wrow[i] = base + 8 * i + g < p.N ? w + size_t(base + 8 * i + g) * p.K : nullptr;
 #pragma unroll
-    for (int c = 0; c < CPW; ++c) {
+  for (int j = 0; j < NT; ++j) {
+    const int32_t r = 8 * j + g;
+    xrow[j] = r >= rows ? nullptr
+              : r < p.M ? static_cast<const uint16_t *>(p.x) + r * p.ld_x
+                        : static_cast<const uint16_t *>(p.tx) + (r - p.M) * p.ld_tx;
+  }
+  float acc[MT][NT][4];
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) acc[r][c] += __shfl_xor_sync(0xFFFFFFFFu, acc[r][c], o);
-      if (lane == 0) z[r][warp * CPW + c] = acc[r][c];
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.f;
+  uint4 wn[2 * MT], xn[NT];  // the next step's pieces
+  auto fetch = [&](int32_t k) {
+#pragma unroll
+    for (int i = 0; i < 2 * MT; ++i) wn[i] = wrow[i] && k < p.K ? __ldg(reinterpret_cast<const uint4 *>(wrow[i] + k)) : none;
+#pragma unroll
+    for (int j = 0; j < NT; ++j) xn[j] = xrow[j] && k < p.K ? __ldg(reinterpret_cast<const uint4 *>(xrow[j] + k)) : none;
+  };
+  auto mma = [](float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  };
+  const int32_t steps = (p.K + 31) / 32;
+  fetch(32 * warp + 8 * t);
+  for (int32_t step = warp; step < steps; step += 8) {
+    uint4 wc[2 * MT], xc[NT];
+#pragma unroll
+    for (int i = 0; i < 2 * MT; ++i) wc[i] = wn[i];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) xc[j] = xn[j];
+    fetch(32 * (step + 8) + 8 * t);
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        mma(acc[i][j], wc[2 * i].x, wc[2 * i + 1].x, wc[2 * i].y, wc[2 * i + 1].y, xc[j].x, xc[j].y);
+        mma(acc[i][j], wc[2 * i].z, wc[2 * i + 1].z, wc[2 * i].w, wc[2 * i + 1].w, xc[j].z, xc[j].w);
+      }
+  }
+  float *mine = red + warp * kRows * kLd;
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      float *at = mine + (8 * j + 2 * t) * kLd + 16 * i + g;
+      at[0] = acc[i][j][0];
+      at[kLd] = acc[i][j][1];
+      at[8] = acc[i][j][2];
+      at[kLd + 8] = acc[i][j][3];
     }
   __syncthreads();
-  if (warp >= rows) return;
-  const int32_t col = base + lane;
-  const bool in = lane < 8 * CPW && col < p.N;
-  float v[1] = {in ? z[warp][lane < 8 * CPW ? lane : 0] : 0.f}, sl[1];
-  if (in && p.bias) v[0] += __uint_as_float(uint32_t(static_cast<const uint16_t *>(p.bias)[col]) << 16);
-  if (CPW == 4 && p.codes) {
-    const uint32_t s = ck::scale_of(__reduce_max_sync(0xFFFFFFFFu, ck::mag_bits(v[0])));
-    float f[1] = {v[0]};
-    ck::saturate(f, s);
-    p.codes[size_t(warp) * (32 * size_t(p.nb)) + col] = s == 255u ? 0 : int8_t(ck::code_word(f[0], ck::up_of(s)) & 0xFFu);
-    if (lane == 0) {
-      p.scales[size_t(warp) * p.ns + base / 32] = uint8_t(s);
-      if (base / 32 == p.nb - 1)
-        for (int32_t i = p.nb; i < p.ns; ++i) p.scales[size_t(warp) * p.ns + i] = 0;
-    }
+  for (int32_t o = int32_t(threadIdx.x); o < kRows * kCols; o += 256) {
+    float *at = red + o / kCols * kLd + o % kCols;
+    float s = at[0];
+#pragma unroll
+    for (int v = 1; v < 8; ++v) s += at[v * kRows * kLd];
+    at[0] = s;
   }
-  if (!in) return;
-  lin::act_all<true>(p.act, v, sl);
-  const __nv_bfloat16 *res = static_cast<const __nv_bfloat16 *>(p.res), *tres = static_cast<const __nv_bfloat16 *>(p.tres);
-  if (res) v[0] += __bfloat162float(res[warp * p.ld_res + col]);
-  static_cast<__nv_bfloat16 *>(p.y)[size_t(warp) * p.N + col] = __float2bfloat16_rn(v[0]);
-  if (jvp) {
-    float t = sl[0] * z[R > 1 ? warp + rows : 0][lane];
-    if (tres) t += __bfloat162float(tres[warp * p.ld_tres + col]);
-    static_cast<__nv_bfloat16 *>(p.ty)[size_t(warp) * p.N + col] = __float2bfloat16_rn(t);
-  }
+  __syncthreads();
+  rows_epilogue<kCols>(p, red, kLd, base);
 }
 
 // ----------------------------------------------------- gradient of the activation
@@ -771,16 +801,15 @@ cudaError_t launch_tiles(const LinearParams &p, cudaStream_t stream) {
                             : launch_tiles<JVP, AMN, BMN, EPI, 256>(p, stream);
 }
 
-template <int R>
+template <int NT>
 cudaError_t launch_rows(const LinearParams &p, cudaStream_t stream) {
-  // columns a warp: more reuse x, fewer give more blocks; a checkpoint needs blocks of 32
-  if (p.codes || p.N >= 32 * 148) {
-    linear_rows_kernel<R, 4><<<unsigned((p.N + 31) / 32), 256, 0, stream>>>(p);
-  } else if (p.N >= 16 * 148) {
-    linear_rows_kernel<R, 2><<<unsigned((p.N + 15) / 16), 256, 0, stream>>>(p);
-  } else {
-    linear_rows_kernel<R, 1><<<unsigned((p.N + 7) / 8), 256, 0, stream>>>(p);
-  }
+  // 16 columns a block where 32 would leave SMs without one; a checkpoint's blocks are 32
+  constexpr int kSmem = 8 * 8 * NT * 33 * int(sizeof(float));
+  static_assert(kSmem <= 48 * 1024, "shared memory without an attribute");
+  if (p.codes || p.N > 32 * 148)
+    linear_rows_kernel<NT, 2><<<unsigned((p.N + 31) / 32), 256, kSmem, stream>>>(p);
+  else
+    linear_rows_kernel<NT, 1><<<unsigned((p.N + 15) / 16), 256, kSmem, stream>>>(p);
   return cudaGetLastError();
 }
 
@@ -789,9 +818,7 @@ cudaError_t launch_rows(const LinearParams &p, cudaStream_t stream) {
 cudaError_t launch_linear_fwd(const LinearParams &p, cudaStream_t stream) {
   const int32_t rows = p.tx ? 2 * p.M : p.M;
   if (rows <= kLinearFewRows) {
-    if (rows == 1) return launch_rows<1>(p, stream);
-    if (rows == 2) return launch_rows<2>(p, stream);
-    return rows <= 4 ? launch_rows<4>(p, stream) : launch_rows<8>(p, stream);
+    return rows <= 8 ? launch_rows<1>(p, stream) : rows <= 16 ? launch_rows<2>(p, stream) : launch_rows<4>(p, stream);
   }
   return p.tx ? launch_tiles<true, false, false, true>(p, stream) : launch_tiles<false, false, false, true>(p, stream);
 }

@@ -193,16 +193,18 @@ def test_infinities_and_nans_stay_in_their_rows(M):
 
 
 def test_few_rows_agree_with_tiles():
-    """The streaming kernel (up to eight rows) and the tile kernel sum in different orders:
+    """The streaming kernels (one row, up to 64) and the tile kernel sum in different orders:
     each is within its bound of the same reference."""
-    for M in (1, 4, 8, 9, 16):
+    for M in (1, 2, 8, 9, 17, 33, 64, 65):
         run_fwd(M, 520, 264, "gelu_tanh", True, True, False, True, seed=3)
+        run_fwd(M, 1544, 72, "silu", True, True, True, True, seed=4)
 
 
 def test_bounded_waits_report_and_the_context_survives():
     L = _lib.lib()
     g = torch.Generator().manual_seed(3)
-    x, tx, w = rnd(g, 64, 64).cuda(), rnd(g, 64, 64).cuda(), rnd(g, 64, 64).cuda()
+    # more than 64 rows: the kernels with copies to wait for
+    x, tx, w = rnd(g, 128, 64).cuda(), rnd(g, 128, 64).cuda(), rnd(g, 64, 64).cuda()
     pre = caj.ckpt8_pack(x)
     calls = [lambda: caj.linear_act_fwd(x, w, act="silu"), lambda: caj.linear_act_fwd(x, w, act="silu", tx=tx),
              lambda: caj.linear_act_bwd(x, x, w, act="silu", pre=pre, need=(True, False)),
