@@ -5,6 +5,9 @@ Public API (a thin layer over the C-ABI library libcausaljvp):
     o, to, lse, tlse = attn_fwd_jvp(q, k, v, tq, tk, tv, mask, scale=None)
     o, to, lse, tlse = attention_jvp(q, k, v, tq, tk, tv, mask)  # o differentiable in q, k, v
 
+and, for the rest of the block, rotary tables, norm + rotation, linear layers and 8-bit
+activation checkpoints (block.py), differentiable as qk_norm_rope and linear_act.
+
 q..tv are [B, H, N, D] tensors (bf16 for the tensor-core path, fp32 for the
 CUDA-core fp32 path), `mask` a MaskDesc (or a (tokens_per_frame,
 frames_per_chunk, n_frames, tf_layout) tuple). With CUDA tensors everything
@@ -33,7 +36,8 @@ __all__ = ["attention_jvp", "attn_fwd_jvp", "attn_fwd_jvp_out", "attn_fwd_jvp_sc
            "ipc_export", "ipc_open", "ipc_close", "part_query_tiles", "attn_bwd", "qk_norm_rope_jvp", "out_proj_jvp", "MaskDesc", "CajError", "visible_pairs",
            "row_key_ranges", "qtile_key_tiles", "device_status", "flops", "EXPORTED", "LIB_PATH",
            "BLOCK_M", "BLOCK_N", "Ckpt8", "ckpt8_pack", "ckpt8_unpack", "rope_frequencies", "rope_table",
-           "qk_norm_rope_fwd", "qk_norm_rope_bwd", "linear_act_fwd", "linear_act_bwd"]
+           "qk_norm_rope_fwd", "qk_norm_rope_bwd", "linear_act_fwd", "linear_act_bwd",
+           "qk_norm_rope", "linear_act"]
 
 BLOCK_M = 128  # query rows per tile of both kernels
 BLOCK_N = 64   # keys per tile of the tensor-core kernel
@@ -42,7 +46,7 @@ _DTYPES = {torch.float32: _lib.CAJ_DTYPE_F32, torch.bfloat16: _lib.CAJ_DTYPE_BF1
 
 from .block import (Ckpt8, ckpt8_pack, ckpt8_unpack, linear_act_bwd, linear_act_fwd,  # noqa: E402
                     qk_norm_rope_bwd, qk_norm_rope_fwd, rope_frequencies, rope_table)
-from .autograd import attention_jvp  # noqa: E402  (autograd binding: fused forward, backward kernels)
+from .autograd import attention_jvp, linear_act, qk_norm_rope  # noqa: E402  (autograd binding: fused forward, backward kernels)
 
 
 def part_query_tiles(mask, part: int, nparts: int):

@@ -1,4 +1,4 @@
-"""Autograd binding of the fused attention forward + JVP.
+"""Autograd bindings of the fused attention and of the block operators around it.
 
     o, to, lse, tlse = attention_jvp(q, k, v, tq, tk, tv, mask)
 
@@ -9,40 +9,140 @@ The tangent branch is stop-gradient, as in the student's gradient step of
 TF-sCM (Causal-rCM, appendix A, the JVP of the stop-gradient network): to,
 lse and tlse are returned as non-differentiable, and the tangents tq, tk, tv
 receive no gradient. bf16 CUDA tensors only (the backward kernels' dtype).
+
+    q, k, v = qk_norm_rope(xq, xk, xv, gq, gk, cos, sin, H)
+    y, ty = linear_act(x, w, bias, act="gelu_tanh", residual=r, tx=tx)
+
+are qk_norm_rope_fwd and linear_act_fwd in the same way: differentiable in the
+primal inputs, gains, weights and bias, with the tangents stop-gradient.
+
+ckpt8=True keeps what the backward reads of the activations in 8 bits
+(ckpt8_pack) instead of bf16, about half the memory: q, k, v and o of the
+attention, the inputs of the norm and of the linear layer. (A linear layer with
+an activation keeps its pre-activation in 8 bits either way, written by the
+product's epilogue.) Values and tangents of the forward do not change; gradients
+are those at the rounded activations.
 """
 from __future__ import annotations
 
 from typing import Optional
 
 import torch
+from torch.autograd.function import once_differentiable
 
-__all__ = ["attention_jvp"]
+from .block import (Ckpt8, ckpt8_pack, ckpt8_unpack, linear_act_bwd, linear_act_fwd, qk_norm_rope_bwd,
+                    qk_norm_rope_fwd)
+
+__all__ = ["attention_jvp", "qk_norm_rope", "linear_act"]
+
+
+def _keep(ckpt8: bool, *tensors):
+    """What a context saves for these tensors: themselves, or their codes and scales."""
+    if not ckpt8:
+        return tensors
+    return tuple(part for t in tensors for part in ckpt8_pack(t)[:2])
+
+
+def _kept(ckpt8: bool, saved, shapes):
+    """The tensors (ckpt8: the Ckpt8s) that _keep was given, and the rest of `saved`."""
+    if not ckpt8:
+        return list(saved[:len(shapes)]), list(saved[len(shapes):])
+    n = 2 * len(shapes)
+    return [Ckpt8(saved[2 * i], saved[2 * i + 1], tuple(s)) for i, s in enumerate(shapes)], list(saved[n:])
 
 
 class _AttentionJvp(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, q, k, v, tq, tk, tv, mask, scale, clean_tangent_zero):
+    def forward(ctx, q, k, v, tq, tk, tv, mask, scale, clean_tangent_zero, ckpt8):
         from . import attn_fwd_jvp
         o, to, lse, tlse = attn_fwd_jvp(q, k, v, tq, tk, tv, mask, scale=scale,
                                         clean_tangent_zero=clean_tangent_zero)
-        ctx.save_for_backward(q, k, v, o, lse)
-        ctx.mask, ctx.scale = mask, scale
+        ctx.save_for_backward(*_keep(ckpt8, q, k, v, o), lse)
+        ctx.mask, ctx.scale, ctx.ckpt8, ctx.shape = mask, scale, ckpt8, q.shape
         ctx.mark_non_differentiable(to, lse, tlse)
         return o, to, lse, tlse
 
     @staticmethod
     def backward(ctx, do, _dto, _dlse, _dtlse):
         from . import attn_bwd
-        q, k, v, o, lse = ctx.saved_tensors
+        tensors, (lse,) = _kept(ctx.ckpt8, ctx.saved_tensors, [ctx.shape] * 4)
+        q, k, v, o = [ckpt8_unpack(t) for t in tensors] if ctx.ckpt8 else tensors
         dq, dk, dv, _ = attn_bwd(q, k, v, o, do.contiguous(), lse, ctx.mask, scale=ctx.scale)
-        return dq, dk, dv, None, None, None, None, None, None
+        return (dq, dk, dv) + (None,) * 7
 
 
 def attention_jvp(q, k, v, tq, tk, tv, mask, scale: Optional[float] = None,
-                  clean_tangent_zero: bool = False):
+                  clean_tangent_zero: bool = False, ckpt8: bool = False):
     """(o, to, lse, tlse) of the fused kernel, with o differentiable in q, k, v.
-    q..tv: [B, H, N, D] contiguous bf16 CUDA tensors; mask: a MaskDesc."""
+    q..tv: [B, H, N, D] contiguous bf16 CUDA tensors; mask: a MaskDesc. ckpt8: keep q, k, v
+    and o in 8 bits for the backward, which runs on the values these stand for (with the
+    forward's LSE)."""
     for t in (q, k, v, tq, tk, tv):
         if not (t.is_cuda and t.dtype == torch.bfloat16 and t.is_contiguous()):
             raise ValueError("attention_jvp: q..tv must be contiguous bf16 CUDA tensors")
-    return _AttentionJvp.apply(q, k, v, tq, tk, tv, mask, scale, clean_tangent_zero)
+    return _AttentionJvp.apply(q, k, v, tq, tk, tv, mask, scale, clean_tangent_zero, bool(ckpt8))
+
+
+class _QkNormRope(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, xq, xk, xv, gq, gk, rope_cos, rope_sin, txq, txk, txv, H, Hk, eps, norm, layout, ckpt8):
+        out = qk_norm_rope_fwd(xq, xk, xv, gq, gk, rope_cos, rope_sin, H, Hk, eps=eps, norm=norm, layout=layout,
+                               txq=txq, txk=txk, txv=txv)
+        normed = norm != "none"
+        ctx.save_for_backward(*(_keep(ckpt8, xq, xk) if normed else ()), rope_cos, rope_sin,
+                              *((gq, gk) if normed else ()))
+        ctx.args = dict(eps=eps, norm=norm, layout=layout)
+        ctx.ckpt8, ctx.shapes, ctx.has_v = ckpt8, [xq.shape, xk.shape] if normed else [], xv is not None
+        ctx.primal = 3 if xv is not None else 2
+        ctx.mark_non_differentiable(*out[ctx.primal:])
+        return out
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, *grads):
+        (xq, xk), rest = _kept(ctx.ckpt8, ctx.saved_tensors, ctx.shapes) if ctx.shapes else \
+            ((None, None), list(ctx.saved_tensors))
+        cos, sin, gq, gk = rest if len(rest) == 4 else (*rest, None, None)
+        dq, dk, dv = [g.contiguous() for g in grads[:ctx.primal]] + ([] if ctx.has_v else [None])
+        return qk_norm_rope_bwd(dq, dk, dv, xq, xk, gq, gk, cos, sin, **ctx.args) + (None,) * 11
+
+
+def qk_norm_rope(xq, xk, xv, gq, gk, rope_cos, rope_sin, H: int, Hk: Optional[int] = None, eps: float = 1e-6,
+                 norm: str = "head", layout: str = "interleaved", txq=None, txk=None, txv=None, ckpt8: bool = False):
+    """qk_norm_rope_fwd (see there), with q, k and v differentiable in xq, xk, xv, gq and gk.
+    ckpt8: keep xq and xk in 8 bits for the backward, which reads them as they are."""
+    return _QkNormRope.apply(xq, xk, xv, gq, gk, rope_cos, rope_sin, txq, txk, txv, H, Hk, eps, norm, layout,
+                             bool(ckpt8))
+
+
+class _LinearAct(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w, bias, residual, tx, tresidual, act, ckpt8):
+        y, ty, pre = linear_act_fwd(x, w, bias, act=act, residual=residual, tx=tx, tresidual=tresidual,
+                                    save_pre=act != "none")
+        ctx.save_for_backward(*_keep(ckpt8, x), w, *(pre[:2] if pre is not None else ()))
+        ctx.act, ctx.ckpt8, ctx.shape, ctx.out_shape = act, ckpt8, x.shape, tuple(y.shape)
+        ctx.bias_dtype = None if bias is None else bias.dtype
+        if ty is None:
+            return y
+        ctx.mark_non_differentiable(ty)
+        return y, ty
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, *_dty):
+        (x,), rest = _kept(ctx.ckpt8, ctx.saved_tensors, [ctx.shape])
+        pre = Ckpt8(rest[1], rest[2], ctx.out_shape) if len(rest) == 3 else None
+        need = ctx.needs_input_grad
+        dx = dw = db = None
+        dy = dy.contiguous()
+        if need[0] or need[1] or need[2]:
+            dx, dw, db = linear_act_bwd(dy, x, rest[0], act=ctx.act, pre=pre, bias=need[2], need=(need[0], need[1]))
+        return (dx, dw, None if db is None else db.to(ctx.bias_dtype), dy if need[3] else None) + (None,) * 4
+
+
+def linear_act(x, w, bias=None, act: str = "none", residual=None, tx=None, tresidual=None, ckpt8: bool = False):
+    """linear_act_fwd (see there): (y, ty), ty None without tx, with y differentiable in x, w,
+    bias and residual. ckpt8: keep x in 8 bits for the backward, which reads it as it is."""
+    out = _LinearAct.apply(x, w, bias, residual, tx, tresidual, act, bool(ckpt8))
+    return out if tx is not None else (out, None)
