@@ -2,8 +2,9 @@
 // scale bytes, and back (format and rounding: ckpt8.cuh).
 //
 // Memory-bound: 3.03 bytes a value for bf16 (2 in, 1.03 out, or the reverse).
-// Vector form: four lanes hold a block, eight values each (one or two 16-byte
-// loads); the block's largest magnitude is a two-step shuffle of ordered bits.
+// Vector form: packing, two lanes hold a block, sixteen values each (16-byte loads and
+// stores), and the block's largest magnitude is one shuffle away; unpacking, four lanes,
+// eight values each, so that a warp's 16-byte stores are neighbours.
 // Each thread takes kUnroll blocks a grid apart, with all loads issued first, to
 // keep enough bytes in flight.
 // Rows whose 16-byte vectors do not line up (C not a multiple of 8, or a base or
@@ -20,7 +21,7 @@
 namespace caj {
 namespace {
 
-constexpr int kUnroll = 4;
+constexpr int kUnroll = 2, kUnpackUnroll = 4;
 constexpr int kThreads = 256;
 
 // Scale byte of block `blk`; the row's last block also zeroes the padding bytes.
@@ -33,41 +34,45 @@ __device__ __forceinline__ void store_scale(uint8_t *row, int32_t blk, int32_t n
 template <typename T>
 __global__ void __launch_bounds__(kThreads) pack_vec_kernel(const Ckpt8Params p) {
   const uint32_t nb = uint32_t(p.nb), total = p.total;
-  const uint32_t step = gridDim.x * (kThreads / 4);
-  const uint32_t first = blockIdx.x * (kThreads / 4) + (threadIdx.x >> 2);
-  const int part = threadIdx.x & 3;
-  v8::Raw<T> raw[kUnroll];
+  const uint32_t step = gridDim.x * (kThreads / 2);
+  const uint32_t first = blockIdx.x * (kThreads / 2) + (threadIdx.x >> 1);
+  const int part = threadIdx.x & 1;
+  v8::Raw<T> raw[kUnroll][2];
   uint32_t row[kUnroll], blk[kUnroll];
 #pragma unroll
   for (int u = 0; u < kUnroll; ++u) {
     const uint64_t g = uint64_t(first) + uint64_t(u) * step;
     row[u] = g < total ? uint32_t(g) / nb : 0xFFFFFFFFu;
     blk[u] = uint32_t(g) - row[u] * nb;
-    raw[u] = v8::zero<T>();
-    const int32_t c = int32_t(blk[u]) * ck::kBlock + 8 * part;
-    if (g < total && c < p.cols)  // cols is a multiple of 8 here
-      raw[u] = v8::load(static_cast<const T *>(p.x) + size_t(row[u]) * p.ld + c);
+    const int32_t c = int32_t(blk[u]) * ck::kBlock + 16 * part;
+    const T *src = static_cast<const T *>(p.x) + size_t(row[u]) * p.ld + c;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      raw[u][h] = v8::zero<T>();
+      if (g < total && c + 8 * h < p.cols) raw[u][h] = v8::load(src + 8 * h);  // cols is a multiple of 8 here
+    }
   }
 #pragma unroll
   for (int u = 0; u < kUnroll; ++u) {
-    float f[8];
-    v8::unpack(raw[u], f);
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, ck::mag_bits(f[i]));
-    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+    float f[2][8];
+    v8::unpack(raw[u][0], f[0]);
+    v8::unpack(raw[u][1], f[1]);
+    float m = ck::max_nan(ck::max_mag(f[0]), ck::max_mag(f[1]));
+    m = ck::max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
     if (row[u] == 0xFFFFFFFFu) continue;
-    const uint32_t s = ck::scale_of(m);
-    uint2 codes = make_uint2(0, 0);
+    const uint32_t s = ck::scale_of(__float_as_uint(m));
+    uint4 codes = make_uint4(0, 0, 0, 0);
     if (s != 255u) {
       const float up = ck::up_of(s);
-      ck::saturate(f, s);
-      codes.x = ck::pack_codes4(f[0], f[1], f[2], f[3], up);
-      codes.y = ck::pack_codes4(f[4], f[5], f[6], f[7], up);
+      ck::saturate(f[0], s);
+      ck::saturate(f[1], s);
+      codes.x = ck::pack_codes4(f[0][0], f[0][1], f[0][2], f[0][3], up);
+      codes.y = ck::pack_codes4(f[0][4], f[0][5], f[0][6], f[0][7], up);
+      codes.z = ck::pack_codes4(f[1][0], f[1][1], f[1][2], f[1][3], up);
+      codes.w = ck::pack_codes4(f[1][4], f[1][5], f[1][6], f[1][7], up);
     }
-    const size_t base = (size_t(row[u]) * nb + blk[u]) * ck::kBlock + 8 * part;
-    __stcs(reinterpret_cast<uint2 *>(p.codes + base), codes);
+    const size_t base = (size_t(row[u]) * nb + blk[u]) * ck::kBlock + 16 * part;
+    __stcs(reinterpret_cast<uint4 *>(p.codes + base), codes);
     if (part == 0) store_scale(p.scales + size_t(row[u]) * p.ns, int32_t(blk[u]), p.nb, p.ns, s);
   }
 }
@@ -78,11 +83,11 @@ __global__ void __launch_bounds__(kThreads) unpack_vec_kernel(const Ckpt8Params 
   const uint32_t step = gridDim.x * (kThreads / 4);
   const uint32_t first = blockIdx.x * (kThreads / 4) + (threadIdx.x >> 2);
   const int part = threadIdx.x & 3;
-  uint2 codes[kUnroll];
-  uint32_t row[kUnroll], scale[kUnroll];
-  int32_t col[kUnroll];
+  uint2 codes[kUnpackUnroll];
+  uint32_t row[kUnpackUnroll], scale[kUnpackUnroll];
+  int32_t col[kUnpackUnroll];
 #pragma unroll
-  for (int u = 0; u < kUnroll; ++u) {
+  for (int u = 0; u < kUnpackUnroll; ++u) {
     const uint64_t g = uint64_t(first) + uint64_t(u) * step;
     row[u] = g < total ? uint32_t(g) / nb : 0xFFFFFFFFu;
     const uint32_t blk = uint32_t(g) - row[u] * nb;
@@ -95,7 +100,7 @@ __global__ void __launch_bounds__(kThreads) unpack_vec_kernel(const Ckpt8Params 
     }
   }
 #pragma unroll
-  for (int u = 0; u < kUnroll; ++u) {
+  for (int u = 0; u < kUnpackUnroll; ++u) {
     if (row[u] == 0xFFFFFFFFu || col[u] >= p.cols) continue;
     const float unit = ck::unit_of(scale[u]);
     float f[8];
@@ -167,7 +172,7 @@ __global__ void __launch_bounds__(kThreads) unpack_lane_kernel(const Ckpt8Params
 template <typename T>
 cudaError_t launch(const Ckpt8Params &p, bool unpack, bool vec, cudaStream_t stream) {
   const uint64_t units = vec ? p.total : uint64_t(p.rows) * ((p.nb + kRun - 1) / kRun);
-  const uint32_t per_cta = vec ? kThreads / 4 * kUnroll : kThreads / 32;
+  const uint32_t per_cta = !vec ? kThreads / 32 : unpack ? kThreads / 4 * kUnpackUnroll : kThreads / 2 * kUnroll;
   const unsigned grid = unsigned((units + per_cta - 1) / per_cta);
   if (unpack) {
     if (vec)

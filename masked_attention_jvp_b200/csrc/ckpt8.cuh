@@ -98,16 +98,22 @@ __device__ __forceinline__ void pack_saturated(const float (&v)[kBlock], uint32_
 #pragma unroll
   for (int i = 0; i < kBlock / 4; ++i) w[i] = o[i];
 }
-// Four codes -> values: byte ^ 0x80 under the exponent of 2^23 is 2^23 + 128 + c; in
-// packed pairs. (One fma with -(2^23 + 128) * unit instead would overflow from unit
-// 2^105 on.) unit = infinity: 0 * infinity = NaN, as the format wants.
-__device__ __forceinline__ void unpack_codes4(uint32_t w, float unit, float &a, float &b, float &c, float &d) {
+// Four codes -> two pairs of values: byte ^ 0x80 under the exponent of 2^23 is
+// 2^23 + 128 + c; in packed arithmetic. (One fma with -(2^23 + 128) * unit instead would
+// overflow from unit 2^105 on.) unit = infinity: 0 * infinity = NaN, as the format wants.
+__device__ __forceinline__ void unpack_codes4(uint32_t w, float unit, uint64_t &ab, uint64_t &cd) {
   const uint32_t u = w ^ 0x80808080u;
   const uint64_t off = ptx::f2(8388736.f, 8388736.f), un = ptx::f2(unit, unit);
-  ptx::f2_split(ptx::mul2(ptx::sub2(ptx::f2(__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7440)),
-                                            __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7441))), off), un), a, b);
-  ptx::f2_split(ptx::mul2(ptx::sub2(ptx::f2(__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7442)),
-                                            __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7443))), off), un), c, d);
+  ab = ptx::mul2(ptx::sub2(ptx::f2(__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7440)),
+                                   __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7441))), off), un);
+  cd = ptx::mul2(ptx::sub2(ptx::f2(__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7442)),
+                                   __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7443))), off), un);
+}
+__device__ __forceinline__ void unpack_codes4(uint32_t w, float unit, float &a, float &b, float &c, float &d) {
+  uint64_t ab, cd;
+  unpack_codes4(w, unit, ab, cd);
+  ptx::f2_split(ab, a, b);
+  ptx::f2_split(cd, c, d);
 }
 
 }  // namespace ck

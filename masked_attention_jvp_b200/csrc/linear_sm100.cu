@@ -673,7 +673,7 @@ __global__ void __launch_bounds__(256) linear_rows_kernel(const LinearParams p) 
 // lane, and walk over the rows of their block's chunk; the eight warps' sums meet in
 // shared memory. ACT none: only the sums, dz is dy.
 constexpr int kDzUnroll = 2;
-template <bool ACT>
+template <int ACT>
 __global__ void __launch_bounds__(256, 4) linear_dz_kernel(const LinearDzParams p) {
   __shared__ float red[8][256];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -681,59 +681,74 @@ __global__ void __launch_bounds__(256, 4) linear_dz_kernel(const LinearDzParams 
   const int64_t r0 = int64_t(blockIdx.y) * p.chunk_rows;
   const int64_t r1 = min(r0 + p.chunk_rows, p.M);
   const bool in = col < p.C;
-  const __nv_bfloat16 *dy = static_cast<const __nv_bfloat16 *>(p.dy);
-  float sum[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) sum[i] = 0.f;
-  for (int64_t base = r0 + warp; base < r1; base += 8 * kDzUnroll) {
-    v8::Raw<__nv_bfloat16> raw[kDzUnroll];
-    uint2 codes[kDzUnroll];
-    uint32_t scale[kDzUnroll];
+  const __nv_bfloat16 *dy = static_cast<const __nv_bfloat16 *>(p.dy) + col;
+  __nv_bfloat16 *dz = static_cast<__nv_bfloat16 *>(p.dz) + col;
+  const int8_t *codes = p.codes + col;
+  const uint8_t *scales = p.scales + col / 32;
+  uint64_t sum[4] = {0, 0, 0, 0};
+  v8::Raw<__nv_bfloat16> raw[kDzUnroll], raw_next[kDzUnroll];  // the next rows are on their way meanwhile
+  uint2 c[kDzUnroll], c_next[kDzUnroll];
+  uint32_t scale[kDzUnroll], scale_next[kDzUnroll];
+  auto fetch = [&](int64_t base) {
 #pragma unroll
     for (int u = 0; u < kDzUnroll; ++u) {
       const int64_t r = base + 8 * u;
-      raw[u] = v8::zero<__nv_bfloat16>();
-      codes[u] = make_uint2(0, 0);
-      scale[u] = 0;
       if (!in || r >= r1) continue;
-      raw[u] = v8::load(dy + r * p.ld_dy + col);
-      if (ACT) {
-        codes[u] = __ldcs(reinterpret_cast<const uint2 *>(p.codes + size_t(r) * (32 * size_t(p.nb)) + col));
-        scale[u] = __ldg(p.scales + size_t(r) * p.ns + col / 32);
+      raw_next[u] = v8::load(dy + r * p.ld_dy);
+      if (ACT != lin::kActNone) {
+        c_next[u] = __ldcs(reinterpret_cast<const uint2 *>(codes + r * (32 * int64_t(p.nb))));
+        scale_next[u] = __ldg(scales + r * p.ns);
       }
     }
+  };
+  fetch(r0 + warp);
+  for (int64_t base = r0 + warp; base < r1; base += 8 * kDzUnroll) {
+#pragma unroll
+    for (int u = 0; u < kDzUnroll; ++u) {
+      raw[u] = raw_next[u];
+      c[u] = c_next[u];
+      scale[u] = scale_next[u];
+    }
+    fetch(base + 8 * kDzUnroll);
 #pragma unroll
     for (int u = 0; u < kDzUnroll; ++u) {
       const int64_t r = base + 8 * u;
-      float d[8];
-      v8::unpack(raw[u], d);
-      if (ACT) {
-        float zv[8], sl[8];
-        const float unit = ck::unit_of(scale[u]);
-        ck::unpack_codes4(codes[u].x, unit, zv[0], zv[1], zv[2], zv[3]);
-        ck::unpack_codes4(codes[u].y, unit, zv[4], zv[5], zv[6], zv[7]);
-        lin::act_all<true>(p.act, zv, sl);
-        if (!in || r >= r1) continue;  // (zero codes of a row that is not there)
+      if (!in || r >= r1) continue;
+      float f[8];
+      v8::unpack(raw[u], f);
+      uint64_t d[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) d[i] *= sl[i];
+      for (int i = 0; i < 4; ++i) d[i] = f2(f[2 * i], f[2 * i + 1]);
+      if (ACT != lin::kActNone) {
+        const float unit = ck::unit_of(scale[u]);
+        uint64_t z[4];
+        ck::unpack_codes4(c[u].x, unit, z[0], z[1]);
+        ck::unpack_codes4(c[u].y, unit, z[2], z[3]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint64_t slope = 0;
+          lin::act2<ACT, true>(z[i], slope);
+          d[i] = mul2(d[i], slope);
+          f2_split(d[i], f[2 * i], f[2 * i + 1]);
+        }
         v8::Raw<__nv_bfloat16> o;
-        v8::pack(d, o);
-        *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.dz) + size_t(r) * p.C + col) = o.a;
+        v8::pack(f, o);
+        *reinterpret_cast<uint4 *>(dz + r * p.C) = o.a;
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum[i] += d[i];
+      for (int i = 0; i < 4; ++i) sum[i] = add2(sum[i], d[i]);
     }
   }
   if (!p.partial) return;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) red[warp][8 * lane + i] = sum[i];
+  for (int i = 0; i < 4; ++i) f2_split(sum[i], red[warp][8 * lane + 2 * i], red[warp][8 * lane + 2 * i + 1]);
   __syncthreads();
-  const int32_t c = int32_t(blockIdx.x) * 256 + int32_t(threadIdx.x);
-  if (c >= p.C) return;
+  const int32_t out = int32_t(blockIdx.x) * 256 + int32_t(threadIdx.x);
+  if (out >= p.C) return;
   float s = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) s += red[i][threadIdx.x];
-  p.partial[size_t(blockIdx.y) * p.C + c] = s;
+  p.partial[size_t(blockIdx.y) * p.C + out] = s;
 }
 
 // Sums the chunks' columns in a fixed order: 8 slices of the chunks, then the slices.
@@ -838,10 +853,14 @@ int32_t linear_dz_chunk_rows(int64_t M, int32_t C) {
 cudaError_t launch_linear_dz(const LinearDzParams &p, float *db, cudaStream_t stream) {
   const int64_t chunks = (p.M + p.chunk_rows - 1) / p.chunk_rows;
   const dim3 grid(unsigned((p.C + 255) / 256), unsigned(chunks));
-  if (p.act != lin::kActNone)
-    linear_dz_kernel<true><<<grid, 256, 0, stream>>>(p);
+  if (p.act == lin::kActNone)
+    linear_dz_kernel<lin::kActNone><<<grid, 256, 0, stream>>>(p);
+  else if (p.act == lin::kActGeluTanh)
+    linear_dz_kernel<lin::kActGeluTanh><<<grid, 256, 0, stream>>>(p);
+  else if (p.act == lin::kActGelu)
+    linear_dz_kernel<lin::kActGelu><<<grid, 256, 0, stream>>>(p);
   else
-    linear_dz_kernel<false><<<grid, 256, 0, stream>>>(p);
+    linear_dz_kernel<lin::kActSilu><<<grid, 256, 0, stream>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !db) return e;
   column_sum_kernel<<<unsigned((p.C + 31) / 32), 256, 0, stream>>>(p.partial, int32_t(chunks), p.C, db);

@@ -78,9 +78,13 @@ __global__ void __launch_bounds__(256) rope_table_kernel(const RopeTableParams p
   }
   for (int64_t n = row0; n < p.N; n += step) {
     float c[V], s[V];
+    const I *row = static_cast<const I *>(p.pos) + n * p.A;
+    double pos = double(__ldg(row + ax[0]));
 #pragma unroll
-    for (int e = 0; e < V; ++e)
-      cos_sin(double(__ldg(static_cast<const I *>(p.pos) + n * p.A + ax[e])), freq[e], p.mscale, c[e], s[e]);
+    for (int e = 0; e < V; ++e) {
+      if (e && ax[e] != ax[e - 1]) pos = double(__ldg(row + ax[e]));  // neighbouring pairs mostly share their axis
+      cos_sin(pos, freq[e], p.mscale, c[e], s[e]);
+    }
     const int64_t at = n * p.P + i;
     if constexpr (V == 4) {
       __stcs(reinterpret_cast<float4 *>(p.cos + at), make_float4(c[0], c[1], c[2], c[3]));
@@ -636,7 +640,7 @@ namespace {
 // The grid's threads are a whole number of rows: a multiple of `cols` blocks.
 template <typename I, int V>
 cudaError_t launch_table(const RopeTableParams &p, cudaStream_t stream) {
-  const int64_t cols = p.P / V, most = 148 * 32;
+  const int64_t cols = p.P / V, most = 148 * 8;
   const int64_t want = (p.N * cols + 255) / 256;
   int64_t blocks = want < most ? want : most;
   blocks = (blocks + cols - 1) / cols * cols;
