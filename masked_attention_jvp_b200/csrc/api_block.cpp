@@ -62,7 +62,7 @@ caj_status check_rope(const caj_qk_rope_shape *s, const float *gq, const float *
   if (s->pairs % 8) return CAJ_ERR_UNSUPPORTED;
   const int64_t wide = int64_t(s->Hq > s->Hk ? s->Hq : s->Hk) * s->D;
   if (wide > 8192) return CAJ_ERR_UNSUPPORTED;
-  if (int64_t(s->B) * s->N > (int64_t(1) << 31) - 1) return CAJ_ERR_UNSUPPORTED;
+  if (int64_t(s->B) * s->N > (int64_t(1) << 30)) return CAJ_ERR_UNSUPPORTED;  // walks step past the last token
   return CAJ_OK;
 }
 

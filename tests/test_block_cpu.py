@@ -126,7 +126,8 @@ _SHAPE_REFUSALS = [
     (dict(norm=3), INVALID), (dict(norm=-1), INVALID), (dict(layout=2), INVALID), (dict(gain_full=2), INVALID),
     (dict(norm=2), INVALID), (dict(eps=0.0), INVALID), (dict(eps=-1.0), INVALID), (dict(eps=float("nan")), INVALID),
     (dict(eps=float("inf")), INVALID), (dict(D=96, pairs=32), UNSUPPORTED), (dict(D=512), UNSUPPORTED),
-    (dict(pairs=20), UNSUPPORTED), (dict(Hq=129), UNSUPPORTED), (dict(B=1 << 16, N=1 << 16), UNSUPPORTED)]
+    (dict(pairs=20), UNSUPPORTED), (dict(Hq=129), UNSUPPORTED), (dict(B=1 << 16, N=1 << 16), UNSUPPORTED),
+    (dict(B=1, N=(1 << 30) + 1), UNSUPPORTED)]
 
 
 @pytest.mark.parametrize("kw,want", _SHAPE_REFUSALS + [

@@ -132,6 +132,11 @@ CASES = [  # B, N, H, Hk, D, P, norm, layout, dtype, gains over all channels
     (2, 11, 5, 5, 64, 24, "none", "interleaved", BF, False),
     (1, 13, 7, 3, 128, 56, "none", "half", F32, False),
     (1, 3000, 2, 2, 64, 32, "head", "half", BF, False),
+    (1, 5, 32, 32, 256, 128, "token", "half", F32, True),     # the widest token, one token's copies at a time
+    (2, 400, 64, 8, 128, 64, "head", "interleaved", BF, True),
+    (1, 9, 256, 16, 32, 16, "token", "interleaved", BF, True),
+    (3, 1, 12, 12, 128, 64, "head", "half", BF, False),       # single tokens of a batch
+    (500, 2, 3, 3, 64, 32, "token", "half", F32, True),       # walks that cross many sequences
 ]
 
 
@@ -296,3 +301,29 @@ def test_calls_on_another_stream_and_in_a_graph():
     for _, got in graphs:
         for a, b in zip(want, got):
             assert torch.equal(a, b)
+
+
+def test_offsets_past_32_bits():
+    """Tensors of more than 2^31 elements: the last tokens must equal a call on them alone."""
+    H, D, N = 12, 128, 1_450_000
+    x = torch.zeros(1, N, H * D, dtype=BF, device="cuda")
+    tail = 300
+    g = torch.Generator().manual_seed(1)
+    x[:, -tail:] = torch.randn(1, tail, H * D, generator=g).to(BF).cuda()
+    assert x.numel() > 2 ** 31
+    gain = torch.ones(D, device="cuda")
+    cos, sin = caj.rope_table(torch.arange(N, device="cuda"), caj.rope_frequencies(D)[0])
+    q, k = caj.qk_norm_rope_fwd(x, x, None, gain, gain, cos, sin, H)
+    small = caj.qk_norm_rope_fwd(*[x[:, -tail:].contiguous()] * 2, None, gain, gain, cos[-tail:].contiguous(),
+                                 sin[-tail:].contiguous(), H)
+    assert torch.equal(q[:, :, -tail:], small[0]) and torch.equal(k[:, :, -tail:], small[1])
+    del k
+    kept = caj.ckpt8_pack(x)
+    assert torch.equal(caj.ckpt8_unpack(kept)[:, -tail:], caj.ckpt8_unpack(caj.ckpt8_pack(x[:, -tail:])))
+    dxq, dxk, _, dgq, _ = caj.qk_norm_rope_bwd(q, q, None, kept, kept, gain, gain, cos, sin)
+    few = caj.ckpt8_pack(x[:, -tail:].contiguous())
+    want = caj.qk_norm_rope_bwd(*[q[:, :, -tail:].contiguous()] * 2, None, few, few, gain, gain,
+                                cos[-tail:].contiguous(), sin[-tail:].contiguous())
+    assert torch.equal(dxq[:, -tail:], want[0]) and torch.equal(dxk[:, -tail:], want[1])
+    # zeros elsewhere: the same sums in another order, K roundings of at most the sum of magnitudes
+    assert float((dgq - want[3]).abs().max()) <= 1e-4 * tail * H

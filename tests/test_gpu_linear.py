@@ -261,3 +261,45 @@ def test_other_streams_and_graphs():
     for _, out in graphs:
         for s, t in zip(want, out):
             assert torch.equal(s, t)
+
+
+def test_two_calls_at_once():
+    """Two streams, each with its own workspace; both kernels take every SM that is free."""
+    g = torch.Generator().manual_seed(11)
+    a = [rnd(g, 700, 1024).cuda(), rnd(g, 512, 1024, std=0.03).cuda()]
+    b = [rnd(g, 300, 4096).cuda(), rnd(g, 256, 4096, std=0.02).cuda()]
+    want = [caj.linear_act_fwd(*t, act="silu", tx=t[0], save_pre=True) for t in (a, b)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = []
+    for _ in range(8):
+        for s, t in zip(streams, (a, b)):
+            with torch.cuda.stream(s):
+                got.append(caj.linear_act_fwd(*t, act="silu", tx=t[0], save_pre=True))
+    torch.cuda.synchronize()
+    caj.device_status()
+    for i, (y, ty, pre) in enumerate(got):
+        w = want[i % 2]
+        assert torch.equal(y, w[0]) and torch.equal(ty, w[1])
+        assert torch.equal(pre.codes, w[2].codes) and torch.equal(pre.scales, w[2].scales)
+
+
+def test_outputs_past_32_bits():
+    """More than 2^31 outputs: the last rows must equal a call on them alone (one block of the
+    contraction, so both sum alike)."""
+    g = torch.Generator().manual_seed(12)
+    M, K, C = 360_000, 64, 6144
+    x, w = torch.zeros(M, K, dtype=BF, device="cuda"), rnd(g, C, K, std=0.2).cuda()
+    tail = 128 * 2 + 128 + 64
+    x[-tail:] = rnd(g, tail, K).cuda()
+    y, ty, pre = caj.linear_act_fwd(x, w, act="gelu_tanh", tx=x, save_pre=True)
+    assert y.numel() > 2 ** 31
+    few = caj.linear_act_fwd(x[-tail:], w, act="gelu_tanh", tx=x[-tail:], save_pre=True)
+    assert torch.equal(y[-tail:], few[0]) and torch.equal(ty[-tail:], few[1])
+    assert torch.equal(pre.codes[-tail:], few[2].codes) and torch.equal(pre.scales[-tail:], few[2].scales)
+    dx, dw, db = caj.linear_act_bwd(y, x, w, act="gelu_tanh", pre=pre, need=(True, False), bias=False)
+    want = caj.linear_act_bwd(few[0], x[-tail:], w, act="gelu_tanh", pre=few[2], need=(True, False), bias=False)
+    rel = float((dx[-tail:].float() - want[0].float()).norm() / want[0].float().norm())
+    assert rel <= 2.0 ** -8  # the contraction may be split differently: one rounding apart
+    caj.device_status()
