@@ -2,16 +2,15 @@
 // scale bytes, and back (format and rounding: ckpt8.cuh).
 //
 // Memory-bound: 3.03 bytes a value for bf16 (2 in, 1.03 out, or the reverse).
-// Vector form: packing, two lanes hold a block, sixteen values each (16-byte loads and
-// stores), and the block's largest magnitude is one shuffle away; unpacking, four lanes,
-// eight values each, so that a warp's 16-byte stores are neighbours.
-// Each thread takes kUnroll blocks a grid apart, with all loads issued first, to
-// keep enough bytes in flight.
-// Rows whose 16-byte vectors do not line up (C not a multiple of 8, or a base or
-// row stride that is not 16-byte aligned) take the lane form: one lane per value,
-// coalesced 2- or 4-byte accesses, the maximum by one redux instruction.
-// 32760 x 1536 bf16 on B200: PACKED us packed, UNPACKED us unpacked in the vector form;
-// 32760 x 1545 ODDP and ODDU us in the lane form.
+// Packing: two lanes hold a block, sixteen values each, and the block's largest magnitude
+// is one shuffle away. Rows may start anywhere (an odd width): a lane loads the aligned
+// 16-byte words around its values and shifts them into place, some 30 instructions that
+// memory hides. (A lane per value with 2-byte loads took 82 us where this takes ODDP.)
+// Unpacking: four lanes a block, eight values each, so that a warp's 16-byte stores are
+// neighbours; where those do not line up (C not a multiple of 8, or a base or row distance
+// that is not 16-byte aligned), a lane per value.
+// 32760 x 1536 bf16 on B200: PACKED us packed, UNPACKED us unpacked (floor 23.3); 32760 x
+// 1545 ODDP and ODDU us.
 #include <cuda_runtime.h>
 
 #include "ckpt8.cuh"
@@ -31,45 +30,92 @@ __device__ __forceinline__ void store_scale(uint8_t *row, int32_t blk, int32_t n
     for (int32_t i = nb; i < ns; ++i) row[i] = 0;
 }
 
+// Sixteen values from any address: `granules` 16-byte words from the aligned address below
+// it, shifted into place by the remainder (bits 8, 4 and 2 of it in turn).
 template <typename T>
-__global__ void __launch_bounds__(kThreads) pack_vec_kernel(const Ckpt8Params p) {
+struct Sixteen {
+  static constexpr int kWords = 4 * int(sizeof(T));  // 32-bit words of 16 values
+  static constexpr int kGranules = kWords / 4;
+  uint32_t w[kWords + 4];
+  // Loads what lies below `end`, the row's last byte + 1: a word that holds a byte of the row
+  // lies in the row's allocation, whose granules are larger than 16 bytes.
+  template <bool ALIGNED>
+  __device__ __forceinline__ void load(const uint8_t *at, const uint8_t *end) {
+    const uint8_t *base = reinterpret_cast<const uint8_t *>(reinterpret_cast<uintptr_t>(at) & ~uintptr_t(15));
+    const bool more = !ALIGNED && base != at;
+#pragma unroll
+    for (int i = 0; i <= kGranules; ++i) {
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (base + 16 * i < end && (i < kGranules || more))
+        v = ALIGNED ? __ldcs(reinterpret_cast<const uint4 *>(base) + i) : __ldg(reinterpret_cast<const uint4 *>(base) + i);
+      w[4 * i] = v.x;
+      w[4 * i + 1] = v.y;
+      w[4 * i + 2] = v.z;
+      w[4 * i + 3] = v.w;
+    }
+  }
+  __device__ __forceinline__ void shift(uint32_t rest) {
+#pragma unroll
+    for (int i = 0; i < kWords + 2; ++i) w[i] = rest & 8 ? w[i + 2] : w[i];
+#pragma unroll
+    for (int i = 0; i < kWords + 1; ++i) w[i] = rest & 4 ? w[i + 1] : w[i];
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 8 * (rest & 2));
+    }
+  }
+  __device__ __forceinline__ void values(float (&f)[16]) const {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      if constexpr (sizeof(T) == 4)
+        f[i] = __uint_as_float(w[i]);
+      else
+        f[i] = __uint_as_float(i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
+    }
+  }
+};
+
+// ALIGNED: rows of whole 16-byte words, so there is nothing to shift or to cut off.
+template <typename T, bool ALIGNED>
+__global__ void __launch_bounds__(kThreads) pack_kernel(const Ckpt8Params p) {
   const uint32_t nb = uint32_t(p.nb), total = p.total;
   const uint32_t step = gridDim.x * (kThreads / 2);
   const uint32_t first = blockIdx.x * (kThreads / 2) + (threadIdx.x >> 1);
   const int part = threadIdx.x & 1;
-  v8::Raw<T> raw[kUnroll][2];
-  uint32_t row[kUnroll], blk[kUnroll];
+  Sixteen<T> in[kUnroll];
+  uint32_t row[kUnroll], blk[kUnroll], rest[kUnroll];
 #pragma unroll
   for (int u = 0; u < kUnroll; ++u) {
     const uint64_t g = uint64_t(first) + uint64_t(u) * step;
     row[u] = g < total ? uint32_t(g) / nb : 0xFFFFFFFFu;
     blk[u] = uint32_t(g) - row[u] * nb;
-    const int32_t c = int32_t(blk[u]) * ck::kBlock + 16 * part;
-    const T *src = static_cast<const T *>(p.x) + size_t(row[u]) * p.ld + c;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      raw[u][h] = v8::zero<T>();
-      if (g < total && c + 8 * h < p.cols) raw[u][h] = v8::load(src + 8 * h);  // cols is a multiple of 8 here
-    }
+    const T *x = static_cast<const T *>(p.x) + size_t(g < total ? row[u] : 0) * p.ld;
+    const uint8_t *at = reinterpret_cast<const uint8_t *>(x + int32_t(blk[u]) * ck::kBlock + 16 * part);
+    rest[u] = uint32_t(reinterpret_cast<uintptr_t>(at)) & 15u;
+    in[u].template load<ALIGNED>(at, g < total ? reinterpret_cast<const uint8_t *>(x + p.cols) : nullptr);
   }
 #pragma unroll
   for (int u = 0; u < kUnroll; ++u) {
-    float f[2][8];
-    v8::unpack(raw[u][0], f[0]);
-    v8::unpack(raw[u][1], f[1]);
-    float m = ck::max_nan(ck::max_mag(f[0]), ck::max_mag(f[1]));
+    if (!ALIGNED) in[u].shift(rest[u]);
+    float f[16];
+    in[u].values(f);
+    if (!ALIGNED && blk[u] == nb - 1) {  // what lies past the row's last column is not its own
+      const int32_t left = p.cols - int32_t(blk[u]) * ck::kBlock - 16 * part;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) f[i] = i < left ? f[i] : 0.f;
+    }
+    float m = ck::max_mag(f);
     m = ck::max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
     if (row[u] == 0xFFFFFFFFu) continue;
     const uint32_t s = ck::scale_of(__float_as_uint(m));
     uint4 codes = make_uint4(0, 0, 0, 0);
     if (s != 255u) {
       const float up = ck::up_of(s);
-      ck::saturate(f[0], s);
-      ck::saturate(f[1], s);
-      codes.x = ck::pack_codes4(f[0][0], f[0][1], f[0][2], f[0][3], up);
-      codes.y = ck::pack_codes4(f[0][4], f[0][5], f[0][6], f[0][7], up);
-      codes.z = ck::pack_codes4(f[1][0], f[1][1], f[1][2], f[1][3], up);
-      codes.w = ck::pack_codes4(f[1][4], f[1][5], f[1][6], f[1][7], up);
+      ck::saturate(f, s);
+      codes.x = ck::pack_codes4(f[0], f[1], f[2], f[3], up);
+      codes.y = ck::pack_codes4(f[4], f[5], f[6], f[7], up);
+      codes.z = ck::pack_codes4(f[8], f[9], f[10], f[11], up);
+      codes.w = ck::pack_codes4(f[12], f[13], f[14], f[15], up);
     }
     const size_t base = (size_t(row[u]) * nb + blk[u]) * ck::kBlock + 16 * part;
     __stcs(reinterpret_cast<uint4 *>(p.codes + base), codes);
@@ -112,36 +158,9 @@ __global__ void __launch_bounds__(kThreads) unpack_vec_kernel(const Ckpt8Params 
   }
 }
 
-// One lane per value: a warp takes a run of up to eight blocks of one row.
+// Unpacking to rows that do not line up: one lane per value; a warp takes a run of up to
+// eight blocks of one row.
 constexpr int kRun = 8;
-
-template <typename T>
-__global__ void __launch_bounds__(kThreads) pack_lane_kernel(const Ckpt8Params p) {
-  const uint32_t runs = (uint32_t(p.nb) + kRun - 1) / kRun;
-  const uint32_t unit = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  const uint32_t row = unit / runs;
-  if (row >= p.rows) return;
-  const int32_t blk0 = int32_t(unit - row * runs) * kRun;
-  const T *x = static_cast<const T *>(p.x) + size_t(row) * p.ld + blk0 * ck::kBlock + lane;
-  int8_t *codes = p.codes + (size_t(row) * p.nb + blk0) * ck::kBlock + lane;
-  const int32_t left = p.cols - blk0 * ck::kBlock - lane, blocks = min(kRun, p.nb - blk0);
-  float v[kRun];
-#pragma unroll
-  for (int j = 0; j < kRun; ++j) v[j] = 32 * j < left ? v8::to_float(x[32 * j]) : 0.f;
-  uint32_t mine = 0;  // lane j keeps the scale of block j
-#pragma unroll
-  for (int j = 0; j < kRun; ++j) {
-    const uint32_t s = ck::scale_of(__reduce_max_sync(0xFFFFFFFFu, ck::mag_bits(v[j])));
-    if (lane == j) mine = s;
-    if (j >= blocks) continue;
-    float f[1] = {v[j]};
-    ck::saturate(f, s);
-    codes[32 * j] = s == 255u ? int8_t(0) : int8_t(ck::code_word(f[0], ck::up_of(s)) & 0xFFu);
-  }
-  if (lane < kRun && blk0 + lane < p.ns)  // runs start at multiples of 8: padding bytes included
-    p.scales[size_t(row) * p.ns + blk0 + lane] = uint8_t(lane < blocks ? mine : 0u);
-}
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads) unpack_lane_kernel(const Ckpt8Params p) {
@@ -170,20 +189,23 @@ __global__ void __launch_bounds__(kThreads) unpack_lane_kernel(const Ckpt8Params
 }
 
 template <typename T>
-cudaError_t launch(const Ckpt8Params &p, bool unpack, bool vec, cudaStream_t stream) {
-  const uint64_t units = vec ? p.total : uint64_t(p.rows) * ((p.nb + kRun - 1) / kRun);
-  const uint32_t per_cta = !vec ? kThreads / 32 : unpack ? kThreads / 4 * kUnpackUnroll : kThreads / 2 * kUnroll;
-  const unsigned grid = unsigned((units + per_cta - 1) / per_cta);
-  if (unpack) {
-    if (vec)
-      unpack_vec_kernel<T><<<grid, kThreads, 0, stream>>>(p);
+cudaError_t launch(const Ckpt8Params &p, bool unpack, cudaStream_t stream) {
+  const void *values = unpack ? p.out : p.x;
+  const bool aligned = p.cols % 8 == 0 && (reinterpret_cast<uintptr_t>(values) & 15u) == 0 &&
+                       p.ld * int64_t(sizeof(T)) % 16 == 0;
+  if (!unpack) {
+    const uint32_t per_cta = kThreads / 2 * kUnroll;
+    const unsigned grid = unsigned((uint64_t(p.total) + per_cta - 1) / per_cta);
+    if (aligned)
+      pack_kernel<T, true><<<grid, kThreads, 0, stream>>>(p);
     else
-      unpack_lane_kernel<T><<<grid, kThreads, 0, stream>>>(p);
+      pack_kernel<T, false><<<grid, kThreads, 0, stream>>>(p);
+  } else if (aligned) {
+    const uint32_t per_cta = kThreads / 4 * kUnpackUnroll;
+    unpack_vec_kernel<T><<<unsigned((uint64_t(p.total) + per_cta - 1) / per_cta), kThreads, 0, stream>>>(p);
   } else {
-    if (vec)
-      pack_vec_kernel<T><<<grid, kThreads, 0, stream>>>(p);
-    else
-      pack_lane_kernel<T><<<grid, kThreads, 0, stream>>>(p);
+    const uint64_t units = uint64_t(p.rows) * ((p.nb + kRun - 1) / kRun);
+    unpack_lane_kernel<T><<<unsigned((units + kThreads / 32 - 1) / (kThreads / 32)), kThreads, 0, stream>>>(p);
   }
   return cudaGetLastError();
 }
@@ -191,10 +213,7 @@ cudaError_t launch(const Ckpt8Params &p, bool unpack, bool vec, cudaStream_t str
 }  // namespace
 
 cudaError_t launch_ckpt8(const Ckpt8Params &p, bool unpack, bool bf16, cudaStream_t stream) {
-  const void *base = unpack ? p.out : p.x;
-  const int64_t size = bf16 ? 2 : 4;
-  const bool vec = p.cols % 8 == 0 && (reinterpret_cast<uintptr_t>(base) & 15u) == 0 && (p.ld * size) % 16 == 0;
-  return bf16 ? launch<__nv_bfloat16>(p, unpack, vec, stream) : launch<float>(p, unpack, vec, stream);
+  return bf16 ? launch<__nv_bfloat16>(p, unpack, stream) : launch<float>(p, unpack, stream);
 }
 
 }  // namespace caj

@@ -234,85 +234,104 @@ __device__ __forceinline__ void group_sums(float (&v)[M], const Lane &l, const Q
   }
 }
 
-// Forward: a thread has its eight channels of q, k and v of one token (and tangents), so
-// up to six 16-byte loads are in flight and the angles serve four vectors.
+// Tokens a thread of the forward takes at a time.
+template <typename T, bool TAN>
+__host__ __device__ constexpr int fwd_tokens() {
+  return !TAN && sizeof(T) == 2 ? 2 : 1;
+}
+
+// Forward: a thread has its eight channels of q, k and v of U tokens (and tangents), so
+// six 16-byte loads are in flight and the angles serve two to four vectors: two tokens a
+// thread without tangents, one with. (One token without tangents: 8.6 us for a frame of
+// 1560 tokens and 239 for 65520, against FRAME and LONG.)
 // MAXT: 256 threads leave 80 registers each, 1024 (tokens wider than 2048 channels) 64.
 template <typename T, bool TAN, bool HALF, int MAXT>
 __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 3 : 1) qk_rope_fwd_kernel(const QkRopeParams p) {
   extern __shared__ float red[];
+  constexpr int U = fwd_tokens<T, TAN>();
   const Lane l = lane_of(p);
-  const int32_t tok = int32_t(min(int64_t(blockIdx.x) * l.T + l.t, int64_t(0x7FFFFFFF)));
-  const bool here = l.t < l.T && tok < p.B * p.N;
-  const int32_t b = here ? tok / p.N : 0, n = here ? tok - b * p.N : 0;
   const int32_t heads[3] = {p.Hq, p.Hk, p.x[2] ? p.Hk : 0};
-  v8::Raw<T> raw[3], traw[3];
-  bool on[3];
+  const bool turns = l.d0 < 2 * p.P;
+  v8::Raw<T> raw[U][3], traw[U][3];
+  Turn<HALF, false> turn[U];
+  bool here[U];
+  int32_t b[U], n[U];
 #pragma unroll
-  for (int i = 0; i < 3; ++i) {
-    on[i] = here && l.head < heads[i];
-    raw[i] = v8::zero<T>();
-    if (TAN) traw[i] = v8::zero<T>();
-    if (on[i]) {
-      raw[i] = v8::load(static_cast<const T *>(p.x[i]) + tok * p.ld[i] + 8 * l.vec);
-      if (TAN) traw[i] = v8::load(static_cast<const T *>(p.tx[i]) + tok * p.tld[i] + 8 * l.vec);
-    }
-  }
-  Turn<HALF, false> turn;
-  turn.rest();
-  if (here && l.d0 < 2 * p.P) {
-    const size_t at = size_t(n) * p.P + turn.offset(p, l);
+  for (int u = 0; u < U; ++u) {
+    const int64_t tok64 = (int64_t(blockIdx.x) * U + u) * l.T + l.t;
+    here[u] = l.t < l.T && tok64 < int64_t(p.B) * p.N;
+    const int32_t tok = here[u] ? int32_t(tok64) : 0;
+    b[u] = tok / p.N;
+    n[u] = tok - b[u] * p.N;
 #pragma unroll
-    for (int i = 0; i < turn.kSlots / 2; ++i) {
-      turn.raw[i] = __ldg(reinterpret_cast<const float4 *>(p.cos + at) + i);
-      turn.raw[turn.kSlots / 2 + i] = __ldg(reinterpret_cast<const float4 *>(p.sin + at) + i);
-    }
-  }
-  turn.set(p, l);
-  auto place = [&](int i) { return ((size_t(b) * heads[i] + l.head) * p.N + n) * p.D + l.d0; };
-  if (on[2]) {
-    v8::store(static_cast<T *>(p.y[2]) + place(2), raw[2]);
-    if (TAN) v8::store(static_cast<T *>(p.ty[2]) + place(2), traw[2]);
-  }
-  uint64_t x[2][4], tx[2][4];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    unpack(raw[i], x[i]);
-    if (TAN) unpack(traw[i], tx[i]);
-  }
-  if (p.norm != kNormNone) {
-    float sums[TAN ? 4 : 2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      sums[i] = dot(x[i], x[i]);
-      if constexpr (TAN) sums[2 + i] = dot(x[i], tx[i]);
-    }
-    group_sums(sums, l, p, red);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float inv_len = 1.f / float(p.norm == kNormHead ? p.D : heads[i] * p.D);
-      const float inv = rsqrtf(fmaf(sums[i], inv_len, p.eps));
-      const uint64_t inv2 = f2(inv, inv);
-      uint64_t g[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) g[j] = 0;
-      if (on[i]) load_pairs(p.g[i] + (p.gain_full ? 8 * l.vec : l.d0), g);
-      if constexpr (TAN) {
-        const float k3 = -(inv * inv * inv * (sums[2 + i] * inv_len));
-        const uint64_t k32 = f2(k3, k3);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) tx[i][j] = mul2(g[j], fma2(tx[i][j], inv2, mul2(x[i][j], k32)));
+    for (int i = 0; i < 3; ++i) {
+      raw[u][i] = v8::zero<T>();
+      if (TAN) traw[u][i] = v8::zero<T>();
+      if (here[u] && l.head < heads[i]) {
+        raw[u][i] = v8::load(static_cast<const T *>(p.x[i]) + tok * p.ld[i] + 8 * l.vec);
+        if (TAN) traw[u][i] = v8::load(static_cast<const T *>(p.tx[i]) + tok * p.tld[i] + 8 * l.vec);
       }
+    }
+    turn[u].rest();
+    if (here[u] && turns) {
+      const size_t at = size_t(n[u]) * p.P + turn[u].offset(p, l);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) x[i][j] = mul2(x[i][j], mul2(g[j], inv2));
+      for (int i = 0; i < turn[u].kSlots / 2; ++i) {
+        turn[u].raw[i] = __ldg(reinterpret_cast<const float4 *>(p.cos + at) + i);
+        turn[u].raw[turn[u].kSlots / 2 + i] = __ldg(reinterpret_cast<const float4 *>(p.sin + at) + i);
+      }
     }
   }
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    turn.apply(x[i]);
-    if (TAN) turn.apply(tx[i]);
-    if (on[i]) {
-      v8::store(static_cast<T *>(p.y[i]) + place(i), pack<T>(x[i]));
-      if (TAN) v8::store(static_cast<T *>(p.ty[i]) + place(i), pack<T>(tx[i]));
+  for (int u = 0; u < U; ++u) {
+    turn[u].set(p, l);
+    const bool on[3] = {here[u] && l.head < heads[0], here[u] && l.head < heads[1], here[u] && l.head < heads[2]};
+    auto place = [&](int i) { return ((size_t(b[u]) * heads[i] + l.head) * p.N + n[u]) * p.D + l.d0; };
+    if (on[2]) {
+      v8::store(static_cast<T *>(p.y[2]) + place(2), raw[u][2]);
+      if (TAN) v8::store(static_cast<T *>(p.ty[2]) + place(2), traw[u][2]);
+    }
+    uint64_t x[2][4], tx[2][4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      unpack(raw[u][i], x[i]);
+      if (TAN) unpack(traw[u][i], tx[i]);
+    }
+    if (p.norm != kNormNone) {
+      float sums[TAN ? 4 : 2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        sums[i] = dot(x[i], x[i]);
+        if constexpr (TAN) sums[2 + i] = dot(x[i], tx[i]);
+      }
+      group_sums(sums, l, p, red);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float inv_len = 1.f / float(p.norm == kNormHead ? p.D : heads[i] * p.D);
+        const float inv = rsqrtf(fmaf(sums[i], inv_len, p.eps));
+        const uint64_t inv2 = f2(inv, inv);
+        uint64_t g[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) g[j] = 0;
+        if (on[i]) load_pairs(p.g[i] + (p.gain_full ? 8 * l.vec : l.d0), g);
+        if constexpr (TAN) {
+          const float k3 = -(inv * inv * inv * (sums[2 + i] * inv_len));
+          const uint64_t k32 = f2(k3, k3);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) tx[i][j] = mul2(g[j], fma2(tx[i][j], inv2, mul2(x[i][j], k32)));
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[i][j] = mul2(x[i][j], mul2(g[j], inv2));
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      turn[u].apply(x[i]);
+      if (TAN) turn[u].apply(tx[i]);
+      if (on[i]) {
+        v8::store(static_cast<T *>(p.y[i]) + place(i), pack<T>(x[i]));
+        if (TAN) v8::store(static_cast<T *>(p.ty[i]) + place(i), pack<T>(tx[i]));
+      }
     }
   }
 }
@@ -590,7 +609,8 @@ size_t token_norm_bytes(const QkRopeParams &p, int32_t values) {  // group_sums'
 template <typename T, bool TAN, int MAXT>
 cudaError_t launch_fwd(const QkRopeParams &p, cudaStream_t stream) {
   const int32_t threads = threads_for(p);
-  const unsigned grid = unsigned(groups_for(p));
+  constexpr int U = fwd_tokens<T, TAN>();
+  const unsigned grid = unsigned((groups_for(p) + U - 1) / U);
   const size_t smem = token_norm_bytes(p, TAN ? 4 : 2);
   if (p.half)
     qk_rope_fwd_kernel<T, TAN, true, MAXT><<<grid, threads, smem, stream>>>(p);
