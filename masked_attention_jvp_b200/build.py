@@ -22,7 +22,7 @@ SOURCES = ["api.cpp", "api_block.cpp", "api_linear.cpp", "fwd_jvp_sm100.cu", "fw
            "host_static.cu", "signal.cu", "out_proj_sm100.cu",
            "qk_rope.cu", "ckpt8.cu", "linear_sm100.cu"]
 HEADERS = ["api_internal.h", "kernels.h", "mask_schedule.h", "ptx_sm100.cuh", "vec8.cuh", "ckpt8.cuh",
-           "linear_act.cuh", "pair_sm100.cuh"]
+           "linear_act.cuh", "pair_sm100.cuh", "launch.h"]
 
 # Python entry of the block operators (torch tensors in, the library's calls below)
 BIND = "bind.cpp"

@@ -15,6 +15,7 @@
 
 #include "ckpt8.cuh"
 #include "kernels.h"
+#include "launch.h"
 #include "vec8.cuh"
 
 namespace caj {
@@ -78,6 +79,7 @@ struct Sixteen {
 // ALIGNED: rows of whole 16-byte words, so there is nothing to shift or to cut off.
 template <typename T, bool ALIGNED>
 __global__ void __launch_bounds__(kThreads) pack_kernel(const Ckpt8Params p) {
+  begin_after_previous();
   const uint32_t nb = uint32_t(p.nb), total = p.total;
   const uint32_t step = gridDim.x * (kThreads / 2);
   const uint32_t first = blockIdx.x * (kThreads / 2) + (threadIdx.x >> 1);
@@ -125,6 +127,7 @@ __global__ void __launch_bounds__(kThreads) pack_kernel(const Ckpt8Params p) {
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads) unpack_vec_kernel(const Ckpt8Params p) {
+  begin_after_previous();
   const uint32_t nb = uint32_t(p.nb), total = p.total;
   const uint32_t step = gridDim.x * (kThreads / 4);
   const uint32_t first = blockIdx.x * (kThreads / 4) + (threadIdx.x >> 2);
@@ -164,6 +167,7 @@ constexpr int kRun = 8;
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads) unpack_lane_kernel(const Ckpt8Params p) {
+  begin_after_previous();
   const uint32_t runs = (uint32_t(p.nb) + kRun - 1) / kRun;
   const uint32_t unit = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
@@ -193,21 +197,14 @@ cudaError_t launch(const Ckpt8Params &p, bool unpack, cudaStream_t stream) {
   const void *values = unpack ? p.out : p.x;
   const bool aligned = p.cols % 8 == 0 && (reinterpret_cast<uintptr_t>(values) & 15u) == 0 &&
                        p.ld * int64_t(sizeof(T)) % 16 == 0;
-  if (!unpack) {
-    const uint32_t per_cta = kThreads / 2 * kUnroll;
-    const unsigned grid = unsigned((uint64_t(p.total) + per_cta - 1) / per_cta);
-    if (aligned)
-      pack_kernel<T, true><<<grid, kThreads, 0, stream>>>(p);
-    else
-      pack_kernel<T, false><<<grid, kThreads, 0, stream>>>(p);
-  } else if (aligned) {
-    const uint32_t per_cta = kThreads / 4 * kUnpackUnroll;
-    unpack_vec_kernel<T><<<unsigned((uint64_t(p.total) + per_cta - 1) / per_cta), kThreads, 0, stream>>>(p);
-  } else {
-    const uint64_t units = uint64_t(p.rows) * ((p.nb + kRun - 1) / kRun);
-    unpack_lane_kernel<T><<<unsigned((units + kThreads / 32 - 1) / (kThreads / 32)), kThreads, 0, stream>>>(p);
-  }
-  return cudaGetLastError();
+  auto blocks = [](uint64_t units, uint32_t per_cta) { return dim3(unsigned((units + per_cta - 1) / per_cta)); };
+  if (!unpack)
+    return launch_in_order(aligned ? pack_kernel<T, true> : pack_kernel<T, false>, blocks(p.total, kThreads / 2 * kUnroll),
+                           kThreads, 0, stream, p);
+  if (aligned)
+    return launch_in_order(unpack_vec_kernel<T>, blocks(p.total, kThreads / 4 * kUnpackUnroll), kThreads, 0, stream, p);
+  const uint64_t runs = uint64_t(p.rows) * ((p.nb + kRun - 1) / kRun);
+  return launch_in_order(unpack_lane_kernel<T>, blocks(runs, kThreads / 32), kThreads, 0, stream, p);
 }
 
 }  // namespace

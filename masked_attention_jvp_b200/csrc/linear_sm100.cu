@@ -54,6 +54,7 @@
 
 #include "ckpt8.cuh"
 #include "kernels.h"
+#include "launch.h"
 #include "linear_act.cuh"
 #include "pair_sm100.cuh"
 #include "ptx_sm100.cuh"
@@ -178,6 +179,7 @@ __global__ void __launch_bounds__((Lay<JVP, TN>::THREADS), 1) linear_sm100_kerne
   pair::sync_cluster();  // barriers of both CTAs initialised, tensor memory allocated
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  begin_after_previous();
   auto wait = [&](uint32_t bar, uint32_t parity, uint32_t site) {
     return pair::wait_warp(bar, parity, &g_linear_error, abort_flag, p.timeout_ns, 0x100u | site);
   };
@@ -469,6 +471,7 @@ __global__ void __launch_bounds__((Lay<JVP, TN>::THREADS), 1) linear_sm100_kerne
 // does the epilogue. Four lanes hold a block of 32 columns, eight each.
 template <bool JVP, bool EPI>
 __global__ void __launch_bounds__(256) linear_finish_kernel(const LinearParams p) {
+  begin_after_previous();
   const int32_t vecs = ck::blocks_of(p.N) * 4;
   const int64_t g = int64_t(blockIdx.x) * 256 + threadIdx.x;
   const int64_t row = g / vecs;
@@ -592,6 +595,7 @@ __device__ __forceinline__ void rows_epilogue(const LinearParams &p, const float
 template <int NT, int MT>
 __global__ void __launch_bounds__(256) linear_rows_kernel(const LinearParams p) {
   extern __shared__ float red[];  // [8 warps][8 NT rows][columns + 1]
+  begin_after_previous();
   constexpr int kRows = 8 * NT, kCols = 16 * MT, kLd = kCols + 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int32_t base = int32_t(blockIdx.x) * kCols, rows = p.tx ? 2 * p.M : p.M;
@@ -676,6 +680,7 @@ constexpr int kDzUnroll = 2;
 template <int ACT>
 __global__ void __launch_bounds__(256, 4) linear_dz_kernel(const LinearDzParams p) {
   __shared__ float red[8][256];
+  begin_after_previous();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int32_t col = int32_t(blockIdx.x) * 256 + 8 * lane;
   const int64_t r0 = int64_t(blockIdx.y) * p.chunk_rows;
@@ -754,6 +759,7 @@ __global__ void __launch_bounds__(256, 4) linear_dz_kernel(const LinearDzParams 
 // Sums the chunks' columns in a fixed order: 8 slices of the chunks, then the slices.
 __global__ void __launch_bounds__(256) column_sum_kernel(const float *part, int32_t chunks, int32_t C, float *out) {
   __shared__ float s[8][32];
+  begin_after_previous();
   const int32_t c = int32_t(blockIdx.x) * 32 + int32_t(threadIdx.x & 31), slice = int32_t(threadIdx.x >> 5);
   float acc = 0.f;
   if (c < C) {
@@ -776,16 +782,18 @@ cudaError_t launch_tiles(const LinearParams &p, cudaStream_t stream) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.blockDim = dim3(Lay<JVP, TN>::THREADS);
   cfg.dynamicSmemBytes = Lay<JVP, TN>::SMEM;
   cfg.stream = stream;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 1;  // (the occupancy query takes the cluster alone)
   cfg.gridDim = dim3(2);
   // per device, once: the shared-memory limit and how many pairs fit at a time
   static std::atomic<uint64_t> set_up{0};
@@ -802,12 +810,12 @@ cudaError_t launch_tiles(const LinearParams &p, cudaStream_t stream) {
   const int64_t max_pairs = dev < 64 ? max_pairs_of[dev].load() : 74;
   const int64_t units = int64_t(p.m_tiles) * p.n_tiles * p.splits;
   cfg.gridDim = dim3(unsigned(2 * (units < max_pairs ? units : max_pairs)));
+  cfg.numAttrs = 2;
   e = cudaLaunchKernelEx(&cfg, kernel, p);
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess || p.splits == 1) return e;
   const int64_t threads = int64_t(p.M) * ck::blocks_of(p.N) * 4;
-  linear_finish_kernel<JVP, EPI><<<unsigned((threads + 255) / 256), 256, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch_in_order(linear_finish_kernel<JVP, EPI>, dim3(unsigned((threads + 255) / 256)), 256, 0, stream, p);
 }
 
 template <bool JVP, bool AMN, bool BMN, bool EPI>
@@ -822,10 +830,8 @@ cudaError_t launch_rows(const LinearParams &p, cudaStream_t stream) {
   constexpr int kSmem = 8 * 8 * NT * 33 * int(sizeof(float));
   static_assert(kSmem <= 48 * 1024, "shared memory without an attribute");
   if (p.codes || p.N > 32 * 148)
-    linear_rows_kernel<NT, 2><<<unsigned((p.N + 31) / 32), 256, kSmem, stream>>>(p);
-  else
-    linear_rows_kernel<NT, 1><<<unsigned((p.N + 15) / 16), 256, kSmem, stream>>>(p);
-  return cudaGetLastError();
+    return launch_in_order(linear_rows_kernel<NT, 2>, dim3(unsigned((p.N + 31) / 32)), 256, kSmem, stream, p);
+  return launch_in_order(linear_rows_kernel<NT, 1>, dim3(unsigned((p.N + 15) / 16)), 256, kSmem, stream, p);
 }
 
 }  // namespace
@@ -853,18 +859,12 @@ int32_t linear_dz_chunk_rows(int64_t M, int32_t C) {
 cudaError_t launch_linear_dz(const LinearDzParams &p, float *db, cudaStream_t stream) {
   const int64_t chunks = (p.M + p.chunk_rows - 1) / p.chunk_rows;
   const dim3 grid(unsigned((p.C + 255) / 256), unsigned(chunks));
-  if (p.act == lin::kActNone)
-    linear_dz_kernel<lin::kActNone><<<grid, 256, 0, stream>>>(p);
-  else if (p.act == lin::kActGeluTanh)
-    linear_dz_kernel<lin::kActGeluTanh><<<grid, 256, 0, stream>>>(p);
-  else if (p.act == lin::kActGelu)
-    linear_dz_kernel<lin::kActGelu><<<grid, 256, 0, stream>>>(p);
-  else
-    linear_dz_kernel<lin::kActSilu><<<grid, 256, 0, stream>>>(p);
-  cudaError_t e = cudaGetLastError();
+  void (*const kernels[4])(LinearDzParams) = {linear_dz_kernel<lin::kActNone>, linear_dz_kernel<lin::kActGeluTanh>,
+                                              linear_dz_kernel<lin::kActGelu>, linear_dz_kernel<lin::kActSilu>};
+  const cudaError_t e = launch_in_order(kernels[p.act], grid, 256, 0, stream, p);
   if (e != cudaSuccess || !db) return e;
-  column_sum_kernel<<<unsigned((p.C + 31) / 32), 256, 0, stream>>>(p.partial, int32_t(chunks), p.C, db);
-  return cudaGetLastError();
+  return launch_in_order(column_sum_kernel, dim3(unsigned((p.C + 31) / 32)), 256, 0, stream,
+                         static_cast<const float *>(p.partial), int32_t(chunks), p.C, db);
 }
 
 cudaError_t read_and_clear_linear_error(uint32_t *out) {

@@ -22,6 +22,7 @@
 
 #include "ckpt8.cuh"
 #include "kernels.h"
+#include "launch.h"
 #include "vec8.cuh"
 
 namespace caj {
@@ -64,6 +65,7 @@ __device__ __forceinline__ void cos_sin(double pos, double freq, float mscale, f
 // positions, so frequencies and axes stay in registers.
 template <typename I, int V>
 __global__ void __launch_bounds__(256) rope_table_kernel(const RopeTableParams p) {
+  begin_after_previous();
   const int32_t cols = p.P / V;  // threads across a row of pairs
   const int64_t id = int64_t(blockIdx.x) * 256 + threadIdx.x;
   const int64_t row0 = id / cols, step = int64_t(gridDim.x) * 256 / cols;  // a whole number of rows
@@ -248,6 +250,7 @@ __host__ __device__ constexpr int fwd_tokens() {
 template <typename T, bool TAN, bool HALF, int MAXT>
 __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 3 : 1) qk_rope_fwd_kernel(const QkRopeParams p) {
   extern __shared__ float red[];
+  begin_after_previous();
   constexpr int U = fwd_tokens<T, TAN>();
   const Lane l = lane_of(p);
   const int32_t heads[3] = {p.Hq, p.Hk, p.x[2] ? p.Hk : 0};
@@ -384,6 +387,7 @@ constexpr int bwd_slots() {
 template <typename T, bool CK, bool HALF, int MAXT>
 __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) qk_rope_bwd_kernel(const QkRopeParams p) {
   extern __shared__ __align__(16) uint8_t smem[];
+  begin_after_previous();
   using Rot = Turn<HALF, true>;
   constexpr int kVec = int(sizeof(T) / 2);  // slots of a vector of T
   constexpr int kSlots = bwd_slots<T, CK, HALF>(), kAngles = kSlots - Rot::kSlots;
@@ -571,6 +575,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) qk_rope_bwd_kernel(
 // Sums the blocks' partial dg in a fixed order: 8 slices of the blocks, then the slices.
 __global__ void __launch_bounds__(256) gain_grad_kernel(const QkRopeParams p) {
   __shared__ float s[8][32];
+  begin_after_previous();
   const int which = blockIdx.y;
   const int32_t len = p.gain_full ? (which ? p.Hk : p.Hq) * p.D : p.D;
   const int32_t c = int32_t(blockIdx.x) * 32 + int32_t(threadIdx.x & 31), slice = int32_t(threadIdx.x >> 5);
@@ -612,11 +617,8 @@ cudaError_t launch_fwd(const QkRopeParams &p, cudaStream_t stream) {
   constexpr int U = fwd_tokens<T, TAN>();
   const unsigned grid = unsigned((groups_for(p) + U - 1) / U);
   const size_t smem = token_norm_bytes(p, TAN ? 4 : 2);
-  if (p.half)
-    qk_rope_fwd_kernel<T, TAN, true, MAXT><<<grid, threads, smem, stream>>>(p);
-  else
-    qk_rope_fwd_kernel<T, TAN, false, MAXT><<<grid, threads, smem, stream>>>(p);
-  return cudaGetLastError();
+  return launch_in_order(p.half ? qk_rope_fwd_kernel<T, TAN, true, MAXT> : qk_rope_fwd_kernel<T, TAN, false, MAXT>,
+                         dim3(grid), threads, smem, stream, p);
 }
 template <typename T>
 cudaError_t launch_fwd(const QkRopeParams &p, cudaStream_t stream) {
@@ -640,12 +642,10 @@ cudaError_t launch_bwd(const QkRopeParams &params, cudaStream_t stream) {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kMaxSmem));
   });
   if (e != cudaSuccess) return e;
-  kernel<<<unsigned(p.blocks), threads, p.ring * token + extra, stream>>>(p);
-  e = cudaGetLastError();
+  e = launch_in_order(kernel, dim3(unsigned(p.blocks)), threads, p.ring * token + extra, stream, p);
   if (e != cudaSuccess || p.norm == kNormNone) return e;
   const int32_t len = p.gain_full ? vectors(p) * 8 : p.D;
-  gain_grad_kernel<<<dim3(unsigned((len + 31) / 32), 2), 256, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch_in_order(gain_grad_kernel, dim3(unsigned((len + 31) / 32), 2), 256, 0, stream, p);
 }
 template <typename T, bool CK>
 cudaError_t launch_bwd(const QkRopeParams &p, cudaStream_t stream) {
@@ -664,8 +664,7 @@ cudaError_t launch_table(const RopeTableParams &p, cudaStream_t stream) {
   const int64_t want = (p.N * cols + 255) / 256;
   int64_t blocks = want < most ? want : most;
   blocks = (blocks + cols - 1) / cols * cols;
-  rope_table_kernel<I, V><<<unsigned(blocks), 256, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch_in_order(rope_table_kernel<I, V>, dim3(unsigned(blocks)), 256, 0, stream, p);
 }
 }  // namespace
 
