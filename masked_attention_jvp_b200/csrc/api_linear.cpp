@@ -26,18 +26,20 @@ struct Plan {
 // tiles and in how many parts the contraction runs, by the least estimate of
 //   waves * (blocks of a part * block time + tile time) + parts written and read again.
 // 74 pairs of SMs work at a time; a 64-wide block of the contraction takes a pair 0.40 us
-// at 256 columns and 0.23 us at 128, a tile 1.5 us (1.0) besides; parts cost 8 bytes an
+// at 256 columns, 0.28 at 160 (forward only) and 0.23 at 128, a tile 1.0 to 1.5 us besides; parts cost 8 bytes an
 // output at about 5 TB/s and a launch (3 us). The figures only weigh one shape against
 // another. Measured on B200 (primal and tangent, 1560 tokens, 1536 x 1536): WIDE us with
 // 78 tiles of 256 columns, NARROW us with 156 of 128.
-Plan plan(int64_t rows, int64_t cols, int64_t depth, bool tangent) {
+Plan plan(int64_t rows, int64_t cols, int64_t depth, bool tangent, bool forward) {
   Plan best{};
   double best_us = 0;
   const int64_t tile_rows = tangent ? kTileRows / 2 : kTileRows, ops = tangent ? 2 : 1;
   const int64_t m_tiles = ceil_div(rows, tile_rows), k_blocks = ceil_div(depth, kBlock);
-  for (const int32_t tile_cols : {256, 128}) {
+  for (const int32_t tile_cols : {256, 160, 128}) {
+    if (tile_cols == 160 && !forward) continue;
     const int64_t n_tiles = ceil_div(cols, tile_cols), tiles = m_tiles * n_tiles;
-    const double block_us = tile_cols == 256 ? 0.40 : 0.23, tile_us = tile_cols == 256 ? 1.5 : 1.0;
+    const double block_us = tile_cols == 256 ? 0.40 : tile_cols == 160 ? 0.28 : 0.23;
+    const double tile_us = tile_cols == 256 ? 1.5 : tile_cols == 160 ? 1.2 : 1.0;
     for (int32_t s = 1; s <= 32 && s <= k_blocks; ++s) {
       const int64_t per = ceil_div(k_blocks, s);
       if (ceil_div(k_blocks, per) != s) continue;  // a part would be empty
@@ -100,8 +102,8 @@ struct BwdSizes {
 };
 BwdSizes bwd_sizes(const caj_linear_act_shape *s, bool x_ckpt, bool want_dx, bool want_dw, bool want_db) {
   BwdSizes b{};
-  b.dx = plan(s->M, s->K, s->C, false);
-  b.dw = plan(s->C, s->K, s->M, false);
+  b.dx = plan(s->M, s->K, s->C, false, false);
+  b.dw = plan(s->C, s->K, s->M, false, false);
   b.chunk_rows = caj::linear_dz_chunk_rows(s->M, s->C);
   if (x_ckpt && want_dw) b.x = padded(s->M * s->K * 2);
   if (s->act != CAJ_ACT_NONE) b.dz = padded(s->M * s->C * 2);
@@ -119,7 +121,7 @@ caj_status caj_linear_act_fwd_workspace(const caj_linear_act_shape *shape, int32
   if (!bytes || (tangent != 0 && tangent != 1)) return CAJ_ERR_INVALID_ARG;
   const caj_status st = check_shape(shape);
   if (st != CAJ_OK) return st;
-  *bytes = few_rows(shape->M, tangent) ? 0 : size_t(plan(shape->M, shape->C, shape->K, tangent).part_bytes);
+  *bytes = few_rows(shape->M, tangent) ? 0 : size_t(plan(shape->M, shape->C, shape->K, tangent, true).part_bytes);
   return CAJ_OK;
 }
 
@@ -140,7 +142,7 @@ caj_status caj_linear_act_fwd(const void *x, const void *tx, const void *w, cons
   if (!pre_codes != !pre_scales) return CAJ_ERR_INVALID_ARG;
   if (pre_codes && (!aligned_to(pre_codes, 16) || !aligned_to(pre_scales, 4))) return CAJ_ERR_INVALID_ARG;
   const bool few = few_rows(M, tan);
-  const Plan pl = plan(M, C, K, tan);
+  const Plan pl = plan(M, C, K, tan, true);
   if (!few && pl.part_bytes && (!workspace || !aligned_to(workspace, 16) || workspace_bytes < size_t(pl.part_bytes)))
     return CAJ_ERR_INVALID_ARG;
   st = caj::check_device();

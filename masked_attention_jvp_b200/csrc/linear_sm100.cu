@@ -31,8 +31,8 @@
 //               scheduler to stay ahead of the products: EPI8 us with eight, EPI16
 //               with sixteen (32760 x 1536 -> 6144, tangents, GELU, checkpoint).
 // Where 256-column tiles would leave the last wave of pairs mostly empty (a frame of
-// tokens: 78 tiles on 74 pairs), tiles of 128 columns are used: half the work each, a
-// little slower per product (A is copied twice as often).
+// tokens: 78 tiles on 74 pairs), tiles of 160 or 128 columns are used: less work each,
+// slower per product (A is copied more often).
 // Column blocks run fastest, so the pairs work on one band of A at a time and it is
 // read from DRAM once; weights stay in L2.
 //
@@ -74,13 +74,14 @@ constexpr uint32_t EX_BYTES = 32 * 128;   // z on its way to the tangents' warp:
 
 enum : uint32_t { kSiteEmpty = 0x21, kSiteFull, kSiteAccEmpty, kSiteAccFull, kSiteExEmpty, kSiteExFull };
 
-// TN: columns of a tile, 256 or 128. An epilogue warp has 32 rows and 64 columns.
+// TN: columns of a tile, 256, 160 or 128. An epilogue warp has 32 rows and 64 columns
+// (of 160, the last four warps 32).
 template <bool JVP, int TN>
 struct Lay {
-  static constexpr int EPI_WARPS = TN / 16, THREADS = 32 * (2 + EPI_WARPS);
+  static constexpr int EPI_WARPS = (TN + 63) / 64 * 4, THREADS = 32 * (2 + EPI_WARPS);
   static constexpr uint32_t B_BYTES = TN / 2 * TK * 2, STAGE_BYTES = A_BYTES + B_BYTES;
-  static constexpr int STAGES = TN == 256 ? 5 : 8;
-  static constexpr uint32_t TMEM_COLS = 2 * TN;
+  static constexpr int STAGES = TN == 256 ? 5 : TN == 160 ? 6 : 8;
+  static constexpr uint32_t TMEM_COLS = TN == 128 ? 256 : 512;  // two accumulators, a power of two
   static constexpr int OUT_BUFS = JVP ? 1 : 2, PAIRS = JVP ? EPI_WARPS / 2 : 0;
   static constexpr uint32_t OFF_OUT = STAGES * STAGE_BYTES;
   static constexpr uint32_t OFF_EX = OFF_OUT + EPI_WARPS * OUT_BUFS * OUT_BYTES;
@@ -124,11 +125,22 @@ __device__ __forceinline__ void fence_async_smem_then_store(const CUtensorMap *m
   __syncwarp();
 }
 
-// The two scale bytes of a row in one warp's 64 columns; the row's last pair also stores
-// the padding that rounds a row up to four.
-__device__ __forceinline__ void store_scales(uint8_t *at, uint32_t word, int32_t blk, const LinearParams &p) {
-  *reinterpret_cast<uint16_t *>(at) = uint16_t(word);
-  if (blk + 2 >= p.nb && blk + 4 <= p.ns) *reinterpret_cast<uint16_t *>(at + 2) = 0;
+// The scale bytes of a row in one warp's columns (two, or one at the end of a 160-column
+// tile); the row's last block also stores the padding that rounds a row up to four.
+template <int TN>
+__device__ __forceinline__ void store_scales(uint8_t *row, uint32_t word, int32_t blk, bool two, const LinearParams &p) {
+  if constexpr (TN % 64 == 0) {
+    *reinterpret_cast<uint16_t *>(row + blk) = uint16_t(word);  // blk is even; past the last block the word is zero
+    if (blk + 2 >= p.nb && blk + 4 <= p.ns) *reinterpret_cast<uint16_t *>(row + blk + 2) = 0;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (blk + i >= p.nb || (i && !two)) continue;
+      row[blk + i] = uint8_t(word >> (8 * i));
+      if (blk + i == p.nb - 1)
+        for (int32_t j = p.nb; j < p.ns; ++j) row[j] = 0;
+    }
+  }
 }
 
 // JVP: tangent rows beside the primal's. AMN, BMN: the operand is MN-major. EPI:
@@ -339,7 +351,7 @@ __global__ void __launch_bounds__((Lay<JVP, TN>::THREADS), 1) linear_sm100_kerne
           if (lane == 0) pair::arrive_remote_relaxed(acc_empty_leader + 8 * buf);
         }
         const int32_t cs = n0 + 32 * c;
-        if (!rows_in || cs >= p.N) continue;
+        if (!rows_in || cs >= p.N || 64 * cols + 32 * c >= TN) continue;
         if (p.splits > 1) {  // fp32 parts, 16 columns at a time
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
@@ -450,7 +462,7 @@ __global__ void __launch_bounds__((Lay<JVP, TN>::THREADS), 1) linear_sm100_kerne
         fence_async_smem_then_store(om, sbuf, cs, row0, lane);
       }
       if (EPI && ok && p.codes && p.splits == 1 && op == 0 && rows_in && row0 + lane < p.M && n0 < 32 * p.nb)
-        store_scales(p.scales + size_t(row0 + lane) * p.ns + n0 / 32, scale_word, n0 / 32, p);
+        store_scales<TN>(p.scales + size_t(row0 + lane) * p.ns, scale_word, n0 / 32, 64 * cols + 32 < TN, p);
     }
     if (lane == 0) pair::store_wait<0>();
     __syncwarp();
@@ -820,8 +832,11 @@ cudaError_t launch_tiles(const LinearParams &p, cudaStream_t stream) {
 
 template <bool JVP, bool AMN, bool BMN, bool EPI>
 cudaError_t launch_tiles(const LinearParams &p, cudaStream_t stream) {
-  return p.tile_cols == 128 ? launch_tiles<JVP, AMN, BMN, EPI, 128>(p, stream)
-                            : launch_tiles<JVP, AMN, BMN, EPI, 256>(p, stream);
+  if (p.tile_cols == 128) return launch_tiles<JVP, AMN, BMN, EPI, 128>(p, stream);
+  if constexpr (!BMN) {  // 80 columns a CTA are not whole 64-column blocks of an MN-major operand
+    if (p.tile_cols == 160) return launch_tiles<JVP, AMN, BMN, EPI, 160>(p, stream);
+  }
+  return launch_tiles<JVP, AMN, BMN, EPI, 256>(p, stream);
 }
 
 template <int NT>

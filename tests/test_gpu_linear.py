@@ -303,3 +303,10 @@ def test_outputs_past_32_bits():
     rel = float((dx[-tail:].float() - want[0].float()).norm() / want[0].float().norm())
     assert rel <= 2.0 ** -8  # the contraction may be split differently: one rounding apart
     caj.device_status()
+
+
+@pytest.mark.parametrize("M,K,C", [(1560, 192, 1536), (1000, 256, 1480), (1560, 64, 1448)])
+@pytest.mark.parametrize("tangent", [False, True])
+def test_sizes_of_every_tile_width(M, K, C, tangent):
+    """A frame's worth of rows, where the width of the tiles is chosen by their number."""
+    run_fwd(M, K, C, "gelu_tanh", True, True, tangent, True, seed=9)
