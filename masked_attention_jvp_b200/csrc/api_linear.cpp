@@ -89,6 +89,7 @@ caj_status check_shape(const caj_linear_act_shape *s) {
   if (s->M > (int64_t(1) << 30) || s->K > (1 << 24) || s->C > (1 << 24)) return CAJ_ERR_UNSUPPORTED;
   const int64_t limit = (int64_t(1) << 31) - 1;
   if (ceil_div(s->M, 128) * ceil_div(std::max(s->K, s->C), 128) > limit / 32) return CAJ_ERR_UNSUPPORTED;
+  if (ceil_div(s->K, 128) * ceil_div(s->C, 128) > limit / 32) return CAJ_ERR_UNSUPPORTED;
   if (s->M > limit / ceil_div(std::max(s->K, s->C), 32)) return CAJ_ERR_UNSUPPORTED;  // checkpoint blocks
   return CAJ_OK;
 }

@@ -215,6 +215,7 @@ struct Turn {
 // fewer heads are zero there.
 template <int M>
 __device__ __forceinline__ void group_sums(float (&v)[M], const Lane &l, const QkRopeParams &p, float *red) {
+  static_assert(M == 2 || M == 4, "");
   for (int o = p.D / 16; o > 0; o >>= 1) {
 #pragma unroll
     for (int i = 0; i < M; ++i) v[i] += __shfl_xor_sync(0xFFFFFFFFu, v[i], o);
@@ -230,9 +231,15 @@ __device__ __forceinline__ void group_sums(float (&v)[M], const Lane &l, const Q
   if (l.t >= l.T) return;
 #pragma unroll
   for (int i = 0; i < M; ++i) v[i] = 0.f;
+#pragma unroll 4
   for (int h = 0; h < heads; ++h) {
-#pragma unroll
-    for (int i = 0; i < M; ++i) v[i] += red[(l.t * heads + h) * M + i];
+    if constexpr (M == 4) {
+      const float4 r = reinterpret_cast<const float4 *>(red)[l.t * heads + h];
+      v[0] += r.x; v[1] += r.y; v[2] += r.z; v[3] += r.w;
+    } else {
+      const float2 r = reinterpret_cast<const float2 *>(red)[l.t * heads + h];
+      v[0] += r.x; v[1] += r.y;
+    }
   }
 }
 
@@ -249,7 +256,7 @@ __host__ __device__ constexpr int fwd_tokens() {
 // MAXT: 256 threads leave 80 registers each, 1024 (tokens wider than 2048 channels) 64.
 template <typename T, bool TAN, bool HALF, int MAXT>
 __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 3 : 1) qk_rope_fwd_kernel(const QkRopeParams p) {
-  extern __shared__ float red[];
+  extern __shared__ __align__(16) float red[];
   begin_after_previous();
   constexpr int U = fwd_tokens<T, TAN>();
   const Lane l = lane_of(p);
@@ -426,9 +433,10 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) qk_rope_bwd_kernel(
   auto advance = [&](Walk &w) {
     w.tok += l.T;
     w.n += l.T;
-    while (w.n >= p.N) {
-      w.n -= p.N;
-      ++w.b;
+    if (w.n >= p.N) {
+      const int32_t sequences = w.n / p.N;
+      w.b += sequences;
+      w.n -= sequences * p.N;
     }
   };
   auto head_row = [&](const Walk &w, int i) {  // element of (b, head, n, d0)

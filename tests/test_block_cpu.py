@@ -256,7 +256,7 @@ def _lbwd(ptrs=None, ws_bytes=1 << 40, **kw):
 _LIN_SHAPES = [(dict(M=0), INVALID), (dict(M=-5), INVALID), (dict(K=0), INVALID), (dict(C=0), INVALID),
                (dict(act=4), INVALID), (dict(act=-1), INVALID), (dict(K=60), UNSUPPORTED), (dict(C=129), UNSUPPORTED),
                (dict(M=1 << 31), UNSUPPORTED), (dict(K=1 << 25), UNSUPPORTED),
-               (dict(M=1 << 30, C=1 << 20), UNSUPPORTED)]
+               (dict(M=1 << 30, C=1 << 20), UNSUPPORTED), (dict(K=1 << 24, C=1 << 24), UNSUPPORTED)]
 
 
 @pytest.mark.parametrize("kw,want", _LIN_SHAPES)
