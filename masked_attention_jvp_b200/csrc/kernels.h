@@ -184,7 +184,7 @@ struct QkRopeParams {
   int32_t B, N, Hq, Hk, D, P;
   float eps;
   int32_t norm, half, gain_full, blocks;
-  int32_t ring;                // backward: tokens in a thread's ring of copies (set by the launch)
+  int32_t ring, angle_slots;   // backward: tokens in a thread's ring of copies, slots for angles (set by the launch)
 };
 
 // Matrix products of the linear operators; the operands' maps have 128-byte-swizzled

@@ -378,26 +378,33 @@ __device__ __forceinline__ v8::Raw<T> lds_vec(uint32_t a, uint32_t stride) {
 
 constexpr int kRing = 3;  // tokens in a thread's ring: one worked on, two on their way (fewer if wide)
 constexpr size_t kMaxSmem = 232448;
-// 16-byte slots of a token: dq, dk and xq, xk (fp32: two each; a checkpoint: eight codes
-// and the word with the scale byte in one slot), and the angles. dv needs none of them
-// and goes through registers.
-template <typename T, bool CK, bool HALF>
+// 16-byte slots a thread has for a token: dq, dk and xq, xk (fp32: two each; a checkpoint:
+// eight codes and the word with the scale byte in one slot), then the angles. dv needs none
+// of them and goes through registers.
+template <typename T, bool CK>
 constexpr int bwd_slots() {
-  return 2 * int(sizeof(T) / 2) + (CK ? 2 : 2 * int(sizeof(T) / 2)) + Turn<HALF, true>::kSlots;
+  return 2 * int(sizeof(T) / 2) + (CK ? 2 : 2 * int(sizeof(T) / 2));
 }
+// Slots for the angles. In the half layout, where a warp's lanes all work on one token
+// (SHARED), they copy its row of the tables once, a piece or two each, and read each
+// other's; otherwise every lane copies its own two or four pieces. (65520 tokens of 12 x 128,
+// own copies against shared: half layout 440 and 346 us; interleaved, which has half as many,
+// 320 and 332, so it keeps its own.)
+int32_t bwd_angle_slots(const QkRopeParams &p, bool shared) { return shared ? (p.P / 2 + 31) / 32 : p.half ? 4 : 2; }
 
 // Each of p.blocks blocks walks over a run of neighbouring tokens, T at a time, so the
 // gains' gradient stays in registers for the whole run and addresses only step on; block
 // i leaves its partial dg in p.partial[q or k][i]. What a token needs comes through a
 // ring of asynchronous copies, up to two tokens ahead: with plain loads the kernel waited
 // for memory half of its time. CK: xq and xk are 8-bit checkpoints.
-template <typename T, bool CK, bool HALF, int MAXT>
+template <typename T, bool CK, bool HALF, bool SHARED, int MAXT>
 __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) qk_rope_bwd_kernel(const QkRopeParams p) {
   extern __shared__ __align__(16) uint8_t smem[];
   begin_after_previous();
   using Rot = Turn<HALF, true>;
   constexpr int kVec = int(sizeof(T) / 2);  // slots of a vector of T
-  constexpr int kSlots = bwd_slots<T, CK, HALF>(), kAngles = kSlots - Rot::kSlots;
+  constexpr int kAngles = bwd_slots<T, CK>();  // the angles' first slot
+  const int kSlots = kAngles + (SHARED ? p.angle_slots : Rot::kSlots);
   float *red = reinterpret_cast<float *>(smem + size_t(p.ring) * kSlots * 16 * blockDim.x);
   const Lane l = lane_of(p);
   const int32_t rows = p.B * p.N, stride = 16 * int32_t(blockDim.x);
@@ -444,7 +451,13 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) qk_rope_bwd_kernel(
   };
   auto fetch = [&](const Walk &w, uint32_t slot0) {
     if (w.tok < end) {
-      if (turns && l.t < l.T) {
+      if (SHARED) {  // pieces 0 .. P/4 of the cosines' row, then of the sines'
+        for (int32_t i = 0, piece = int32_t(threadIdx.x & 31); i < p.angle_slots; ++i, piece += 32) {
+          if (piece >= p.P / 2) continue;
+          const float *row = piece < p.P / 4 ? p.cos : p.sin;
+          copy16(slot0 + (kAngles + i) * stride, row + int64_t(w.n) * p.P + 4 * (piece < p.P / 4 ? piece : piece - p.P / 4));
+        }
+      } else if (turns && l.t < l.T) {
         const int64_t at = int64_t(w.n) * p.P + Rot::offset(p, l);
 #pragma unroll
         for (int i = 0; i < Rot::kSlots / 2; ++i) {
@@ -479,6 +492,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) qk_rope_bwd_kernel(
                             1.f / float(p.norm == kNormHead ? p.D : heads[1] * p.D)};
   int at = 0, to = p.ring - 1;  // ring positions
   for (int32_t round = 0; round < rounds; ++round) {
+    if (SHARED) __syncwarp();  // every lane has read what the next copies replace
     fetch(next, mine + to * kSlots * stride);
     advance(next);
     const uint32_t slot0 = mine + at * kSlots * stride;
@@ -496,10 +510,16 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) qk_rope_bwd_kernel(
     // past the `on` conditions, and a head's lanes are all there or all not)
     Rot turn;
     turn.rest();
+    if (SHARED) __syncwarp();  // the other lanes' copies have landed too
     if (turns) {
 #pragma unroll
       for (int i = 0; i < Rot::kSlots; ++i) {
-        const uint4 w = lds16(slot0 + (kAngles + i) * stride);
+        uint32_t from = slot0 + (kAngles + i) * stride;
+        if (SHARED) {
+          const int32_t piece = Rot::offset(p, l) / 4 + i % (Rot::kSlots / 2) + (i < Rot::kSlots / 2 ? 0 : p.P / 4);
+          from = slot0 - 16 * (threadIdx.x & 31) + (kAngles + piece / 32) * stride + 16 * (piece % 32);
+        }
+        const uint4 w = lds16(from);
         turn.raw[i] = make_float4(__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w));
       }
     }
@@ -634,12 +654,13 @@ cudaError_t launch_fwd(const QkRopeParams &p, cudaStream_t stream) {
   return p.tx[0] ? launch_fwd<T, true, 1024>(p, stream) : launch_fwd<T, false, 1024>(p, stream);
 }
 
-template <typename T, bool CK, bool HALF, int MAXT>
+template <typename T, bool CK, bool HALF, bool SHARED, int MAXT>
 cudaError_t launch_bwd(const QkRopeParams &params, cudaStream_t stream) {
-  auto kernel = qk_rope_bwd_kernel<T, CK, HALF, MAXT>;
+  auto kernel = qk_rope_bwd_kernel<T, CK, HALF, SHARED, MAXT>;
   QkRopeParams p = params;
   const int32_t threads = threads_for(p);
-  const size_t token = size_t(bwd_slots<T, CK, HALF>()) * 16 * threads, extra = token_norm_bytes(p, 4);
+  p.angle_slots = bwd_angle_slots(p, SHARED);
+  const size_t token = size_t(bwd_slots<T, CK>() + p.angle_slots) * 16 * threads, extra = token_norm_bytes(p, 4);
   // the deepest ring with which the blocks that the grid counts on fit an SM (228 KB, 1 KB
   // of it reserved a block); one block a SM for wide tokens
   const size_t resident = size_t(qk_rope_resident(threads));
@@ -655,11 +676,15 @@ cudaError_t launch_bwd(const QkRopeParams &params, cudaStream_t stream) {
   const int32_t len = p.gain_full ? vectors(p) * 8 : p.D;
   return launch_in_order(gain_grad_kernel, dim3(unsigned((len + 31) / 32), 2), 256, 0, stream, p);
 }
+template <typename T, bool CK, int MAXT>
+cudaError_t launch_bwd(const QkRopeParams &p, cudaStream_t stream) {
+  if (!p.half) return launch_bwd<T, CK, false, false, MAXT>(p, stream);
+  return vectors(p) % 32 == 0 ? launch_bwd<T, CK, true, true, MAXT>(p, stream)
+                              : launch_bwd<T, CK, true, false, MAXT>(p, stream);
+}
 template <typename T, bool CK>
 cudaError_t launch_bwd(const QkRopeParams &p, cudaStream_t stream) {
-  if (threads_for(p) <= 256)
-    return p.half ? launch_bwd<T, CK, true, 256>(p, stream) : launch_bwd<T, CK, false, 256>(p, stream);
-  return p.half ? launch_bwd<T, CK, true, 1024>(p, stream) : launch_bwd<T, CK, false, 1024>(p, stream);
+  return threads_for(p) <= 256 ? launch_bwd<T, CK, 256>(p, stream) : launch_bwd<T, CK, 1024>(p, stream);
 }
 
 }  // namespace
