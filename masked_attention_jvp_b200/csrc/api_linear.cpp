@@ -19,66 +19,80 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 size_t padded(int64_t bytes) { return size_t((bytes + 255) & ~int64_t(255)); }
 
 struct Plan {
-  int32_t m_tiles, n_tiles, k_blocks, splits, split_blocks, tile_cols;
-  int64_t part_rows, part_bytes;
+  caj::LinearProblem prob;
+  int64_t part_bytes;
+  double us, work_us, unit_us;  // estimates: wave after wave; all units' work; one unit
 };
-// rows x cols outputs (and as many tangents), contraction of `depth`: the width of the
-// tiles and in how many parts the contraction runs, by the least estimate of
+// rows x cols outputs (and as many tangents), contraction of `depth`, in tiles of
+// `tile_cols` columns: in how many parts the contraction runs, by the least estimate of
 //   waves * (blocks of a part * block time + tile time) + parts written and read again.
 // 74 pairs of SMs work at a time; a 64-wide block of the contraction takes a pair 0.40 us
-// at 256 columns, 0.28 at 160 (forward only) and 0.23 at 128, a tile 1.0 to 1.5 us besides; parts cost 8 bytes an
-// output at about 5 TB/s and a launch (3 us). The figures only weigh one shape against
-// another. Measured on B200 (primal and tangent, 1560 tokens, 1536 x 1536): 78 tiles of
-// 256 columns 25.2 us where 156 of 128 took 21.1, then (another epilogue) 156 of 128
-// columns 18.8 us and 130 of 160 columns 16.2.
-Plan plan(int64_t rows, int64_t cols, int64_t depth, bool tangent, bool forward) {
+// at 256 columns, 0.28 at 160 and 0.23 at 128, a tile 1.0 to 1.5 us besides; parts cost 8
+// bytes an output at about 5 TB/s and a launch (3 us). The figures only weigh one shape
+// against another.
+Plan plan_tiles(int64_t rows, int64_t cols, int64_t depth, bool tangent, int32_t tile_cols) {
   Plan best{};
-  double best_us = 0;
   const int64_t tile_rows = tangent ? kTileRows / 2 : kTileRows, ops = tangent ? 2 : 1;
-  const int64_t m_tiles = ceil_div(rows, tile_rows), k_blocks = ceil_div(depth, kBlock);
+  const int64_t m_tiles = ceil_div(rows, tile_rows), n_tiles = ceil_div(cols, tile_cols), k_blocks = ceil_div(depth, kBlock);
+  const int64_t tiles = m_tiles * n_tiles;
+  const double block_us = tile_cols == 256 ? 0.40 : tile_cols == 160 ? 0.28 : 0.23;
+  const double tile_us = tile_cols == 256 ? 1.5 : tile_cols == 160 ? 1.2 : 1.0;
+  for (int32_t s = 1; s <= 32 && s <= k_blocks; ++s) {
+    const int64_t per = ceil_div(k_blocks, s);
+    if (ceil_div(k_blocks, per) != s) continue;  // a part would be empty
+    const double unit_us = block_us * double(per) + tile_us;
+    const double parts_us = s > 1 ? 3.0 + 8.0 * s * double(rows * cols * ops) / 5e6 : 0.0;
+    const double us = double(ceil_div(tiles * s, 74)) * unit_us + parts_us;
+    if (s > 1 && us >= best.us) continue;
+    best.us = us;
+    best.unit_us = unit_us;
+    best.work_us = double(tiles * s) / 74 * unit_us + parts_us;
+    best.prob = {int32_t(rows), int32_t(cols), int32_t(m_tiles), int32_t(n_tiles), int32_t(k_blocks), s, int32_t(per),
+                 m_tiles * tile_rows};
+    best.part_bytes = s > 1 ? int64_t(s) * ops * best.prob.part_rows * cols * 4 : 0;
+  }
+  return best;
+}
+// The forward's tiles: the width with the least estimate. Measured on B200 (primal and
+// tangent, 1560 tokens, 1536 x 1536): 78 tiles of 256 columns 25.2 us where 156 of 128 took
+// 21.1, then (another epilogue) 156 of 128 columns 18.8 us and 130 of 160 columns 16.2.
+struct FwdPlan : Plan {
+  int32_t tile_cols;
+};
+FwdPlan plan_fwd(int64_t M, int64_t C, int64_t K, bool tangent) {
+  FwdPlan best{};
   for (const int32_t tile_cols : {256, 160, 128}) {
-    if (tile_cols == 160 && !forward) continue;
-    const int64_t n_tiles = ceil_div(cols, tile_cols), tiles = m_tiles * n_tiles;
-    const double block_us = tile_cols == 256 ? 0.40 : tile_cols == 160 ? 0.28 : 0.23;
-    const double tile_us = tile_cols == 256 ? 1.5 : tile_cols == 160 ? 1.2 : 1.0;
-    for (int32_t s = 1; s <= 32 && s <= k_blocks; ++s) {
-      const int64_t per = ceil_div(k_blocks, s);
-      if (ceil_div(k_blocks, per) != s) continue;  // a part would be empty
-      const double us = double(ceil_div(tiles * s, 74)) * (block_us * double(per) + tile_us) +
-                        (s > 1 ? 3.0 + 8.0 * s * double(rows * cols * ops) / 5e6 : 0.0);
-      if (best.splits && us >= best_us) continue;
-      best_us = us;
-      best.m_tiles = int32_t(m_tiles);
-      best.n_tiles = int32_t(n_tiles);
-      best.k_blocks = int32_t(k_blocks);
-      best.splits = s;
-      best.split_blocks = int32_t(per);
-      best.tile_cols = tile_cols;
-      best.part_rows = m_tiles * tile_rows;
-      best.part_bytes = s > 1 ? int64_t(s) * ops * best.part_rows * cols * 4 : 0;
-    }
+    const Plan p = plan_tiles(M, C, K, tangent, tile_cols);
+    if (best.tile_cols && p.us >= best.us) continue;
+    static_cast<Plan &>(best) = p;
+    best.tile_cols = tile_cols;
+  }
+  return best;
+}
+// The gradients' tiles, dx and dW in one launch: their units together, and one unit's time
+// of imbalance at the end. Planned for both even where one is wanted, so that a gradient
+// does not depend, in its last bits, on whether the other was asked for.
+struct GradPlan {
+  Plan dx, dw;
+  int32_t tile_cols;
+};
+GradPlan plan_grads(int64_t M, int64_t C, int64_t K) {
+  GradPlan best{};
+  double best_us = 0;
+  for (const int32_t tile_cols : {256, 128}) {
+    const GradPlan p{plan_tiles(M, K, C, false, tile_cols), plan_tiles(C, K, M, false, tile_cols), tile_cols};
+    const double us = p.dx.work_us + p.dw.work_us + std::max(p.dx.unit_us, p.dw.unit_us);
+    if (best.tile_cols && us >= best_us) continue;
+    best = p;
+    best_us = us;
   }
   return best;
 }
 bool few_rows(int64_t M, bool tangent) { return (tangent ? 2 : 1) * M <= caj::kLinearFewRows; }
 
-bool use_plan(caj::LinearParams *p, const Plan &pl, int64_t rows, int64_t cols, int64_t depth, bool tangent,
-              void *workspace) {
-  p->M = int32_t(rows);
-  p->N = int32_t(cols);
-  p->K = int32_t(depth);
-  p->m_tiles = pl.m_tiles;
-  p->n_tiles = pl.n_tiles;
-  p->k_blocks = pl.k_blocks;
-  p->splits = pl.splits;
-  p->split_blocks = pl.split_blocks;
-  p->tile_cols = pl.tile_cols;
-  p->part_rows = pl.part_rows;
-  p->part = static_cast<float *>(workspace);
-  p->timeout_ns = caj::wait_timeout_ns();
-  p->fault_mode = caj::fault_mode();
-  return pl.splits == 1 || caj::encode_out_2d(&p->tm_part, workspace, int64_t(pl.splits) * (tangent ? 2 : 1) * pl.part_rows, cols,
-                                              true);
+bool part_map(CUtensorMap *map, const Plan &pl, bool tangent, void *parts) {
+  return pl.prob.splits <= 1 || caj::encode_out_2d(map, parts, int64_t(pl.prob.splits) * (tangent ? 2 : 1) * pl.prob.part_rows,
+                                                   pl.prob.N, true);
 }
 
 caj_status check_shape(const caj_linear_act_shape *s) {
@@ -98,20 +112,22 @@ bool good_rows(const void *p, int64_t ld, int64_t width) {
 }
 
 struct BwdSizes {
-  Plan dx, dw;
+  GradPlan grads;
   int32_t chunk_rows;
-  size_t x, dz, sums, parts, total;
+  size_t x, dz, sums, dx_parts, dw_parts, total;
 };
 BwdSizes bwd_sizes(const caj_linear_act_shape *s, bool x_ckpt, bool want_dx, bool want_dw, bool want_db) {
   BwdSizes b{};
-  b.dx = plan(s->M, s->K, s->C, false, false);
-  b.dw = plan(s->C, s->K, s->M, false, false);
+  b.grads = plan_grads(s->M, s->C, s->K);
+  if (!want_dx) b.grads.dx = Plan{};
+  if (!want_dw) b.grads.dw = Plan{};
   b.chunk_rows = caj::linear_dz_chunk_rows(s->M, s->C);
   if (x_ckpt && want_dw) b.x = padded(s->M * s->K * 2);
   if (s->act != CAJ_ACT_NONE) b.dz = padded(s->M * s->C * 2);
   if (want_db) b.sums = padded(ceil_div(s->M, b.chunk_rows) * s->C * 4);
-  b.parts = padded(std::max(want_dx ? b.dx.part_bytes : 0, want_dw ? b.dw.part_bytes : 0));
-  b.total = b.x + b.dz + b.sums + b.parts;
+  b.dx_parts = padded(b.grads.dx.part_bytes);
+  b.dw_parts = padded(b.grads.dw.part_bytes);
+  b.total = b.x + b.dz + b.sums + b.dx_parts + b.dw_parts;
   return b;
 }
 
@@ -123,7 +139,7 @@ caj_status caj_linear_act_fwd_workspace(const caj_linear_act_shape *shape, int32
   if (!bytes || (tangent != 0 && tangent != 1)) return CAJ_ERR_INVALID_ARG;
   const caj_status st = check_shape(shape);
   if (st != CAJ_OK) return st;
-  *bytes = few_rows(shape->M, tangent) ? 0 : size_t(plan(shape->M, shape->C, shape->K, tangent, true).part_bytes);
+  *bytes = few_rows(shape->M, tangent) ? 0 : size_t(plan_fwd(shape->M, shape->C, shape->K, tangent).part_bytes);
   return CAJ_OK;
 }
 
@@ -144,7 +160,7 @@ caj_status caj_linear_act_fwd(const void *x, const void *tx, const void *w, cons
   if (!pre_codes != !pre_scales) return CAJ_ERR_INVALID_ARG;
   if (pre_codes && (!aligned_to(pre_codes, 16) || !aligned_to(pre_scales, 4))) return CAJ_ERR_INVALID_ARG;
   const bool few = few_rows(M, tan);
-  const Plan pl = plan(M, C, K, tan, true);
+  const FwdPlan pl = plan_fwd(M, C, K, tan);
   if (!few && pl.part_bytes && (!workspace || !aligned_to(workspace, 16) || workspace_bytes < size_t(pl.part_bytes)))
     return CAJ_ERR_INVALID_ARG;
   st = caj::check_device();
@@ -167,13 +183,15 @@ caj_status caj_linear_act_fwd(const void *x, const void *tx, const void *w, cons
   p.nb = caj::ck::blocks_of(shape->C);
   p.ns = caj::ck::scale_bytes(shape->C);
   p.act = shape->act;
+  p.prob[0] = pl.prob;
+  p.K = shape->K;
   bool ok = true;
-  if (few) {
-    p.M = int32_t(M);
-    p.N = shape->C;
-    p.K = shape->K;
-  } else {
-    ok = use_plan(&p, pl, M, C, K, tan, workspace) &&
+  if (!few) {
+    p.tile_cols = pl.tile_cols;
+    p.part = static_cast<float *>(workspace);
+    p.timeout_ns = caj::wait_timeout_ns();
+    p.fault_mode = caj::fault_mode();
+    ok = part_map(&p.tm_part, pl, tan, workspace) &&
          caj::encode_map_2d_ld(&p.tm_a, x, M, K, shape->ldx, tan ? 64 : 128) &&
          caj::encode_map_2d_ld(&p.tm_b, w, C, K, K, pl.tile_cols / 2) && caj::encode_out_2d(&p.tm_y, y, M, C, false);
     if (ok && tan)
@@ -219,7 +237,7 @@ caj_status caj_linear_act_bwd(const void *dy, const void *x, const uint8_t *x_sc
   void *x_values = at;
   void *dz = at + b.x;
   float *sums = reinterpret_cast<float *>(at + b.x + b.dz);
-  void *parts = at + b.x + b.dz + b.sums;
+  char *parts = at + b.x + b.dz + b.sums;
 
   int64_t ld_dz = C;
   if (!act) {
@@ -243,40 +261,42 @@ caj_status caj_linear_act_bwd(const void *dy, const void *x, const uint8_t *x_sc
     st = done(caj::launch_linear_dz(d, db, s));
     if (st != CAJ_OK) return st;
   }
-  if (dx) {
-    caj::LinearParams p{};
-    p.y = dx;
-    if (!use_plan(&p, b.dx, M, K, C, false, parts) || !caj::encode_map_2d_ld(&p.tm_a, dz, M, C, ld_dz, 128) ||
-        !caj::encode_map_2d_ld(&p.tm_b, w, C, K, K, 64) || !caj::encode_out_2d(&p.tm_y, dx, M, K, false))
-      return caj::cuda_fail(cudaErrorInvalidValue);
-    st = done(caj::launch_linear_dx(p, s));
+  if (!dx && !dw) return CAJ_OK;
+  int64_t ld_x = shape->ldx;
+  if (dw && x_scales) {
+    caj::Ckpt8Params c{};
+    c.codes = static_cast<int8_t *>(const_cast<void *>(x));
+    c.scales = const_cast<uint8_t *>(x_scales);
+    c.out = x_values;
+    c.ld = ld_x = K;
+    c.cols = shape->K;
+    c.nb = caj::ck::blocks_of(shape->K);
+    c.ns = caj::ck::scale_bytes(shape->K);
+    c.total = uint32_t(M * c.nb);
+    c.rows = uint32_t(M);
+    st = done(caj::launch_ckpt8(c, true, true, s));
     if (st != CAJ_OK) return st;
+    x = x_values;
   }
-  if (dw) {
-    int64_t ld_x = shape->ldx;
-    if (x_scales) {
-      caj::Ckpt8Params c{};
-      c.codes = static_cast<int8_t *>(const_cast<void *>(x));
-      c.scales = const_cast<uint8_t *>(x_scales);
-      c.out = x_values;
-      c.ld = ld_x = K;
-      c.cols = shape->K;
-      c.nb = caj::ck::blocks_of(shape->K);
-      c.ns = caj::ck::scale_bytes(shape->K);
-      c.total = uint32_t(M * c.nb);
-      c.rows = uint32_t(M);
-      st = done(caj::launch_ckpt8(c, true, true, s));
-      if (st != CAJ_OK) return st;
-      x = x_values;
-    }
-    caj::LinearParams p{};
-    p.y = dw;
-    if (!use_plan(&p, b.dw, C, K, M, false, parts) || !caj::encode_map_2d_ld(&p.tm_a, dz, M, C, ld_dz, 64) ||
-        !caj::encode_map_2d_ld(&p.tm_b, x, M, K, ld_x, 64) || !caj::encode_out_2d(&p.tm_y, dw, C, K, false))
-      return caj::cuda_fail(cudaErrorInvalidValue);
-    st = done(caj::launch_linear_dw(p, s));
-  }
-  return st;
+  caj::LinearParams p{};
+  p.prob[0] = b.grads.dx.prob;
+  p.prob[1] = b.grads.dw.prob;
+  p.tile_cols = b.grads.tile_cols;
+  p.y = dx;
+  p.ty = dw;
+  p.part = reinterpret_cast<float *>(parts);
+  p.part2 = reinterpret_cast<float *>(parts + b.dx_parts);
+  p.timeout_ns = caj::wait_timeout_ns();
+  p.fault_mode = caj::fault_mode();
+  bool ok = caj::encode_map_2d_ld(&p.tm_a, dz, M, C, ld_dz, 64);
+  if (dx)
+    ok = ok && caj::encode_map_2d_ld(&p.tm_b, w, C, K, K, 64) && caj::encode_out_2d(&p.tm_y, dx, M, K, false) &&
+         part_map(&p.tm_part, b.grads.dx, false, p.part);
+  if (dw)
+    ok = ok && caj::encode_map_2d_ld(&p.tm_b2, x, M, K, ld_x, 64) && caj::encode_out_2d(&p.tm_y2, dw, C, K, false) &&
+         part_map(&p.tm_part2, b.grads.dw, false, p.part2);
+  if (!ok) return caj::cuda_fail(cudaErrorInvalidValue);
+  return done(caj::launch_linear_grads(p, s));
 }
 
 }  // extern "C"

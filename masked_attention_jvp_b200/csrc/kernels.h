@@ -191,23 +191,29 @@ struct QkRopeParams {
 // boxes of 64 bf16 columns (K-major A: 128 rows, 64 with tangents; K-major B: half a
 // tile's columns; MN-major: 64).
 constexpr int32_t kLinearFewRows = 32;  // rows (tangents counted) up to which W is streamed
+struct LinearProblem {
+  int32_t M, N;                                   // output rows and columns
+  int32_t m_tiles, n_tiles, k_blocks;             // 0 tiles: not wanted
+  int32_t splits, split_blocks;                   // parts of the contraction, blocks of a part
+  int64_t part_rows;                              // rows of a part's buffer
+};
 struct LinearParams {
-  CUtensorMap tm_a, tm_a2, tm_b;  // x (or dz), tx, W (or x)
-  CUtensorMap tm_y, tm_y2;        // outputs, 64-byte-swizzled boxes of 32 columns x 32 rows
-  CUtensorMap tm_part;            // splits > 1: fp32 parts, boxes of 16 x 32
-  const void *x, *tx, *w;         // few rows: x, tx, W themselves; tx also says whether there are tangents
-  const void *bias, *res, *tres;  // bf16 or null
-  void *y, *ty;                   // [M, N] bf16
-  float *part;                    // [splits][1 or 2][part_rows][N]
-  int8_t *codes;                  // z's 8-bit checkpoint, or null
+  CUtensorMap tm_a, tm_a2, tm_b;   // forward: x, tx, W; gradients: dz (64 x 64 boxes), -, W
+  CUtensorMap tm_b2;               // gradients: x
+  CUtensorMap tm_y, tm_y2;         // y, ty or dx, dW; 64-byte-swizzled boxes of 32 columns x 32 rows
+  CUtensorMap tm_part, tm_part2;   // splits > 1: fp32 parts (of dW: the second), boxes of 16 x 32
+  LinearProblem prob[2];           // the forward (or dx), and dW
+  const void *x, *tx, *w;          // few rows: x, tx, W themselves; tx also says whether there are tangents
+  const void *bias, *res, *tres;   // bf16 or null
+  void *y, *ty;                    // [M, N] bf16; gradients: dx, dW
+  float *part, *part2;             // [splits][1 or 2][part_rows][N]
+  int8_t *codes;                   // z's 8-bit checkpoint, or null
   uint8_t *scales;
   int64_t ld_x, ld_tx, ld_res, ld_tres;
-  int64_t part_rows;
-  int32_t M, N, K;                // output rows and columns, contraction
-  int32_t m_tiles, n_tiles, k_blocks, splits, split_blocks, tile_cols;
+  int32_t K, tile_cols;
   int32_t nb, ns;
   int32_t act;
-  int32_t fault_mode;             // test hook: 1 = the producer issues no copies
+  int32_t fault_mode;              // test hook: 1 = the producer issues no copies
   uint64_t timeout_ns;
 };
 struct LinearDzParams {
@@ -267,8 +273,7 @@ cudaError_t launch_qk_rope_fwd(const QkRopeParams &p, bool bf16, cudaStream_t st
 cudaError_t launch_qk_rope_bwd(const QkRopeParams &p, bool bf16, cudaStream_t stream);
 int32_t qk_rope_bwd_blocks(int32_t B, int32_t N, int32_t Hq, int32_t Hk, int32_t D);
 cudaError_t launch_linear_fwd(const LinearParams &p, cudaStream_t stream);
-cudaError_t launch_linear_dx(const LinearParams &p, cudaStream_t stream);
-cudaError_t launch_linear_dw(const LinearParams &p, cudaStream_t stream);
+cudaError_t launch_linear_grads(const LinearParams &p, cudaStream_t stream);
 cudaError_t launch_linear_dz(const LinearDzParams &p, float *db, cudaStream_t stream);
 int32_t linear_dz_chunk_rows(int64_t M, int32_t C);
 cudaError_t read_and_clear_linear_error(uint32_t *out);

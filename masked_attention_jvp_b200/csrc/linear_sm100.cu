@@ -2,11 +2,13 @@
 //   forward    z = x W^T + b,  y = act(z) + res,  ty = act'(z) * (tx W^T) + tres,
 //              optionally z kept as an 8-bit checkpoint
 //   gradients  dx = dz W,  dW = dz^T x
-// All are one persistent kernel over 256 x 256 output tiles, instantiated by where
-// the contraction runs in each operand:
+// All are one persistent kernel over 256 x 256 output tiles. Where the contraction runs
+// in each operand:
 //   forward  x [M, K], W [C, K]: both along the rows (K-major)
 //   dx       dz [M, C] along the rows, W [C, K] across them (MN-major B)
 //   dW       dz [M, C] and x [M, K], contraction over the tokens: both MN-major
+// One launch computes dx and dW: a second one's start and end (about 5 us) are saved, and
+// the tiles of one fill the pairs that the other's last wave leaves idle.
 //
 // Design (clusters of two CTAs, one CTA per SM, 18 warps per CTA, 10 for narrow tiles):
 //   A pair computes 256 x 256 tiles with tcgen05 cta_group::2 (M = 256, N = 256):
@@ -145,13 +147,15 @@ __device__ __forceinline__ void store_scales(uint8_t *row, uint32_t word, int32_
   }
 }
 
-// JVP: tangent rows beside the primal's. AMN, BMN: the operand is MN-major. EPI:
-// bias, activation, residual and checkpoint (otherwise the plain product).
-template <bool JVP, bool AMN, bool BMN, bool EPI, int TN>
+// JVP: tangent rows beside the primal's. GRADS: the plain products dW and dx, either or both
+// (otherwise the forward with its epilogue); the tiles of dW, which have the longer
+// contractions in large problems, go first.
+template <bool JVP, bool GRADS, int TN>
 __global__ void __launch_bounds__((Lay<JVP, TN>::THREADS), 1) linear_sm100_kernel(const __grid_constant__ LinearParams p) {
   using L = Lay<JVP, TN>;
   constexpr uint32_t STAGE_BYTES = L::STAGE_BYTES, B_BYTES = L::B_BYTES;
   constexpr int TM = JVP ? 128 : 256;  // tokens (or output rows) of a tile
+  constexpr bool EPI = !GRADS;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t sbase = (raw + 1023u) & ~1023u;
@@ -162,7 +166,25 @@ __global__ void __launch_bounds__((Lay<JVP, TN>::THREADS), 1) linear_sm100_kerne
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = pair::cluster_rank();
   const int32_t first = int32_t(pair::cluster_id()), step = int32_t(pair::clusters());
-  const int32_t n_tiles = p.m_tiles * p.n_tiles, n_units = n_tiles * p.splits;
+  // units of work: a tile of an output and a part of its contraction
+  const int32_t units_dw = GRADS ? p.prob[1].m_tiles * p.prob[1].n_tiles * p.prob[1].splits : 0;
+  const int32_t n_units = units_dw + p.prob[0].m_tiles * p.prob[0].n_tiles * p.prob[0].splits;
+  struct Unit {
+    int32_t dw, m, n, split, kb0, kb1;  // which product; tile row and column; blocks of the contraction
+  };
+  auto unit_of = [&](int32_t u) {
+    Unit w;
+    w.dw = GRADS && u < units_dw;
+    if (GRADS && !w.dw) u -= units_dw;
+    const LinearProblem &q = p.prob[w.dw];
+    const int32_t tiles = q.m_tiles * q.n_tiles, t = u % tiles;
+    w.split = u / tiles;
+    w.m = t / q.n_tiles;
+    w.n = t - w.m * q.n_tiles;
+    w.kb0 = w.split * q.split_blocks;
+    w.kb1 = min(q.k_blocks, w.kb0 + q.split_blocks);
+    return w;
+  };
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < L::STAGES; ++s) {
@@ -184,8 +206,8 @@ __global__ void __launch_bounds__((Lay<JVP, TN>::THREADS), 1) linear_sm100_kerne
   if (warp == 0 && lane == 0) {
     prefetch_tmap(&p.tm_a);
     if (JVP) prefetch_tmap(&p.tm_a2);
-    prefetch_tmap(&p.tm_b);
-    prefetch_tmap(&p.tm_y);
+    if (!GRADS) prefetch_tmap(&p.tm_b);
+    if (!GRADS) prefetch_tmap(&p.tm_y);
     if (JVP) prefetch_tmap(&p.tm_y2);
   }
   if (warp == 1) pair::tmem_alloc(smem_u32(tmem_slot), L::TMEM_COLS);
@@ -204,11 +226,10 @@ __global__ void __launch_bounds__((Lay<JVP, TN>::THREADS), 1) linear_sm100_kerne
     uint32_t stage = 0, phase = 0, issued = 0;
     bool ok = true;
     for (int32_t u = first; ok && u < n_units; u += step) {
-      const int32_t t = u % n_tiles, split = u / n_tiles;
-      const int32_t m0 = (t / p.n_tiles) * TM + int32_t(rank) * (TM / 2);
-      const int32_t n0 = (t % p.n_tiles) * TN + int32_t(rank) * (TN / 2);
-      const int32_t kb1 = min(p.k_blocks, (split + 1) * p.split_blocks);
-      for (int32_t kb = split * p.split_blocks; kb < kb1; ++kb) {
+      const Unit w = unit_of(u);
+      const int32_t m0 = w.m * TM + int32_t(rank) * (TM / 2), n0 = w.n * TN + int32_t(rank) * (TN / 2);
+      const CUtensorMap *bm = GRADS && w.dw ? &p.tm_b2 : &p.tm_b;
+      for (int32_t kb = w.kb0; kb < w.kb1; ++kb) {
         if (!wait(bars + L::EMPTY + 8 * stage, phase ^ 1u, kSiteEmpty)) {
           ok = false;
           break;
@@ -217,20 +238,15 @@ __global__ void __launch_bounds__((Lay<JVP, TN>::THREADS), 1) linear_sm100_kerne
           const uint32_t sa = sbase + stage * STAGE_BYTES, sb = sa + A_BYTES;
           const uint32_t fb = pair::at_rank(bars + L::FULL + 8 * stage, 0);  // the leader's barrier
           if (rank == 0) mbar_arrive_expect_tx_if(leader, bars + L::FULL + 8 * stage, 2 * STAGE_BYTES);
-          if (AMN) {
-            pair::load_2d(leader, sa, &p.tm_a, fb, m0, kb * TK);
-            pair::load_2d(leader, sa + A_BYTES / 2, &p.tm_a, fb, m0 + 64, kb * TK);
-          } else if (JVP) {
-            pair::load_2d(leader, sa, &p.tm_a, fb, kb * TK, m0);
-            pair::load_2d(leader, sa + A_BYTES / 2, &p.tm_a2, fb, kb * TK, m0);
+          if (GRADS) {  // 64 x 64 boxes of dz: two of rows for dx, two of columns for dW
+            pair::load_2d(leader, sa, &p.tm_a, fb, w.dw ? m0 : kb * TK, w.dw ? kb * TK : m0);
+            pair::load_2d(leader, sa + A_BYTES / 2, &p.tm_a, fb, w.dw ? m0 + 64 : kb * TK, w.dw ? kb * TK : m0 + 64);
+            pair::load_2d(leader, sb, bm, fb, n0, kb * TK);
+            if (TN == 256) pair::load_2d(leader, sb + B_BYTES / 2, bm, fb, n0 + 64, kb * TK);
           } else {
             pair::load_2d(leader, sa, &p.tm_a, fb, kb * TK, m0);
-          }
-          if (BMN) {
-            pair::load_2d(leader, sb, &p.tm_b, fb, n0, kb * TK);
-            if (TN == 256) pair::load_2d(leader, sb + B_BYTES / 2, &p.tm_b, fb, n0 + 64, kb * TK);
-          } else {
-            pair::load_2d(leader, sb, &p.tm_b, fb, kb * TK, n0);
+            if (JVP) pair::load_2d(leader, sa + A_BYTES / 2, &p.tm_a2, fb, kb * TK, m0);
+            pair::load_2d(leader, sb, bm, fb, kb * TK, n0);
           }
           ++issued;
         }
@@ -257,11 +273,12 @@ __global__ void __launch_bounds__((Lay<JVP, TN>::THREADS), 1) linear_sm100_kerne
     if (rank == 0) {
       // ---------------------------------------------------- MMA issuer (leader only)
       const uint32_t leader = elect_one();
-      constexpr uint32_t IDESC = idesc_bf16_f32(256, TN, BMN ? 1 : 0) | (AMN ? 1u << 15 : 0u);
-      // per 16-wide step of the contraction: 32 bytes along a K-major row, 16 rows of
-      // 128 bytes of an MN-major block
-      constexpr uint64_t A_STEP = AMN ? 128 : 2, B_STEP = BMN ? 128 : 2;
-      constexpr uint32_t A_LBO = AMN ? A_BYTES / 2 : 16, B_LBO = BMN ? 64 * TK * 2 : 16;
+      // The contraction runs along the rows of x, W and, for dx, dz (K-major); across those
+      // of W for dx and of dz and x for dW (MN-major). Per 16-wide step of it: 32 bytes along
+      // a K-major row, 16 rows of 128 bytes of an MN-major block.
+      constexpr uint32_t kAcross = 64 * TK * 2;  // from one 64-wide block to the next
+      constexpr uint64_t B_STEP = GRADS ? 128 : 2;
+      constexpr uint32_t B_LBO = GRADS ? kAcross : 16;
       uint32_t stage = 0, phase = 0, count = 0;
       bool ok = true;
       for (int32_t u = first; ok && u < n_units; u += step, ++count) {
@@ -269,19 +286,21 @@ __global__ void __launch_bounds__((Lay<JVP, TN>::THREADS), 1) linear_sm100_kerne
         if (!wait(bars + L::ACC_EMPTY + 8 * buf, (use & 1u) ^ 1u, kSiteAccEmpty)) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem + buf * TN;
-        const int32_t split = u / n_tiles, kb0 = split * p.split_blocks;
-        const int32_t kb1 = min(p.k_blocks, kb0 + p.split_blocks);
-        for (int32_t kb = kb0; kb < kb1; ++kb) {
+        const Unit w = unit_of(u);
+        const bool a_across = GRADS && w.dw;
+        const uint32_t idesc = idesc_bf16_f32(256, TN, GRADS ? 1 : 0) | (a_across ? 1u << 15 : 0u);
+        const uint64_t a_step = a_across ? 128 : 2;
+        for (int32_t kb = w.kb0; kb < w.kb1; ++kb) {
           if (!wait(bars + L::FULL + 8 * stage, phase, kSiteFull)) {
             ok = false;
             break;
           }
           tc_fence_after();
           const uint32_t sa = sbase + stage * STAGE_BYTES, sb = sa + A_BYTES;
-          const uint64_t da = sdesc_sw128(sa, A_LBO, 1024), db = sdesc_sw128(sb, B_LBO, 1024);
+          const uint64_t da = sdesc_sw128(sa, a_across ? kAcross : 16, 1024), db = sdesc_sw128(sb, B_LBO, 1024);
 #pragma unroll
           for (int kk = 0; kk < TK / 16; ++kk)
-            pair::mma(leader, d_tmem, da + kk * A_STEP, db + kk * B_STEP, IDESC, kb != kb0 || kk != 0);
+            pair::mma(leader, d_tmem, da + kk * a_step, db + kk * B_STEP, idesc, kb != w.kb0 || kk != 0);
           pair::commit(leader, bars + L::EMPTY + 8 * stage);  // both CTAs' stage is free
           __syncwarp();
           if (++stage == uint32_t(L::STAGES)) {
@@ -309,8 +328,7 @@ __global__ void __launch_bounds__((Lay<JVP, TN>::THREADS), 1) linear_sm100_kerne
     const uint32_t ex_id = uint32_t((q & 1) + 2 * cols);
     const uint32_t ex = sbase + L::OFF_EX + ex_id * EX_BYTES;
     const uint32_t acc_empty_leader = pair::at_rank(bars + L::ACC_EMPTY, 0);
-    const CUtensorMap *om = op ? &p.tm_y2 : &p.tm_y;
-    const uint16_t *res = EPI && p.splits == 1 ? static_cast<const uint16_t *>(op ? p.tres : p.res) : nullptr;
+    const uint16_t *res = EPI && p.prob[0].splits == 1 ? static_cast<const uint16_t *>(op ? p.tres : p.res) : nullptr;
     const int64_t ld_res = op ? p.ld_tres : p.ld_res;
     uint32_t count = 0, exchanged = 0, stores = 0;
     bool ok = true;
@@ -321,11 +339,14 @@ __global__ void __launch_bounds__((Lay<JVP, TN>::THREADS), 1) linear_sm100_kerne
       return sbuf0 + (stores++ % L::OUT_BUFS) * OUT_BYTES;
     };
     for (int32_t u = first; ok && u < n_units; u += step, ++count) {
-      const int32_t t = u % n_tiles, split = u / n_tiles;
-      const int32_t row0 = (t / p.n_tiles) * TM + int32_t(rank) * (TM / 2) + 32 * (JVP ? q & 1 : q);
-      const int32_t n0 = (t % p.n_tiles) * TN + 64 * cols;
+      const Unit w = unit_of(u);
+      const LinearProblem &prob = p.prob[w.dw];
+      const int32_t M = prob.M, N = prob.N;
+      const CUtensorMap *om = op || w.dw ? &p.tm_y2 : &p.tm_y;
+      const int32_t row0 = w.m * TM + int32_t(rank) * (TM / 2) + 32 * (JVP ? q & 1 : q);
+      const int32_t n0 = w.n * TN + 64 * cols;
       const uint32_t buf = count & 1u, use = count >> 1;
-      const bool rows_in = row0 < p.M;
+      const bool rows_in = row0 < M;
       // residual, a chunk ahead, coalesced: four lanes a row, eight rows at a time
       uint4 rv[4];
       auto fetch_residual = [&](int32_t cs) {
@@ -333,12 +354,12 @@ __global__ void __launch_bounds__((Lay<JVP, TN>::THREADS), 1) linear_sm100_kerne
         for (int i = 0; i < 4; ++i) {
           const int32_t r = row0 + 8 * i + (lane >> 2), cc = cs + 8 * (lane & 3);
           rv[i] = make_uint4(0, 0, 0, 0);
-          if (r < p.M && cc < p.N) rv[i] = __ldcs(reinterpret_cast<const uint4 *>(res + r * ld_res + cc));
+          if (r < M && cc < N) rv[i] = __ldcs(reinterpret_cast<const uint4 *>(res + r * ld_res + cc));
         }
       };
       if (EPI && res) fetch_residual(n0);
       uint32_t bias2 = 0;  // the bias of this lane's two columns, zero past the last
-      if (EPI && p.bias && op == 0 && n0 + 2 * lane < p.N)
+      if (EPI && p.bias && op == 0 && n0 + 2 * lane < N)
         bias2 = __ldg(reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(p.bias) + n0) + lane);
       if (!wait(bars + L::ACC_FULL + 8 * buf, use & 1u, kSiteAccFull)) break;
       tc_fence_after();
@@ -353,18 +374,18 @@ __global__ void __launch_bounds__((Lay<JVP, TN>::THREADS), 1) linear_sm100_kerne
           if (lane == 0) pair::arrive_remote_relaxed(acc_empty_leader + 8 * buf);
         }
         const int32_t cs = n0 + 32 * c;
-        if (!rows_in || cs >= p.N || 64 * cols + 32 * c >= TN) continue;
-        if (p.splits > 1) {  // fp32 parts, 16 columns at a time
+        if (!rows_in || cs >= N || 64 * cols + 32 * c >= TN) continue;
+        if (prob.splits > 1) {  // fp32 parts, 16 columns at a time
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            if (cs + 16 * h >= p.N) continue;
+            if (cs + 16 * h >= N) continue;
             const uint32_t sbuf = next_tile();
 #pragma unroll
             for (int g = 0; g < 4; ++g)
               sts128(swz64(sbuf, lane, g), acc[16 * h + 4 * g], acc[16 * h + 4 * g + 1], acc[16 * h + 4 * g + 2],
                      acc[16 * h + 4 * g + 3]);
-            fence_async_smem_then_store(&p.tm_part, sbuf, cs + 16 * h,
-                                        (split * (JVP ? 2 : 1) + op) * p.part_rows + row0, lane);
+            fence_async_smem_then_store(GRADS && w.dw ? &p.tm_part2 : &p.tm_part, sbuf, cs + 16 * h,
+                                        int32_t((w.split * (JVP ? 2 : 1) + op) * prob.part_rows) + row0, lane);
           }
           continue;
         }
@@ -426,7 +447,7 @@ __global__ void __launch_bounds__((Lay<JVP, TN>::THREADS), 1) linear_sm100_kerne
               } else if (sc == ck::kMaxScale) {
                 ck::pack_saturated(v, w);
               }
-              if (row0 + lane < p.M) {
+              if (row0 + lane < M) {
                 uint4 *dst = reinterpret_cast<uint4 *>(p.codes + size_t(row0 + lane) * (32 * size_t(p.nb)) + cs);
                 dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
                 dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
@@ -463,7 +484,7 @@ __global__ void __launch_bounds__((Lay<JVP, TN>::THREADS), 1) linear_sm100_kerne
         }
         fence_async_smem_then_store(om, sbuf, cs, row0, lane);
       }
-      if (EPI && ok && p.codes && p.splits == 1 && op == 0 && rows_in && row0 + lane < p.M && n0 < 32 * p.nb)
+      if (EPI && ok && p.codes && prob.splits == 1 && op == 0 && rows_in && row0 + lane < M && n0 < 32 * p.nb)
         store_scales<TN>(p.scales + size_t(row0 + lane) * p.ns, scale_word, n0 / 32, 64 * cols + 32 < TN, p);
     }
     if (lane == 0) pair::store_wait<0>();
@@ -486,11 +507,13 @@ __global__ void __launch_bounds__((Lay<JVP, TN>::THREADS), 1) linear_sm100_kerne
 template <bool JVP, bool EPI>
 __global__ void __launch_bounds__(256) linear_finish_kernel(const LinearParams p) {
   begin_after_previous();
-  const int32_t vecs = ck::blocks_of(p.N) * 4;
+  const int32_t M = p.prob[0].M, N = p.prob[0].N, splits = p.prob[0].splits;
+  const int64_t part_rows = p.prob[0].part_rows;
+  const int32_t vecs = ck::blocks_of(N) * 4;
   const int64_t g = int64_t(blockIdx.x) * 256 + threadIdx.x;
   const int64_t row = g / vecs;
   const int32_t col = int32_t(g - row * vecs) * 8;
-  const bool on = row < p.M, in = on && col < p.N;
+  const bool on = row < M, in = on && col < N;
   float v[2][8];
 #pragma unroll
   for (int op = 0; op < (JVP ? 2 : 1); ++op) {
@@ -498,9 +521,9 @@ __global__ void __launch_bounds__(256) linear_finish_kernel(const LinearParams p
     for (int i = 0; i < 8; ++i) v[op][i] = 0.f;
     if (!in) continue;
 #pragma unroll 4
-    for (int32_t s = 0; s < p.splits; ++s) {
+    for (int32_t s = 0; s < splits; ++s) {
       const float4 *src = reinterpret_cast<const float4 *>(
-          p.part + (size_t(s * (JVP ? 2 : 1) + op) * p.part_rows + row) * p.N + col);
+          p.part + (size_t(s * (JVP ? 2 : 1) + op) * part_rows + row) * N + col);
       const float4 a = __ldcs(src), b = __ldcs(src + 1);
       v[op][0] += a.x; v[op][1] += a.y; v[op][2] += a.z; v[op][3] += a.w;
       v[op][4] += b.x; v[op][5] += b.y; v[op][6] += b.z; v[op][7] += b.w;
@@ -558,7 +581,7 @@ __global__ void __launch_bounds__(256) linear_finish_kernel(const LinearParams p
     }
     v8::Raw<__nv_bfloat16> o;
     v8::pack(v[op], o);
-    v8::store(static_cast<__nv_bfloat16 *>(op ? p.ty : p.y) + size_t(row) * p.N + col, o);
+    v8::store(static_cast<__nv_bfloat16 *>(op ? p.ty : p.y) + size_t(row) * N + col, o);
   }
 }
 
@@ -571,9 +594,9 @@ __global__ void __launch_bounds__(256) linear_finish_kernel(const LinearParams p
 // the products. One warp per token, one lane per column.
 template <int COLS>
 __device__ __forceinline__ void rows_epilogue(const LinearParams &p, const float *z, int32_t ldz, int32_t base) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rows = p.M;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rows = p.prob[0].M;
   const int32_t col = base + lane;
-  const bool jvp = p.tx != nullptr, in = lane < COLS && col < p.N;
+  const bool jvp = p.tx != nullptr, in = lane < COLS && col < p.prob[0].N;
   const float bias = in && p.bias ? __uint_as_float(uint32_t(static_cast<const uint16_t *>(p.bias)[col]) << 16) : 0.f;
   for (int32_t r = warp; r < rows; r += int32_t(blockDim.x >> 5)) {
     float v[1] = {in ? z[r * ldz + lane] + bias : 0.f}, sl[1];
@@ -591,11 +614,11 @@ __device__ __forceinline__ void rows_epilogue(const LinearParams &p, const float
     if (!in) continue;
     lin::act_all<true>(p.act, v, sl);
     if (p.res) v[0] += __bfloat162float(static_cast<const __nv_bfloat16 *>(p.res)[r * p.ld_res + col]);
-    static_cast<__nv_bfloat16 *>(p.y)[size_t(r) * p.N + col] = __float2bfloat16_rn(v[0]);
+    static_cast<__nv_bfloat16 *>(p.y)[size_t(r) * p.prob[0].N + col] = __float2bfloat16_rn(v[0]);
     if (jvp) {
       float t = sl[0] * z[(r + rows) * ldz + lane];
       if (p.tres) t += __bfloat162float(static_cast<const __nv_bfloat16 *>(p.tres)[r * p.ld_tres + col]);
-      static_cast<__nv_bfloat16 *>(p.ty)[size_t(r) * p.N + col] = __float2bfloat16_rn(t);
+      static_cast<__nv_bfloat16 *>(p.ty)[size_t(r) * p.prob[0].N + col] = __float2bfloat16_rn(t);
     }
   }
 }
@@ -612,18 +635,18 @@ __global__ void __launch_bounds__(256) linear_rows_kernel(const LinearParams p) 
   begin_after_previous();
   constexpr int kRows = 8 * NT, kCols = 16 * MT, kLd = kCols + 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int32_t base = int32_t(blockIdx.x) * kCols, rows = p.tx ? 2 * p.M : p.M;
+  const int32_t base = int32_t(blockIdx.x) * kCols, M = p.prob[0].M, N = p.prob[0].N, K = p.K, rows = p.tx ? 2 * M : M;
   const uint16_t *w = static_cast<const uint16_t *>(p.w);
   const uint4 none = make_uint4(0, 0, 0, 0);
   const uint16_t *wrow[2 * MT], *xrow[NT];
 #pragma unroll
-  for (int i = 0; i < 2 * MT; ++i) wrow[i] = base + 8 * i + g < p.N ? w + size_t(base + 8 * i + g) * p.K : nullptr;
+  for (int i = 0; i < 2 * MT; ++i) wrow[i] = base + 8 * i + g < N ? w + size_t(base + 8 * i + g) * K : nullptr;
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
     const int32_t r = 8 * j + g;
     xrow[j] = r >= rows ? nullptr
-              : r < p.M ? static_cast<const uint16_t *>(p.x) + r * p.ld_x
-                        : static_cast<const uint16_t *>(p.tx) + (r - p.M) * p.ld_tx;
+              : r < M ? static_cast<const uint16_t *>(p.x) + r * p.ld_x
+                        : static_cast<const uint16_t *>(p.tx) + (r - M) * p.ld_tx;
   }
   float acc[MT][NT][4];
 #pragma unroll
@@ -635,9 +658,9 @@ __global__ void __launch_bounds__(256) linear_rows_kernel(const LinearParams p) 
   uint4 wn[2 * MT], xn[NT];  // the next step's pieces
   auto fetch = [&](int32_t k) {
 #pragma unroll
-    for (int i = 0; i < 2 * MT; ++i) wn[i] = wrow[i] && k < p.K ? __ldg(reinterpret_cast<const uint4 *>(wrow[i] + k)) : none;
+    for (int i = 0; i < 2 * MT; ++i) wn[i] = wrow[i] && k < K ? __ldg(reinterpret_cast<const uint4 *>(wrow[i] + k)) : none;
 #pragma unroll
-    for (int j = 0; j < NT; ++j) xn[j] = xrow[j] && k < p.K ? __ldg(reinterpret_cast<const uint4 *>(xrow[j] + k)) : none;
+    for (int j = 0; j < NT; ++j) xn[j] = xrow[j] && k < K ? __ldg(reinterpret_cast<const uint4 *>(xrow[j] + k)) : none;
   };
   auto mma = [](float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
     asm volatile(
@@ -645,7 +668,7 @@ __global__ void __launch_bounds__(256) linear_rows_kernel(const LinearParams p) 
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
   };
-  const int32_t steps = (p.K + 31) / 32;
+  const int32_t steps = (K + 31) / 32;
   fetch(32 * warp + 8 * t);
   for (int32_t step = warp; step < steps; step += 8) {
     uint4 wc[2 * MT], xc[NT];
@@ -789,9 +812,9 @@ __global__ void __launch_bounds__(256) column_sum_kernel(const float *part, int3
   }
 }
 
-template <bool JVP, bool AMN, bool BMN, bool EPI, int TN>
+template <bool JVP, bool GRADS, int TN>
 cudaError_t launch_tiles(const LinearParams &p, cudaStream_t stream) {
-  auto kernel = linear_sm100_kernel<JVP, AMN, BMN, EPI, TN>;
+  auto kernel = linear_sm100_kernel<JVP, GRADS, TN>;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -822,23 +845,28 @@ cudaError_t launch_tiles(const LinearParams &p, cudaStream_t stream) {
   });
   if (e != cudaSuccess) return e;
   const int64_t max_pairs = dev < 64 ? max_pairs_of[dev].load() : 74;
-  const int64_t units = int64_t(p.m_tiles) * p.n_tiles * p.splits;
+  int64_t units = 0;
+  for (int i = 0; i < (GRADS ? 2 : 1); ++i) units += int64_t(p.prob[i].m_tiles) * p.prob[i].n_tiles * p.prob[i].splits;
   cfg.gridDim = dim3(unsigned(2 * (units < max_pairs ? units : max_pairs)));
   cfg.numAttrs = 2;
   e = cudaLaunchKernelEx(&cfg, kernel, p);
-  if (e == cudaSuccess) e = cudaGetLastError();
-  if (e != cudaSuccess || p.splits == 1) return e;
-  const int64_t threads = int64_t(p.M) * ck::blocks_of(p.N) * 4;
+  return e == cudaSuccess ? cudaGetLastError() : e;
+}
+
+// Adds the parts of prob[0], if its contraction is split.
+template <bool JVP, bool EPI>
+cudaError_t finish(const LinearParams &p, cudaStream_t stream) {
+  if (p.prob[0].splits <= 1) return cudaSuccess;
+  const int64_t threads = int64_t(p.prob[0].M) * ck::blocks_of(p.prob[0].N) * 4;
   return launch_in_order(linear_finish_kernel<JVP, EPI>, dim3(unsigned((threads + 255) / 256)), 256, 0, stream, p);
 }
 
-template <bool JVP, bool AMN, bool BMN, bool EPI>
-cudaError_t launch_tiles(const LinearParams &p, cudaStream_t stream) {
-  if (p.tile_cols == 128) return launch_tiles<JVP, AMN, BMN, EPI, 128>(p, stream);
-  if constexpr (!BMN) {  // 80 columns a CTA are not whole 64-column blocks of an MN-major operand
-    if (p.tile_cols == 160) return launch_tiles<JVP, AMN, BMN, EPI, 160>(p, stream);
-  }
-  return launch_tiles<JVP, AMN, BMN, EPI, 256>(p, stream);
+template <bool JVP>
+cudaError_t launch_fwd_tiles(const LinearParams &p, cudaStream_t stream) {
+  const cudaError_t e = p.tile_cols == 128   ? launch_tiles<JVP, false, 128>(p, stream)
+                        : p.tile_cols == 160 ? launch_tiles<JVP, false, 160>(p, stream)
+                                             : launch_tiles<JVP, false, 256>(p, stream);
+  return e == cudaSuccess ? finish<JVP, true>(p, stream) : e;
 }
 
 template <int NT>
@@ -846,25 +874,29 @@ cudaError_t launch_rows(const LinearParams &p, cudaStream_t stream) {
   // 16 columns a block where 32 would leave SMs without one; a checkpoint's blocks are 32
   constexpr int kSmem = 8 * 8 * NT * 33 * int(sizeof(float));
   static_assert(kSmem <= 48 * 1024, "shared memory without an attribute");
-  if (p.codes || p.N > 32 * 148)
-    return launch_in_order(linear_rows_kernel<NT, 2>, dim3(unsigned((p.N + 31) / 32)), 256, kSmem, stream, p);
-  return launch_in_order(linear_rows_kernel<NT, 1>, dim3(unsigned((p.N + 15) / 16)), 256, kSmem, stream, p);
+  if (p.codes || p.prob[0].N > 32 * 148)
+    return launch_in_order(linear_rows_kernel<NT, 2>, dim3(unsigned((p.prob[0].N + 31) / 32)), 256, kSmem, stream, p);
+  return launch_in_order(linear_rows_kernel<NT, 1>, dim3(unsigned((p.prob[0].N + 15) / 16)), 256, kSmem, stream, p);
 }
 
 }  // namespace
 
 cudaError_t launch_linear_fwd(const LinearParams &p, cudaStream_t stream) {
-  const int32_t rows = p.tx ? 2 * p.M : p.M;
-  if (rows <= kLinearFewRows) {
+  const int32_t rows = p.tx ? 2 * p.prob[0].M : p.prob[0].M;
+  if (rows <= kLinearFewRows)
     return rows <= 8 ? launch_rows<1>(p, stream) : rows <= 16 ? launch_rows<2>(p, stream) : launch_rows<4>(p, stream);
-  }
-  return p.tx ? launch_tiles<true, false, false, true>(p, stream) : launch_tiles<false, false, false, true>(p, stream);
+  return p.tx ? launch_fwd_tiles<true>(p, stream) : launch_fwd_tiles<false>(p, stream);
 }
-cudaError_t launch_linear_dx(const LinearParams &p, cudaStream_t stream) {
-  return launch_tiles<false, false, true, false>(p, stream);
-}
-cudaError_t launch_linear_dw(const LinearParams &p, cudaStream_t stream) {
-  return launch_tiles<false, true, true, false>(p, stream);
+
+cudaError_t launch_linear_grads(const LinearParams &p, cudaStream_t stream) {
+  cudaError_t e = p.tile_cols == 128 ? launch_tiles<false, true, 128>(p, stream) : launch_tiles<false, true, 256>(p, stream);
+  if (e == cudaSuccess) e = finish<false, false>(p, stream);
+  if (e != cudaSuccess) return e;
+  LinearParams dw = p;
+  dw.prob[0] = p.prob[1];
+  dw.part = p.part2;
+  dw.y = p.ty;
+  return finish<false, false>(dw, stream);
 }
 
 // Chunks of rows of the dz pass: about eight blocks an SM, at least 32 rows each.
