@@ -504,7 +504,8 @@ caj_status caj_qk_rope_bwd(const void *dq, const void *dk, const void *dv, const
  *        bias       [C] bf16, or null
  *        res, tres  [M, C] bf16, rows ldres, ldtres apart, or null (tres needs tx)
  *   out: y, ty      [M, C] bf16, contiguous, fully overwritten (ty null without tx)
- *        pre_codes, pre_scales  z's checkpoint, rows of C values; both null: none
+ *        pre_codes, pre_scales  z's checkpoint, rows of C values (codes 32-byte aligned:
+ *                   a block is stored at once); both null: none
  *   workspace       caj_linear_act_fwd_workspace() bytes (0 for most sizes), 16-byte
  *                   aligned; no other work may use it until the call is done
  * Sums are fp32; bias, activation, tangent and residual are applied in fp32 before

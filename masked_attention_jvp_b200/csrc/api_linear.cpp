@@ -158,7 +158,7 @@ caj_status caj_linear_act_fwd(const void *x, const void *tx, const void *w, cons
   if (res && !good_rows(res, shape->ldres, C)) return CAJ_ERR_INVALID_ARG;
   if (tres && (!tan || !good_rows(tres, shape->ldtres, C))) return CAJ_ERR_INVALID_ARG;
   if (!pre_codes != !pre_scales) return CAJ_ERR_INVALID_ARG;
-  if (pre_codes && (!aligned_to(pre_codes, 16) || !aligned_to(pre_scales, 4))) return CAJ_ERR_INVALID_ARG;
+  if (pre_codes && (!aligned_to(pre_codes, 32) || !aligned_to(pre_scales, 4))) return CAJ_ERR_INVALID_ARG;
   const bool few = few_rows(M, tan);
   const FwdPlan pl = plan_fwd(M, C, K, tan);
   if (!few && pl.part_bytes && (!workspace || !aligned_to(workspace, 16) || workspace_bytes < size_t(pl.part_bytes)))

@@ -129,6 +129,13 @@ __device__ __forceinline__ void fence_async_smem_then_store(const CUtensorMap *m
   __syncwarp();
 }
 
+// 32 bytes, a whole sector, by one instruction.
+__device__ __forceinline__ void store_sector(void *dst, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
 // The scale bytes of a row in one warp's columns (two, or one at the end of a 160-column
 // tile); the row's last block also stores the padding that rounds a row up to four.
 template <int TN>
@@ -448,9 +455,7 @@ __global__ void __launch_bounds__((Lay<JVP, TN>::THREADS), 1) linear_sm100_kerne
                 ck::pack_saturated(v, w);
               }
               if (row0 + lane < M) {
-                uint4 *dst = reinterpret_cast<uint4 *>(p.codes + size_t(row0 + lane) * (32 * size_t(p.nb)) + cs);
-                dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-                dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                store_sector(p.codes + size_t(row0 + lane) * (32 * size_t(p.nb)) + cs, w);
               }
             }
             if (p.act != lin::kActNone) {

@@ -275,7 +275,7 @@ def test_linear_fwd_row_refusals(kw):
 
 @pytest.mark.parametrize("ptrs", [dict(x=0), dict(w=0), dict(y=0), dict(x=A + 8), dict(tx=A + 2), dict(w=A + 8),
                                   dict(bias=A + 2), dict(res=A + 8), dict(tres=A + 8), dict(tx=0), dict(ty=0),
-                                  dict(codes=0), dict(scales=0), dict(scales=A + 2), dict(codes=A + 8),
+                                  dict(codes=0), dict(scales=0), dict(scales=A + 2), dict(codes=A + 16),
                                   dict(tx=0, ty=0)])
 def test_linear_fwd_pointer_refusals(ptrs):
     assert _lfwd(ptrs) == INVALID  # the last: tres without tx
