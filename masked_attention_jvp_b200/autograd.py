@@ -22,6 +22,13 @@ attention, the inputs of the norm and of the linear layer. (A linear layer with
 an activation keeps its pre-activation in 8 bits either way, written by the
 product's epilogue.) Values and tangents of the forward do not change; gradients
 are those at the rounded activations.
+
+In a CUDA graph: capture forward and gradients together after one call outside, on
+leaves taken anew inside the capture (t.detach().requires_grad_()). PyTorch keeps a
+leaf's accumulation node on the stream where it was first used for as long as a graph
+of it is alive, and refuses to capture a backward() or autograd.grad() that meets such
+a node of another stream. The calls beneath (linear_act_fwd, linear_act_bwd and so on)
+have no such node.
 """
 from __future__ import annotations
 

@@ -217,3 +217,33 @@ def test_backward_replays_in_a_graph():
         torch.cuda.synchronize()
         for a, c in zip(out, grads(x, dy)):
             assert torch.equal(a, c)
+
+
+def test_autograd_replays_in_a_graph():
+    """Forward and gradients through autograd captured while an eager graph of the same tensors
+    is alive, on leaves taken anew inside the capture, and replayed on new inputs."""
+    g = torch.Generator().manual_seed(10)
+    tensors = [rnd(g, 200, 256), rnd(g, 128, 256, std=0.06), rnd(g, 128)]
+    eager = [t.requires_grad_() for t in tensors]
+    dy = rnd(g, 200, 128)
+
+    def grads():
+        leaves = [t.detach().requires_grad_() for t in tensors]
+        y, _ = caj.linear_act(*leaves, "gelu_tanh", ckpt8=True)
+        return (y.detach(),) + torch.autograd.grad(y, leaves, dy)
+
+    alive, _ = caj.linear_act(*eager, "silu")
+    grads()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = grads()
+    alive.backward(dy)  # the eager graph is none the worse
+    with torch.no_grad():
+        tensors[0].mul_(-0.5)
+        dy.mul_(2)
+    graph.replay()
+    torch.cuda.synchronize()
+    for a, c in zip(out, grads()):
+        assert torch.equal(a, c)
+    assert all(t.grad is not None for t in eager)
