@@ -492,7 +492,7 @@ __global__ void __launch_bounds__((Lay<JVP, TN>::THREADS), 1) linear_sm100_kerne
       if (EPI && ok && p.codes && prob.splits == 1 && op == 0 && rows_in && row0 + lane < M && n0 < 32 * p.nb)
         store_scales<TN>(p.scales + size_t(row0 + lane) * p.ns, scale_word, n0 / 32, 64 * cols + 32 < TN, p);
     }
-    if (lane == 0) pair::store_wait<0>();
+    if (lane == 0) pair::store_wait_read<0>();  // (the writes end before the grid does)
     __syncwarp();
   }
 
