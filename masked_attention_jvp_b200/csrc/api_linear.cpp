@@ -20,58 +20,80 @@ size_t padded(int64_t bytes) { return size_t((bytes + 255) & ~int64_t(255)); }
 
 struct Plan {
   caj::LinearProblem prob;
-  int64_t part_bytes;
-  double us, work_us, unit_us;  // estimates: wave after wave; all units' work; one unit
+  int64_t units, part_bytes;
+  double unit_us, parts_us;
 };
-// rows x cols outputs (and as many tangents), contraction of `depth`, in tiles of
-// `tile_cols` columns: in how many parts the contraction runs, by the least estimate of
-//   waves * (blocks of a part * block time + tile time) + parts written and read again.
-// 74 pairs of SMs work at a time; a 64-wide block of the contraction takes a pair 0.40 us
-// at 256 columns, 0.28 at 160 and 0.23 at 128, a tile 1.0 to 1.5 us besides; parts cost 8
-// bytes an output at about 5 TB/s and a launch (3 us). The figures only weigh one shape
-// against another.
-Plan plan_tiles(int64_t rows, int64_t cols, int64_t depth, bool tangent, int32_t tile_cols) {
-  Plan best{};
-  const int64_t tile_rows = tangent ? kTileRows / 2 : kTileRows, ops = tangent ? 2 : 1;
-  const int64_t m_tiles = ceil_div(rows, tile_rows), n_tiles = ceil_div(cols, tile_cols), k_blocks = ceil_div(depth, kBlock);
-  const int64_t tiles = m_tiles * n_tiles;
-  const double block_us = tile_cols == 256 ? 0.40 : tile_cols == 160 ? 0.28 : 0.23;
-  const double tile_us = tile_cols == 256 ? 1.5 : tile_cols == 160 ? 1.2 : 1.0;
-  for (int32_t s = 1; s <= 32 && s <= k_blocks; ++s) {
-    const int64_t per = ceil_div(k_blocks, s);
-    if (ceil_div(k_blocks, per) != s) continue;  // a part would be empty
-    const double unit_us = block_us * double(per) + tile_us;
-    const double parts_us = s > 1 ? 3.0 + 8.0 * s * double(rows * cols * ops) / 5e6 : 0.0;
-    const double us = double(ceil_div(tiles * s, 74)) * unit_us + parts_us;
-    if (s > 1 && us >= best.us) continue;
-    best.us = us;
-    best.unit_us = unit_us;
-    best.work_us = double(tiles * s) / 74 * unit_us + parts_us;
-    best.prob = {int32_t(rows), int32_t(cols), int32_t(m_tiles), int32_t(n_tiles), int32_t(k_blocks), s, int32_t(per),
-                 m_tiles * tile_rows};
-    best.part_bytes = s > 1 ? int64_t(s) * ops * best.prob.part_rows * cols * 4 : 0;
-  }
-  return best;
+constexpr int64_t kPairs = 74;  // pairs of SMs, each at one tile (or part of one) at a time
+constexpr int32_t kMaxSplits = 32;
+
+// rows x cols outputs (and as many tangents), contraction of `depth` in `splits` parts, tiles
+// of `tile_cols` columns. The estimates weigh one shape against another; they were fitted to
+// the times on B200 of 154 shapes of each product (33 to 32760 tokens, 256 to 8192 channels),
+// every width and up to 10 parts: the choice by them takes 0.7% longer than each shape's
+// best forward and 1.0% longer backward, where figures from a few long products had taken
+// 2.4% and 4.0%. A 64-wide block of the contraction takes a pair 0.35 us at
+// 256 columns, 0.225 at 160 and 0.205 at 128, a tile 0.5 to 1 us besides. Parts cost 8
+// bytes an output at 8 TB/s and a launch that adds them.
+bool can_split(int32_t k_blocks, int32_t splits) {  // no part without blocks
+  if (splits > k_blocks) return false;
+  const int32_t per = (k_blocks + splits - 1) / splits;
+  return (k_blocks + per - 1) / per == splits;
 }
-// The forward's tiles: the width with the least estimate. Measured on B200 (primal and
-// tangent, 1560 tokens, 1536 x 1536): 78 tiles of 256 columns 25.2 us where 156 of 128 took
-// 21.1, then (another epilogue) 156 of 128 columns 18.8 us and 130 of 160 columns 16.2.
+Plan plan_tiles(int64_t rows, int64_t cols, int64_t depth, bool tangent, int32_t tile_cols, int64_t splits) {
+  Plan p{};
+  const int64_t tile_rows = tangent ? kTileRows / 2 : kTileRows, ops = tangent ? 2 : 1;
+  const int64_t m_tiles = ceil_div(rows, tile_rows), n_tiles = ceil_div(cols, tile_cols);
+  const int64_t k_blocks = ceil_div(depth, kBlock), per = ceil_div(k_blocks, splits);
+  const double block_us = tile_cols == 256 ? 0.35 : tile_cols == 160 ? 0.225 : 0.205;
+  p.units = m_tiles * n_tiles * splits;
+  p.unit_us = block_us * double(per) + (tile_cols == 256 ? 1.0 : tile_cols == 160 ? 0.8 : 0.5);
+  if (splits > 1) p.parts_us = 1.0 + 0.3 * double(splits) + double(8 * splits * ops) * double(rows * cols) / 8e6;
+  p.prob = {int32_t(rows), int32_t(cols), int32_t(m_tiles), int32_t(n_tiles), int32_t(k_blocks), int32_t(splits),
+            int32_t(per), m_tiles * tile_rows};
+  p.part_bytes = splits > 1 ? splits * ops * p.prob.part_rows * cols * 4 : 0;
+  return p;
+}
+// One launch over a's units, then b's, dealt out to the pairs in turn: the longest share is
+// the first pair's, or that of the first pair to begin with b. The launch that adds parts
+// starts later (0.5 us) when no SM is free to hold its blocks before.
+double launch_us(const Plan &a, const Plan &b) {
+  const int64_t all = a.units + b.units, n = ceil_div(a.units, kPairs), turn = a.units % kPairs;
+  const double first = double(n) * a.unit_us + double(ceil_div(all, kPairs) - n) * b.unit_us;
+  const int64_t m = a.units / kPairs, of_b = all > turn ? ceil_div(all - turn, kPairs) - m : 0;
+  const double parts = a.parts_us + b.parts_us + (a.part_bytes + b.part_bytes > 0 && all > 64 ? 0.5 : 0);
+  return std::max(first, double(m) * a.unit_us + double(of_b) * b.unit_us) + parts;
+}
+// More parts are not looked at once every pair has several units: what imbalance is left is
+// less than the parts cost.
+bool enough(const Plan &p) { return p.units >= 4 * kPairs; }
+
+// The forward's tiles: the width and split with the least estimate. Measured (primal and
+// tangent, 1560 tokens, 1536 x 1536): 78 tiles of 256 columns 26.3 us, 156 of 128 columns
+// 20.5, 130 of 160 columns 18.0.
 struct FwdPlan : Plan {
   int32_t tile_cols;
 };
 FwdPlan plan_fwd(int64_t M, int64_t C, int64_t K, bool tangent) {
   FwdPlan best{};
+  double best_us = 0;
   for (const int32_t tile_cols : {256, 160, 128}) {
-    const Plan p = plan_tiles(M, C, K, tangent, tile_cols);
-    if (best.tile_cols && p.us >= best.us) continue;
-    static_cast<Plan &>(best) = p;
-    best.tile_cols = tile_cols;
+    for (int32_t s = 1; s <= kMaxSplits; ++s) {
+      if (!can_split(int32_t(ceil_div(K, kBlock)), s)) continue;
+      const Plan p = plan_tiles(M, C, K, tangent, tile_cols, s);
+      const double us = launch_us(p, Plan{});
+      if (!best.tile_cols || us < best_us) {
+        static_cast<Plan &>(best) = p;
+        best.tile_cols = tile_cols;
+        best_us = us;
+      }
+      if (enough(p)) break;
+    }
   }
   return best;
 }
-// The gradients' tiles, dx and dW in one launch: their units together, and one unit's time
-// of imbalance at the end. Planned for both even where one is wanted, so that a gradient
-// does not depend, in its last bits, on whether the other was asked for.
+// The gradients' tiles, dW's and then dx's in one launch: of each width dW's split beside an
+// unsplit dx, then dx's beside that. Planned for both even where one is wanted, so that a
+// gradient does not depend, in its last bits, on whether the other was asked for.
 struct GradPlan {
   Plan dx, dw;
   int32_t tile_cols;
@@ -80,10 +102,24 @@ GradPlan plan_grads(int64_t M, int64_t C, int64_t K) {
   GradPlan best{};
   double best_us = 0;
   for (const int32_t tile_cols : {256, 128}) {
-    const GradPlan p{plan_tiles(M, K, C, false, tile_cols), plan_tiles(C, K, M, false, tile_cols), tile_cols};
-    const double us = p.dx.work_us + p.dw.work_us + std::max(p.dx.unit_us, p.dw.unit_us);
+    GradPlan g{plan_tiles(M, K, C, false, tile_cols, 1), plan_tiles(C, K, M, false, tile_cols, 1), tile_cols};
+    double us = launch_us(g.dw, g.dx);
+    for (int32_t s = 2; s <= kMaxSplits && !enough(g.dw); ++s) {
+      if (!can_split(int32_t(ceil_div(M, kBlock)), s)) continue;
+      const Plan p = plan_tiles(C, K, M, false, tile_cols, s);
+      const double t = launch_us(p, g.dx);
+      if (t < us) g.dw = p, us = t;
+      if (enough(p)) break;
+    }
+    for (int32_t s = 2; s <= kMaxSplits && !enough(g.dx); ++s) {
+      if (!can_split(int32_t(ceil_div(C, kBlock)), s)) continue;
+      const Plan p = plan_tiles(M, K, C, false, tile_cols, s);
+      const double t = launch_us(g.dw, p);
+      if (t < us) g.dx = p, us = t;
+      if (enough(p)) break;
+    }
     if (best.tile_cols && us >= best_us) continue;
-    best = p;
+    best = g;
     best_us = us;
   }
   return best;
