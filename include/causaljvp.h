@@ -416,14 +416,15 @@ caj_status caj_ckpt_unpack(const int8_t *codes, const uint8_t *scales, int64_t r
  *        freq   [pairs] fp64, radians per position; |pos * freq| < 2^50
  *        axis   [pairs] int32, which column of pos turns pair i; null: column 0.
  *               A pair whose axis is not in [0, axes) gets NaN.
+ *        mscale |mscale| < 2^126
  *   out: cos, sin [N, pairs] fp32
- * The product and its reduction are in 64 bits and carry the product's rounding
- * error along, so far positions are as exact as near ones. Scaled frequencies
+ * The angle is reduced in 64 bits, with the rest of freq * 2/pi carried along, so
+ * far positions are as exact as near ones. Scaled frequencies
  * (long contexts) are the caller's: freq is used as it is. Pointers aligned to
  * their elements. N = 0 launches nothing. Returns as above.
  */
 caj_status caj_rope_table(const void *pos, int32_t pos64, const double *freq, const int32_t *axis,
-                          int64_t N, int32_t axes, int32_t pairs, float mscale, float *cos, float *sin,
+                          int64_t N, int32_t axes, int32_t pairs, double mscale, float *cos, float *sin,
                           void *stream);
 
 /*

@@ -164,7 +164,7 @@ def lib() -> ctypes.CDLL:
         L.caj_ckpt_pack.restype = ctypes.c_int
         L.caj_ckpt_unpack.argtypes = [vp, vp, i64, i32, i64, i32, vp, vp]
         L.caj_ckpt_unpack.restype = ctypes.c_int
-        L.caj_rope_table.argtypes = [vp, i32, vp, vp, i64, i32, i32, ctypes.c_float, vp, vp, vp]
+        L.caj_rope_table.argtypes = [vp, i32, vp, vp, i64, i32, i32, ctypes.c_double, vp, vp, vp]
         L.caj_rope_table.restype = ctypes.c_int
         L.caj_qk_rope_fwd.argtypes = [vp] * 10 + [rope] + [vp] * 7
         L.caj_qk_rope_fwd.restype = ctypes.c_int

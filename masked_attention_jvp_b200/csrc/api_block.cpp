@@ -107,9 +107,9 @@ caj_status caj_ckpt_unpack(const int8_t *codes, const uint8_t *scales, int64_t r
 }
 
 caj_status caj_rope_table(const void *pos, int32_t pos64, const double *freq, const int32_t *axis, int64_t N,
-                          int32_t axes, int32_t pairs, float mscale, float *cos, float *sin, void *stream) {
+                          int32_t axes, int32_t pairs, double mscale, float *cos, float *sin, void *stream) {
   if (N < 0 || axes <= 0 || pairs <= 0 || (pos64 != 0 && pos64 != 1)) return CAJ_ERR_INVALID_ARG;
-  if (!std::isfinite(mscale)) return CAJ_ERR_INVALID_ARG;
+  if (!(std::fabs(mscale) < 0x1p126)) return CAJ_ERR_INVALID_ARG;  // pi/2 of it is a float
   if (N == 0) return CAJ_OK;
   if (!pos || !aligned_to(pos, pos64 ? 8 : 4) || !freq || !aligned_to(freq, 8)) return CAJ_ERR_INVALID_ARG;
   if (axis && !aligned_to(axis, 4)) return CAJ_ERR_INVALID_ARG;

@@ -219,7 +219,7 @@ PyObject *rope_table(PyObject *, PyObject *const *a, Py_ssize_t n) {
   Tensor cos = make({N, P}, at::kFloat, pos), sin = make({N, P}, at::kFloat, pos);
   On on(pos);
   check(caj_rope_table(ptr(pos), wide, static_cast<const double *>(ptr(freq)), static_cast<const int32_t *>(ptr(axis)), N,
-                       int32_t(A), int32_t(P), float(number(a[3])), static_cast<float *>(ptr(cos)),
+                       int32_t(A), int32_t(P), number(a[3]), static_cast<float *>(ptr(cos)),
                        static_cast<float *>(ptr(sin)), on.stream),
         "caj_rope_table");
   return tuple_of({cos, sin});

@@ -166,7 +166,7 @@ struct RopeTableParams {
   float *cos, *sin;      // [N, P]
   int64_t N;
   int32_t A, P;
-  float mscale;
+  double mscale;
 };
 
 // Norm + rotation of q and k (and v's new layout), forward or backward; index 0, 1, 2

@@ -31,61 +31,117 @@ namespace {
 constexpr int kNormNone = 0, kNormHead = 1, kNormToken = 2;
 
 // ------------------------------------------------------------- rotary angles
-// cos and sin of pos * freq, scaled by mscale. The product is kept exactly, as a
-// double and its rounding error (one fma), and reduced by multiples of pi/2 held
-// in two doubles, so an angle of 10^9 radians is as exact as one of 1. The rest,
-// |r| <= pi/4, goes through the Taylor series in fp32: sin to r^9 (the next term
-// is below 2e-9 r), cos to r^10 (below 2e-10).
-// Written once (8 bytes a pair), so bound by its stores; the 64-bit part is about
-// ten instructions a pair, well under the 64 a clock that an SM issues.
-__device__ __forceinline__ void cos_sin(double pos, double freq, float mscale, float &c, float &s) {
-  const double hi = __dmul_rn(pos, freq), lo = __fma_rn(pos, freq, -hi);
+using ptx::add2;
+using ptx::f2;
+using ptx::f2_split;
+using ptx::fma2;
+using ptx::mul2;
+
+// mscale cos and mscale sin of the angle pos * freq, counted in quarter turns: a thread holds
+// freq * 2/pi as a double and its rest (two fma's, once), and pos times that, less its nearest
+// whole number k, is exact but for the rest's rounding, so an angle of 10^9 radians is as
+// exact as one of 1. What remains, f in [-1/2, 1/2], goes through the Taylor series of
+// mscale sin(f pi/2) and mscale cos(f pi/2) in fp32, two pairs to an instruction: to f^9
+// (the next term is below 2e-9 of the sum) and f^10 (below 2e-10), the leading coefficient
+// with its rounding error. k's last bits say which series is which, and the signs.
+struct TurnSeries {
+  float s1, s1_rest, s3, s5, s7, s9;
+  float c0, c0_rest, c2, c4, c6, c8, c10;
+};
+__host__ TurnSeries turn_series(double mscale) {
+  double t[11] = {mscale};  // mscale (pi/2)^n / n!
+  for (int n = 1; n < 11; ++n) t[n] = t[n - 1] * 1.5707963267948966 / n;
+  TurnSeries o;
+  o.s1 = float(t[1]);
+  o.s1_rest = float(t[1] - double(o.s1));
+  o.s3 = float(-t[3]);
+  o.s5 = float(t[5]);
+  o.s7 = float(-t[7]);
+  o.s9 = float(t[9]);
+  o.c0 = float(t[0]);
+  o.c0_rest = float(t[0] - double(o.c0));
+  o.c2 = float(-t[2]);
+  o.c4 = float(t[4]);
+  o.c6 = float(-t[6]);
+  o.c8 = float(t[8]);
+  o.c10 = float(-t[10]);
+  return o;
+}
+__device__ __forceinline__ float quarter_turns(double pos, double turn, double rest, int &quadrant) {
   // 1.5 * 2^52 rounds to the nearest whole number, whose low bits it leaves in the mantissa
-  const double shifted = __fma_rn(hi, 0.63661977236758134308, 6755399441055744.0);
-  const int quadrant = __double2loint(shifted);
+  const double shifted = __fma_rn(pos, turn, 6755399441055744.0);
+  quadrant = __double2loint(shifted);
   const double k = shifted - 6755399441055744.0;
-  double r = __fma_rn(-k, 1.5707963267948965580, hi);       // pi/2, leading 53 bits
-  r = __fma_rn(-k, 6.1232339957367658860e-17, r) + lo;      // and the next 53
-  const float x = float(r), x2 = x * x;
-  float sn = fmaf(x2, 2.7557319e-6f, -1.9841270e-4f);
-  sn = fmaf(x2, sn, 8.3333333e-3f);
-  sn = fmaf(x2, sn, -1.6666667e-1f);
-  sn = fmaf(x2 * x, sn, x);
-  float cs = fmaf(x2, -2.7557319e-7f, 2.4801587e-5f);
-  cs = fmaf(x2, cs, -1.3888889e-3f);
-  cs = fmaf(x2, cs, 4.1666667e-2f);
-  cs = fmaf(x2, cs, -0.5f);
-  cs = fmaf(x2, cs, 1.f);
+  return float(__fma_rn(pos, rest, __fma_rn(pos, turn, -k)));
+}
+__device__ __forceinline__ void turned(float sn, float cs, int quadrant, float &s, float &c) {
   const float a = quadrant & 1 ? cs : sn, b = quadrant & 1 ? sn : cs;
-  s = (quadrant & 2 ? -a : a) * mscale;
-  c = ((quadrant + 1) & 2 ? -b : b) * mscale;
+  const uint32_t q = uint32_t(quadrant) << 30;  // the sign bit is q & 2, or (q + 1) & 2
+  s = __uint_as_float(__float_as_uint(a) ^ (q & 0x80000000u));
+  c = __uint_as_float(__float_as_uint(b) ^ ((q + 0x40000000u) & 0x80000000u));
+}
+__device__ __forceinline__ uint64_t twice(float v) { return f2(v, v); }
+__device__ __forceinline__ void sin_cos_pair(const TurnSeries &k, uint64_t f, uint64_t &sn, uint64_t &cs) {
+  const uint64_t f_f = mul2(f, f);
+  sn = fma2(f_f, twice(k.s9), twice(k.s7));
+  sn = fma2(f_f, sn, twice(k.s5));
+  sn = fma2(f_f, sn, twice(k.s3));
+  sn = fma2(f_f, sn, twice(k.s1_rest));
+  sn = fma2(f, twice(k.s1), mul2(f, sn));
+  cs = fma2(f_f, twice(k.c10), twice(k.c8));
+  cs = fma2(f_f, cs, twice(k.c6));
+  cs = fma2(f_f, cs, twice(k.c4));
+  cs = fma2(f_f, cs, twice(k.c2));
+  cs = add2(fma2(f_f, cs, twice(k.c0_rest)), twice(k.c0));
 }
 
-// A thread owns V neighbouring pairs (V = 4: 16-byte stores) and walks over the
-// positions, so frequencies and axes stay in registers.
+// A thread owns V neighbouring pairs (V = 4: 16-byte stores) and walks over the positions, so
+// turns and axes stay in registers; the next position is on its way meanwhile. Written once
+// (8 bytes a pair): 131072 x 64 take 13.8 us of 10.4 that the stores alone would (four blocks
+// an SM, 64 registers; five at 48 registers 17.3; 8 pairs a thread at two blocks 13.1, but
+// with 32-byte rows). With the reduction in radians, seven 64-bit operations a pair
+// instead of four, and scalar series it took 16.7.
+constexpr int kTableBlocks = 4;
 template <typename I, int V>
-__global__ void __launch_bounds__(256) rope_table_kernel(const RopeTableParams p) {
+__global__ void __launch_bounds__(256, kTableBlocks) rope_table_kernel(const RopeTableParams p, const TurnSeries series) {
   begin_after_previous();
   const int32_t cols = p.P / V;  // threads across a row of pairs
   const int64_t id = int64_t(blockIdx.x) * 256 + threadIdx.x;
   const int64_t row0 = id / cols, step = int64_t(gridDim.x) * 256 / cols;  // a whole number of rows
   const int32_t i = int32_t(id - row0 * cols) * V;
-  double freq[V];
+  double turn[V], rest[V];
   int32_t ax[V];
 #pragma unroll
   for (int e = 0; e < V; ++e) {
-    freq[e] = __ldg(p.freq + i + e);
+    double freq = __ldg(p.freq + i + e);
     ax[e] = p.axis ? __ldg(p.axis + i + e) : 0;
-    if (ax[e] < 0 || ax[e] >= p.A) freq[e] = __longlong_as_double(0x7FF8000000000000ll), ax[e] = 0;  // NaN
+    if (ax[e] < 0 || ax[e] >= p.A) freq = __longlong_as_double(0x7FF8000000000000ll), ax[e] = 0;  // NaN
+    turn[e] = __dmul_rn(freq, 0.6366197723675814);  // 2/pi, leading 53 bits
+    rest[e] = __fma_rn(freq, -3.935735335036497e-17, __fma_rn(freq, 0.6366197723675814, -turn[e]));  // and the next
   }
+  const I *at_pos = static_cast<const I *>(p.pos);
+  I next = row0 < p.N ? __ldg(at_pos + row0 * p.A + ax[0]) : I(0);
   for (int64_t n = row0; n < p.N; n += step) {
-    float c[V], s[V];
-    const I *row = static_cast<const I *>(p.pos) + n * p.A;
-    double pos = double(__ldg(row + ax[0]));
+    const I *row = at_pos + n * p.A;
+    double pos = double(next);
+    if (n + step < p.N) next = __ldg(row + step * p.A + ax[0]);
+    float f[V], c[V], s[V];
+    int quadrant[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) {
       if (e && ax[e] != ax[e - 1]) pos = double(__ldg(row + ax[e]));  // neighbouring pairs mostly share their axis
-      cos_sin(pos, freq[e], p.mscale, c[e], s[e]);
+      f[e] = quarter_turns(pos, turn[e], rest[e], quadrant[e]);
+    }
+#pragma unroll
+    for (int e = 0; e < V; e += 2) {
+      constexpr int kNext = V > 1;
+      uint64_t sn, cs;
+      sin_cos_pair(series, f2(f[e], f[e + kNext]), sn, cs);
+      float s0, s1, c0, c1;
+      f2_split(sn, s0, s1);
+      f2_split(cs, c0, c1);
+      turned(s0, c0, quadrant[e], s[e], c[e]);
+      if (kNext) turned(s1, c1, quadrant[e + kNext], s[e + kNext], c[e + kNext]);
     }
     const int64_t at = n * p.P + i;
     if constexpr (V == 4) {
@@ -99,12 +155,6 @@ __global__ void __launch_bounds__(256) rope_table_kernel(const RopeTableParams p
 }
 
 // ------------------------------------------------------------ norm + rotation
-using ptx::add2;
-using ptx::f2;
-using ptx::f2_split;
-using ptx::fma2;
-using ptx::mul2;
-
 struct Lane {        // a thread's place: eight channels of one head, one token of T
   int32_t V, T;      // vectors of a token (of the wider tensor), tokens of a block
   int32_t t, vec, head, d0;
@@ -690,14 +740,15 @@ cudaError_t launch_bwd(const QkRopeParams &p, cudaStream_t stream) {
 }  // namespace
 
 namespace {
-// The grid's threads are a whole number of rows: a multiple of `cols` blocks.
+// The grid's threads are a whole number of rows: a multiple of `cols` blocks, and no more
+// than are resident at once.
 template <typename I, int V>
 cudaError_t launch_table(const RopeTableParams &p, cudaStream_t stream) {
-  const int64_t cols = p.P / V, most = 148 * 8;
+  const int64_t cols = p.P / V, most = 148 * kTableBlocks;
   const int64_t want = (p.N * cols + 255) / 256;
-  int64_t blocks = want < most ? want : most;
-  blocks = (blocks + cols - 1) / cols * cols;
-  return launch_in_order(rope_table_kernel<I, V>, dim3(unsigned(blocks)), 256, 0, stream, p);
+  int64_t blocks = (want + cols - 1) / cols * cols;
+  if (blocks > most) blocks = cols < most ? most / cols * cols : cols;
+  return launch_in_order(rope_table_kernel<I, V>, dim3(unsigned(blocks)), 256, 0, stream, p, turn_series(p.mscale));
 }
 }  // namespace
 

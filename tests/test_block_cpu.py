@@ -102,6 +102,13 @@ def test_rope_table_refusals(kw, want):
     assert _table(**kw) == want
 
 
+@pytest.mark.parametrize("mscale", [2.0**126, -2.0**126, 1e300])
+def test_rope_table_refuses_scales_past_fp32(mscale):
+    assert _table(mscale=mscale) == INVALID
+    assert _table(mscale=mscale, N=0) == INVALID
+    assert _table(mscale=2.0**125, N=0) == 0
+
+
 def _rope_shape(**kw):
     v = dict(B=1, N=5, Hq=4, Hk=2, D=64, pairs=32, dtype=1, norm=1, layout=0, gain_full=0, eps=1e-6, ldq=256,
              ldk=128, ldv=128, ldtq=256, ldtk=128, ldtv=128)

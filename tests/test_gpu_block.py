@@ -104,6 +104,21 @@ def test_rope_table(N, axes, P, start, dt):
                 assert abs(float(sin[n, i]) - m * math.sin(r)) <= m * 4 * U + U * m
 
 
+@pytest.mark.parametrize("P", [3, 61, 64])
+@pytest.mark.parametrize("dt", [torch.int32, torch.int64])
+def test_rope_table_long(P, dt):
+    """More rows than threads at work: every thread walks, the last ones end early."""
+    N, m = 30011, 1.2079
+    freq, axis = caj.rope_frequencies([2 * ((P + a) // 3) for a in range(3)])
+    pos = torch.stack([(torch.arange(N) * (7 + a)) % 65521 - 1000 * a for a in range(3)], 1).to(dt).cuda()
+    cos, sin = caj.rope_table(pos, freq, axis, mscale=m)
+    angle = pos[:, axis.long()].double() * freq  # below 2^17: off by 2^-37
+    for got, want in ((cos, angle.cos() * m), (sin, angle.sin() * m)):
+        # the reduced angle and each series round a few times: 4 half-steps at 1, and the result's own
+        assert float((got - want).abs().max()) <= m * 5 * U
+    assert float((cos.double() ** 2 + sin.double() ** 2 - m * m).abs().max()) <= 2 * m * m * 5 * U * 2
+
+
 def test_rope_table_one_axis_and_bad_axis():
     freq, axis = caj.rope_frequencies(16)
     pos = torch.arange(5, device="cuda")
