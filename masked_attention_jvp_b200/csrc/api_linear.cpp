@@ -280,8 +280,11 @@ caj_status caj_linear_act_bwd(const void *dy, const void *x, const uint8_t *x_sc
     dz = const_cast<void *>(dy);
     ld_dz = shape->ldy;
   }
+  // db: the products do not wait for it. Without an activation its sums over dy run beside
+  // them, with one the chunks' sums are added after them.
+  const bool products = dx || dw;
+  caj::LinearDzParams d{};
   if (act || db) {
-    caj::LinearDzParams d{};
     d.dy = dy;
     d.codes = pre_codes;
     d.scales = pre_scales;
@@ -294,10 +297,11 @@ caj_status caj_linear_act_bwd(const void *dy, const void *x, const uint8_t *x_sc
     d.ns = caj::ck::scale_bytes(shape->C);
     d.act = shape->act;
     d.chunk_rows = b.chunk_rows;
-    st = done(caj::launch_linear_dz(d, db, s));
+    d.late = !act && products;
+    if (!d.late) st = done(caj::launch_linear_dz(d, s));
     if (st != CAJ_OK) return st;
   }
-  if (!dx && !dw) return CAJ_OK;
+  if (!products) return db ? done(caj::launch_linear_db(d, db, false, s)) : CAJ_OK;
   int64_t ld_x = shape->ldx;
   if (dw && x_scales) {
     caj::Ckpt8Params c{};
@@ -332,7 +336,8 @@ caj_status caj_linear_act_bwd(const void *dy, const void *x, const uint8_t *x_sc
     ok = ok && caj::encode_map_2d_ld(&p.tm_b2, x, M, K, ld_x, 64) && caj::encode_out_2d(&p.tm_y2, dw, C, K, false) &&
          part_map(&p.tm_part2, b.grads.dw, false, p.part2);
   if (!ok) return caj::cuda_fail(cudaErrorInvalidValue);
-  return done(caj::launch_linear_grads(p, s));
+  st = done(caj::launch_linear_grads(p, d.late ? &d : nullptr, s));
+  return st == CAJ_OK && db ? done(caj::launch_linear_db(d, db, !d.late, s)) : st;
 }
 
 }  // extern "C"

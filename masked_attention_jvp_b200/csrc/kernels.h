@@ -224,6 +224,7 @@ struct LinearDzParams {
   float *partial;         // [chunks][C], or null
   int64_t M, ld_dy;
   int32_t C, nb, ns, act, chunk_rows;
+  int32_t late;           // beside the products that went before (act = none: nothing of theirs is read)
 };
 
 // 8-bit checkpoints of `rows` rows: nb blocks and ns scale bytes a row, total = rows * nb.
@@ -273,8 +274,10 @@ cudaError_t launch_qk_rope_fwd(const QkRopeParams &p, bool bf16, cudaStream_t st
 cudaError_t launch_qk_rope_bwd(const QkRopeParams &p, bool bf16, cudaStream_t stream);
 int32_t qk_rope_bwd_blocks(int32_t B, int32_t N, int32_t Hq, int32_t Hk, int32_t D);
 cudaError_t launch_linear_fwd(const LinearParams &p, cudaStream_t stream);
-cudaError_t launch_linear_grads(const LinearParams &p, cudaStream_t stream);
-cudaError_t launch_linear_dz(const LinearDzParams &p, float *db, cudaStream_t stream);
+// `sums`: column sums alone (late), to run beside the products
+cudaError_t launch_linear_grads(const LinearParams &p, const LinearDzParams *sums, cudaStream_t stream);
+cudaError_t launch_linear_dz(const LinearDzParams &p, cudaStream_t stream);
+cudaError_t launch_linear_db(const LinearDzParams &p, float *db, bool late, cudaStream_t stream);
 int32_t linear_dz_chunk_rows(int64_t M, int32_t C);
 cudaError_t read_and_clear_linear_error(uint32_t *out);
 cudaError_t launch_ckpt8(const Ckpt8Params &p, bool unpack, bool bf16, cudaStream_t stream);

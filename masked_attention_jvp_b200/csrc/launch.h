@@ -16,6 +16,14 @@ __device__ __forceinline__ void begin_after_previous() {
 }
 #endif
 
+// For a kernel that reads nothing of the one before it on the stream, only what was there
+// before that one (which began by begin_after_previous, so all of it is in place): in place of
+// begin_after_previous, last in one block. The grid then ends after its predecessor's end,
+// which is what the next kernel's wait relies on.
+#ifdef __CUDACC__
+__device__ __forceinline__ void end_after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+#endif
+
 template <typename... Params, typename... Args>
 cudaError_t launch_in_order(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
                             const Args &...args) {

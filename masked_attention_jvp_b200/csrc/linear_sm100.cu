@@ -722,7 +722,8 @@ constexpr int kDzUnroll = 2;
 template <int ACT>
 __global__ void __launch_bounds__(256, 4) linear_dz_kernel(const LinearDzParams p) {
   __shared__ float red[8][256];
-  begin_after_previous();
+  const bool late = ACT == lin::kActNone && p.late;
+  if (!late) begin_after_previous();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int32_t col = int32_t(blockIdx.x) * 256 + 8 * lane;
   const int64_t r0 = int64_t(blockIdx.y) * p.chunk_rows;
@@ -791,17 +792,20 @@ __global__ void __launch_bounds__(256, 4) linear_dz_kernel(const LinearDzParams 
   for (int i = 0; i < 4; ++i) f2_split(sum[i], red[warp][8 * lane + 2 * i], red[warp][8 * lane + 2 * i + 1]);
   __syncthreads();
   const int32_t out = int32_t(blockIdx.x) * 256 + int32_t(threadIdx.x);
-  if (out >= p.C) return;
-  float s = 0.f;
+  if (out < p.C) {
+    float s = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) s += red[i][threadIdx.x];
-  p.partial[size_t(blockIdx.y) * p.C + out] = s;
+    for (int i = 0; i < 8; ++i) s += red[i][threadIdx.x];
+    p.partial[size_t(blockIdx.y) * p.C + out] = s;
+  }
+  if (late && blockIdx.x == 0 && blockIdx.y == 0) end_after_previous();
 }
 
 // Sums the chunks' columns in a fixed order: 8 slices of the chunks, then the slices.
-__global__ void __launch_bounds__(256) column_sum_kernel(const float *part, int32_t chunks, int32_t C, float *out) {
+__global__ void __launch_bounds__(256) column_sum_kernel(const float *part, int32_t chunks, int32_t C, float *out,
+                                                         bool late) {
   __shared__ float s[8][32];
-  begin_after_previous();
+  if (!late) begin_after_previous();
   const int32_t c = int32_t(blockIdx.x) * 32 + int32_t(threadIdx.x & 31), slice = int32_t(threadIdx.x >> 5);
   float acc = 0.f;
   if (c < C) {
@@ -815,6 +819,7 @@ __global__ void __launch_bounds__(256) column_sum_kernel(const float *part, int3
     for (int i = 1; i < 8; ++i) acc += s[i][threadIdx.x & 31];
     out[c] = acc;
   }
+  if (late && blockIdx.x == 0) end_after_previous();
 }
 
 template <bool JVP, bool GRADS, int TN>
@@ -893,8 +898,9 @@ cudaError_t launch_linear_fwd(const LinearParams &p, cudaStream_t stream) {
   return p.tx ? launch_fwd_tiles<true>(p, stream) : launch_fwd_tiles<false>(p, stream);
 }
 
-cudaError_t launch_linear_grads(const LinearParams &p, cudaStream_t stream) {
+cudaError_t launch_linear_grads(const LinearParams &p, const LinearDzParams *sums, cudaStream_t stream) {
   cudaError_t e = p.tile_cols == 128 ? launch_tiles<false, true, 128>(p, stream) : launch_tiles<false, true, 256>(p, stream);
+  if (e == cudaSuccess && sums) e = launch_linear_dz(*sums, stream);
   if (e == cudaSuccess) e = finish<false, false>(p, stream);
   if (e != cudaSuccess) return e;
   LinearParams dw = p;
@@ -910,15 +916,17 @@ int32_t linear_dz_chunk_rows(int64_t M, int32_t C) {
   const int64_t rows = (M + want - 1) / want;
   return int32_t(rows < 32 ? 32 : (rows + 31) & ~int64_t(31));
 }
-cudaError_t launch_linear_dz(const LinearDzParams &p, float *db, cudaStream_t stream) {
+cudaError_t launch_linear_dz(const LinearDzParams &p, cudaStream_t stream) {
   const int64_t chunks = (p.M + p.chunk_rows - 1) / p.chunk_rows;
   const dim3 grid(unsigned((p.C + 255) / 256), unsigned(chunks));
   void (*const kernels[4])(LinearDzParams) = {linear_dz_kernel<lin::kActNone>, linear_dz_kernel<lin::kActGeluTanh>,
                                               linear_dz_kernel<lin::kActGelu>, linear_dz_kernel<lin::kActSilu>};
-  const cudaError_t e = launch_in_order(kernels[p.act], grid, 256, 0, stream, p);
-  if (e != cudaSuccess || !db) return e;
+  return launch_in_order(kernels[p.act], grid, 256, 0, stream, p);
+}
+cudaError_t launch_linear_db(const LinearDzParams &p, float *db, bool late, cudaStream_t stream) {
   return launch_in_order(column_sum_kernel, dim3(unsigned((p.C + 31) / 32)), 256, 0, stream,
-                         static_cast<const float *>(p.partial), int32_t(chunks), p.C, db);
+                         static_cast<const float *>(p.partial), int32_t((p.M + p.chunk_rows - 1) / p.chunk_rows), p.C,
+                         db, late);
 }
 
 cudaError_t read_and_clear_linear_error(uint32_t *out) {

@@ -310,3 +310,48 @@ def test_outputs_past_32_bits():
 def test_sizes_of_every_tile_width(M, K, C, tangent):
     """A frame's worth of rows, where the width of the tiles is chosen by their number."""
     run_fwd(M, K, C, "gelu_tanh", True, True, tangent, True, seed=9)
+
+
+@pytest.mark.parametrize("act", ["none", "silu"])
+@pytest.mark.parametrize("M,K,C", [(64, 256, 512), (700, 512, 2568), (1560, 1536, 1536)])
+def test_bias_gradients_back_to_back(M, K, C, act):
+    """The bias's sums run beside the products: calls in a row, each on what the one before left
+    and with its inputs overwritten at once, give what the same calls give one at a time."""
+    g = torch.Generator().manual_seed(M)
+    dys = [rnd(g, M, C).cuda() for _ in range(4)]
+    x, w = rnd(g, M, K).cuda(), rnd(g, C, K, std=K ** -0.5).cuda()
+    pre = caj.ckpt8_pack(rnd(g, M, C).cuda()) if act != "none" else None
+
+    def run(alone):
+        dy, outs = torch.empty_like(dys[0]), []
+        for d in dys:
+            dy.copy_(d)
+            dx, dw, db = caj.linear_act_bwd(dy, x, w, act=act, pre=pre)
+            if alone:
+                torch.cuda.synchronize()
+            # the library's own kernel reads dx right behind, its predecessor's inputs change
+            y, _, _ = caj.linear_act_fwd(dx, w)
+            again = caj.linear_act_bwd(y, x, w, act=act, pre=pre)
+            dy.zero_()
+            outs += [dx, dw, db, *again]
+            if alone:
+                torch.cuda.synchronize()
+        return outs
+
+    want, got = run(True), run(False)
+    torch.cuda.synchronize()
+    for a, b in zip(want, got):
+        assert torch.equal(a, b)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = run(False)
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(want, got):
+        assert torch.equal(a, b)
+    # the sums themselves: fp32 over M rows, off by at most M steps of the sum of magnitudes
+    if act == "none":
+        for i, d in enumerate(dys):
+            d = d.double()
+            assert bool(((want[6 * i + 2] - d.sum(0)).abs() <= M * 2.0**-24 * d.abs().sum(0)).all())
