@@ -173,7 +173,7 @@ caj_status caj_qk_rope_bwd_workspace(const caj_qk_rope_shape *shape, size_t *byt
   if (st != CAJ_OK) return st;
   *bytes = 0;
   if (shape->norm != CAJ_NORM_NONE) {
-    const size_t blocks = size_t(caj::qk_rope_bwd_blocks(shape->B, shape->N, shape->Hq, shape->Hk, shape->D));
+    const size_t blocks = size_t(caj::qk_rope_bwd_blocks(shape->B, shape->N, shape->Hq, shape->Hk, shape->D, shape->norm));
     *bytes = blocks * (rope_gain_len(shape, shape->Hq) + rope_gain_len(shape, shape->Hk)) * sizeof(float);
   }
   return CAJ_OK;
@@ -218,7 +218,7 @@ caj_status caj_qk_rope_bwd(const void *dq, const void *dk, const void *dv, const
   if (need && (!workspace || !aligned_to(workspace, 16) || workspace_bytes < need)) return CAJ_ERR_INVALID_ARG;
   st = caj::check_device();
   if (st != CAJ_OK) return st;
-  p.blocks = caj::qk_rope_bwd_blocks(shape->B, shape->N, shape->Hq, shape->Hk, shape->D);
+  p.blocks = caj::qk_rope_bwd_blocks(shape->B, shape->N, shape->Hq, shape->Hk, shape->D, shape->norm);
   if (normed) {
     p.partial[0] = static_cast<float *>(workspace);
     p.partial[1] = p.partial[0] + size_t(p.blocks) * rope_gain_len(shape, shape->Hq);

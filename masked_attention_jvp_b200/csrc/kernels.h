@@ -183,8 +183,10 @@ struct QkRopeParams {
   const float *cos, *sin;      // [N, P]
   int32_t B, N, Hq, Hk, D, P;
   float eps;
-  int32_t norm, half, gain_full, blocks;
-  int32_t ring, angle_slots;   // backward: tokens in a thread's ring of copies, slots for angles (set by the launch)
+  int32_t norm, half, gain_full;
+  int32_t blocks;              // backward: all blocks, those of every share of the heads
+  // backward, set by the launch: heads a block has, tokens in a thread's ring of copies, slots for angles
+  int32_t share_heads, ring, angle_slots;
 };
 
 // Matrix products of the linear operators; the operands' maps have 128-byte-swizzled
@@ -272,7 +274,7 @@ cudaError_t read_and_clear_bwd_error(uint32_t *out);
 cudaError_t launch_rope_table(const RopeTableParams &p, bool pos64, cudaStream_t stream);
 cudaError_t launch_qk_rope_fwd(const QkRopeParams &p, bool bf16, cudaStream_t stream);
 cudaError_t launch_qk_rope_bwd(const QkRopeParams &p, bool bf16, cudaStream_t stream);
-int32_t qk_rope_bwd_blocks(int32_t B, int32_t N, int32_t Hq, int32_t Hk, int32_t D);
+int32_t qk_rope_bwd_blocks(int32_t B, int32_t N, int32_t Hq, int32_t Hk, int32_t D, int32_t norm);
 cudaError_t launch_linear_fwd(const LinearParams &p, cudaStream_t stream);
 // `sums`: column sums alone (late), to run beside the products
 cudaError_t launch_linear_grads(const LinearParams &p, const LinearDzParams *sums, cudaStream_t stream);

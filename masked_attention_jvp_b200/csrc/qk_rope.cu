@@ -156,12 +156,12 @@ __global__ void __launch_bounds__(256, kTableBlocks) rope_table_kernel(const Rop
 
 // ------------------------------------------------------------ norm + rotation
 struct Lane {        // a thread's place: eight channels of one head, one token of T
-  int32_t V, T;      // vectors of a token (of the wider tensor), tokens of a block
+  int32_t V, T;      // vectors of a token (of the wider tensor, or a share of it), tokens of a block
   int32_t t, vec, head, d0;
 };
-__device__ __forceinline__ Lane lane_of(const QkRopeParams &p) {
+__device__ __forceinline__ Lane lane_of(const QkRopeParams &p, int32_t heads) {
   Lane l;
-  l.V = max(p.Hq, p.Hk) * p.D / 8;
+  l.V = heads * p.D / 8;
   l.T = int32_t(blockDim.x) / l.V;
   l.t = int32_t(threadIdx.x) / l.V;
   l.vec = int32_t(threadIdx.x) - l.t * l.V;
@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 3 : 1) qk_rope_fwd_kernel(
   extern __shared__ __align__(16) float red[];
   begin_after_previous();
   constexpr int U = fwd_tokens<T, TAN>();
-  const Lane l = lane_of(p);
+  const Lane l = lane_of(p, max(p.Hq, p.Hk));
   const int32_t heads[3] = {p.Hq, p.Hk, p.x[2] ? p.Hk : 0};
   const bool turns = l.d0 < 2 * p.P;
   v8::Raw<T> raw[U][3], traw[U][3];
@@ -442,7 +442,7 @@ constexpr int bwd_slots() {
 // 320 and 332, so it keeps its own.)
 int32_t bwd_angle_slots(const QkRopeParams &p, bool shared) { return shared ? (p.P / 2 + 31) / 32 : p.half ? 4 : 2; }
 
-// Each of p.blocks blocks walks over a run of neighbouring tokens, T at a time, so the
+// Each block (blockIdx.x) walks over a run of neighbouring tokens, T at a time, so the
 // gains' gradient stays in registers for the whole run and addresses only step on; block
 // i leaves its partial dg in p.partial[q or k][i]. What a token needs comes through a
 // ring of asynchronous copies, up to two tokens ahead: with plain loads the kernel waited
@@ -456,7 +456,10 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) qk_rope_bwd_kernel(
   constexpr int kAngles = bwd_slots<T, CK>();  // the angles' first slot
   const int kSlots = kAngles + (SHARED ? p.angle_slots : Rot::kSlots);
   float *red = reinterpret_cast<float *>(smem + size_t(p.ring) * kSlots * 16 * blockDim.x);
-  const Lane l = lane_of(p);
+  Lane l = lane_of(p, p.share_heads);
+  const int32_t head0 = int32_t(blockIdx.y) * p.share_heads;
+  l.vec += head0 * p.D / 8;
+  l.head += head0;
   const int32_t rows = p.B * p.N, stride = 16 * int32_t(blockDim.x);
   const uint32_t mine = ptx::smem_u32(smem) + 16 * threadIdx.x;
   const int32_t heads[3] = {p.Hq, p.Hk, p.dy[2] ? p.Hk : 0};
@@ -471,7 +474,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) qk_rope_bwd_kernel(
   }
 
   // this thread's tokens: tok0, tok0 + T, ... below end
-  const int32_t rounds = (rows + p.blocks * l.T - 1) / (p.blocks * l.T);
+  const int32_t walkers = int32_t(gridDim.x), rounds = (rows + walkers * l.T - 1) / (walkers * l.T);
   const uint32_t tok0 = uint32_t(int64_t(blockIdx.x) * rounds * l.T + l.t);
   const uint32_t end = uint32_t(min(int64_t(rows), (int64_t(blockIdx.x) + 1) * rounds * l.T));
   // A place in the walk: the token, its position, and where its sequence begins in the
@@ -507,7 +510,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) qk_rope_bwd_kernel(
   };
   // elements of (b, head, n, d0), and of a token's vector in rows of `ld`
   auto head_row = [&](const Walk &w, int i) {
-    return (MAXT == 256 ? w.head_at[i] : sequence_at(w, i)) + int64_t(w.n) * p.D;
+    return (MAXT <= 512 ? w.head_at[i] : sequence_at(w, i)) + int64_t(w.n) * p.D;
   };
   auto token_row = [&](const Walk &w, int32_t ld) { return int64_t(uint64_t(w.tok) * uint32_t(ld)) + 8 * l.vec; };
   auto fetch = [&](const Walk &w, uint32_t slot0) {
@@ -638,8 +641,10 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) qk_rope_bwd_kernel(
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
   if (!normed) return;
-  // this block's dg: over its T tokens a round, and over the heads where they share a gain
+  // this block's dg: over its T tokens a round, and over its heads where they share a gain
+  // (else only the columns of its share)
   float *sum = reinterpret_cast<float *>(smem);
+  const int32_t first = head0 * p.D / 8;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     __syncthreads();
@@ -647,31 +652,36 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) qk_rope_bwd_kernel(
       float f[8];
       singles_of(dg[i], f);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) sum[(l.t * l.V + l.vec) * 8 + j] = f[j];
+      for (int j = 0; j < 8; ++j) sum[(l.t * l.V + l.vec - first) * 8 + j] = f[j];
     }
     __syncthreads();
-    const int32_t width = heads[i] * p.D, len = p.gain_full ? width : p.D;
-    float *part = p.partial[i] + size_t(blockIdx.x) * len;
-    for (int32_t c = int32_t(threadIdx.x); c < len; c += int32_t(blockDim.x)) {
+    const int32_t width = max(0, min(heads[i] - head0, p.share_heads)) * p.D;
+    const int32_t len = p.gain_full ? heads[i] * p.D : p.D, step = p.gain_full ? width : p.D;
+    float *part = p.partial[i] + size_t(blockIdx.y * gridDim.x + blockIdx.x) * len + (p.gain_full ? 8 * first : 0);
+    for (int32_t c = int32_t(threadIdx.x); c < step; c += int32_t(blockDim.x)) {
       float s = 0.f;
       for (int32_t t = 0; t < l.T; ++t)
-        for (int32_t k = c; k < width; k += len) s += sum[t * l.V * 8 + k];
+        for (int32_t k = c; k < width; k += step) s += sum[t * l.V * 8 + k];
       part[c] = s;
     }
   }
 }
 
-// Sums the blocks' partial dg in a fixed order: 8 slices of the blocks, then the slices.
+// Sums the blocks' partial dg in a fixed order: 8 slices of the blocks, then the slices. A
+// gain of every channel is the matter of one share's blocks.
 __global__ void __launch_bounds__(256) gain_grad_kernel(const QkRopeParams p) {
   __shared__ float s[8][32];
   begin_after_previous();
   const int which = blockIdx.y;
   const int32_t len = p.gain_full ? (which ? p.Hk : p.Hq) * p.D : p.D;
   const int32_t c = int32_t(blockIdx.x) * 32 + int32_t(threadIdx.x & 31), slice = int32_t(threadIdx.x >> 5);
+  const int32_t heads = max(p.Hq, p.Hk), shares = (heads + p.share_heads - 1) / p.share_heads;
+  const int32_t blocks = p.gain_full ? p.blocks / shares : p.blocks;
+  const float *part = p.partial[which] + (p.gain_full ? size_t(c / (p.share_heads * p.D)) * blocks * len : 0) + c;
   float acc = 0.f;
   if (c < len) {
 #pragma unroll 8
-    for (int32_t b = slice; b < p.blocks; b += 8) acc += p.partial[which][size_t(b) * len + c];
+    for (int32_t b = slice; b < blocks; b += 8) acc += part[size_t(b) * len];
   }
   s[slice][threadIdx.x & 31] = acc;
   __syncthreads();
@@ -682,36 +692,43 @@ __global__ void __launch_bounds__(256) gain_grad_kernel(const QkRopeParams p) {
   }
 }
 
-// Threads of a block: whole tokens of the wider tensor, near 256.
-int32_t threads_for(const QkRopeParams &p) {
-  const int32_t V = (p.Hq > p.Hk ? p.Hq : p.Hk) * p.D / 8;
+// Threads of a block: whole tokens of V vectors, near 256.
+int32_t threads_for(int32_t V) {
   const int32_t t = V >= 256 ? 1 : 256 / V;
   return (V * t + 31) & ~31;
+}
+int32_t vectors(const QkRopeParams &p) { return (p.Hq > p.Hk ? p.Hq : p.Hk) * p.D / 8; }  // of the wider tensor
+int64_t groups_for(const QkRopeParams &p, int32_t V) {  // blocks that hold all tokens, T each
+  const int32_t T = threads_for(V) / V;
+  return (int64_t(p.B) * p.N + T - 1) / T;
+}
+size_t token_norm_bytes(const QkRopeParams &p, int32_t values) {  // group_sums' shared memory
+  return p.norm == kNormToken ? size_t(threads_for(vectors(p))) / (p.D / 8) * values * sizeof(float) : 0;
 }
 
 // Blocks of the backward that an SM holds (registers: 512 threads).
 int32_t qk_rope_resident(int32_t threads) { return threads >= 512 ? 1 : 512 / threads; }
-int32_t vectors(const QkRopeParams &p) { return (p.Hq > p.Hk ? p.Hq : p.Hk) * p.D / 8; }
-int64_t groups_for(const QkRopeParams &p) {  // blocks that hold all tokens, T each
-  const int32_t T = threads_for(p) / vectors(p);
-  return (int64_t(p.B) * p.N + T - 1) / T;
-}
-size_t token_norm_bytes(const QkRopeParams &p, int32_t values) {  // group_sums' shared memory
-  return p.norm == kNormToken ? size_t(threads_for(p)) / (p.D / 8) * values * sizeof(float) : 0;
+// Heads of the backward's blocks: all of a token's, or, where that is more than 512 threads
+// and heads are normalised each by itself, equal shares (128 registers a thread instead of
+// 80 or 64, at which it spills; 16384 tokens of 40 x 128: @40@, of 64 query and 8 key
+// heads @64@).
+int32_t share_heads(const QkRopeParams &p) {
+  const int32_t heads = p.Hq > p.Hk ? p.Hq : p.Hk, shares = p.norm == kNormToken ? 1 : (vectors(p) + 511) / 512;
+  return (heads + shares - 1) / shares;
 }
 
 template <typename T, bool TAN, int MAXT>
 cudaError_t launch_fwd(const QkRopeParams &p, cudaStream_t stream) {
-  const int32_t threads = threads_for(p);
+  const int32_t threads = threads_for(vectors(p));
   constexpr int U = fwd_tokens<T, TAN>();
-  const unsigned grid = unsigned((groups_for(p) + U - 1) / U);
+  const unsigned grid = unsigned((groups_for(p, vectors(p)) + U - 1) / U);
   const size_t smem = token_norm_bytes(p, TAN ? 4 : 2);
   return launch_in_order(p.half ? qk_rope_fwd_kernel<T, TAN, true, MAXT> : qk_rope_fwd_kernel<T, TAN, false, MAXT>,
                          dim3(grid), threads, smem, stream, p);
 }
 template <typename T>
 cudaError_t launch_fwd(const QkRopeParams &p, cudaStream_t stream) {
-  if (threads_for(p) <= 256) return p.tx[0] ? launch_fwd<T, true, 256>(p, stream) : launch_fwd<T, false, 256>(p, stream);
+  if (threads_for(vectors(p)) <= 256) return p.tx[0] ? launch_fwd<T, true, 256>(p, stream) : launch_fwd<T, false, 256>(p, stream);
   return p.tx[0] ? launch_fwd<T, true, 1024>(p, stream) : launch_fwd<T, false, 1024>(p, stream);
 }
 
@@ -719,7 +736,7 @@ template <typename T, bool CK, bool HALF, bool SHARED, int MAXT>
 cudaError_t launch_bwd(const QkRopeParams &params, cudaStream_t stream) {
   auto kernel = qk_rope_bwd_kernel<T, CK, HALF, SHARED, MAXT>;
   QkRopeParams p = params;
-  const int32_t threads = threads_for(p);
+  const int32_t threads = threads_for(p.share_heads * p.D / 8);
   p.angle_slots = bwd_angle_slots(p, SHARED);
   const size_t token = size_t(bwd_slots<T, CK>() + p.angle_slots) * 16 * threads, extra = token_norm_bytes(p, 4);
   // the deepest ring with which the blocks that the grid counts on fit an SM (228 KB, 1 KB
@@ -732,7 +749,8 @@ cudaError_t launch_bwd(const QkRopeParams &params, cudaStream_t stream) {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kMaxSmem));
   });
   if (e != cudaSuccess) return e;
-  e = launch_in_order(kernel, dim3(unsigned(p.blocks)), threads, p.ring * token + extra, stream, p);
+  const int32_t heads = p.Hq > p.Hk ? p.Hq : p.Hk, shares = (heads + p.share_heads - 1) / p.share_heads;
+  e = launch_in_order(kernel, dim3(unsigned(p.blocks / shares), unsigned(shares)), threads, p.ring * token + extra, stream, p);
   if (e != cudaSuccess || p.norm == kNormNone) return e;
   const int32_t len = p.gain_full ? vectors(p) * 8 : p.D;
   return launch_in_order(gain_grad_kernel, dim3(unsigned((len + 31) / 32), 2), 256, 0, stream, p);
@@ -740,12 +758,18 @@ cudaError_t launch_bwd(const QkRopeParams &params, cudaStream_t stream) {
 template <typename T, bool CK, int MAXT>
 cudaError_t launch_bwd(const QkRopeParams &p, cudaStream_t stream) {
   if (!p.half) return launch_bwd<T, CK, false, false, MAXT>(p, stream);
-  return vectors(p) % 32 == 0 ? launch_bwd<T, CK, true, true, MAXT>(p, stream)
-                              : launch_bwd<T, CK, true, false, MAXT>(p, stream);
+  return p.share_heads * p.D % 256 == 0 ? launch_bwd<T, CK, true, true, MAXT>(p, stream)
+                                        : launch_bwd<T, CK, true, false, MAXT>(p, stream);
 }
 template <typename T, bool CK>
-cudaError_t launch_bwd(const QkRopeParams &p, cudaStream_t stream) {
-  return threads_for(p) <= 256 ? launch_bwd<T, CK, 256>(p, stream) : launch_bwd<T, CK, 1024>(p, stream);
+cudaError_t launch_bwd(const QkRopeParams &params, cudaStream_t stream) {
+  QkRopeParams p = params;
+  p.share_heads = share_heads(p);
+  const int32_t threads = threads_for(p.share_heads * p.D / 8);
+  return threads <= 256   ? launch_bwd<T, CK, 256>(p, stream)
+         : threads <= 512 ? launch_bwd<T, CK, 512>(p, stream)
+         : threads <= 768 ? launch_bwd<T, CK, 768>(p, stream)
+                          : launch_bwd<T, CK, 1024>(p, stream);
 }
 
 }  // namespace
@@ -771,15 +795,17 @@ cudaError_t launch_rope_table(const RopeTableParams &p, bool pos64, cudaStream_t
 
 // Blocks of the backward: fixed by the sizes alone, so that the order of the gains'
 // sums is too. About as many as are resident on 148 SMs at once.
-int32_t qk_rope_bwd_blocks(int32_t B, int32_t N, int32_t Hq, int32_t Hk, int32_t D) {
+int32_t qk_rope_bwd_blocks(int32_t B, int32_t N, int32_t Hq, int32_t Hk, int32_t D, int32_t norm) {
   QkRopeParams p{};
   p.B = B;
   p.N = N;
   p.Hq = Hq;
   p.Hk = Hk;
   p.D = D;
-  const int64_t groups = groups_for(p), most = 148 * int64_t(qk_rope_resident(threads_for(p)));
-  return int32_t(groups < most ? groups : most);
+  p.norm = norm;
+  const int32_t heads = Hq > Hk ? Hq : Hk, own = share_heads(p), shares = (heads + own - 1) / own, V = own * D / 8;
+  const int64_t groups = groups_for(p, V), most = 148 * int64_t(qk_rope_resident(threads_for(V))) / shares;
+  return shares * int32_t(groups < most ? groups : most);
 }
 
 cudaError_t launch_qk_rope_fwd(const QkRopeParams &p, bool bf16, cudaStream_t stream) {

@@ -232,6 +232,28 @@ def test_norm_rope_backward(case, kept):
         assert a is None and b is None or torch.equal(a, b)  # the same sums in the same order
 
 
+WIDE = [  # tokens whose heads are shared out between blocks, and those next to them
+    (1, 700, 40, 40, 128, 64, "head", "interleaved", BF, False),
+    (2, 301, 64, 8, 128, 64, "head", "half", BF, False),      # the second share has no key heads
+    (1, 160, 33, 33, 128, 32, "head", "half", BF, True),      # shares of 17 and 16 heads
+    (1, 450, 8, 48, 128, 64, "head", "half", F32, True),
+    (3, 90, 127, 5, 64, 32, "head", "interleaved", F32, False),
+    (1, 40, 32, 9, 256, 24, "none", "half", BF, False),
+    (1, 333, 32, 8, 128, 64, "head", "half", BF, False),      # one block a token, 512 threads
+    (1, 300, 20, 20, 128, 64, "head", "interleaved", BF, True),
+    (1, 200, 48, 8, 128, 64, "token", "half", BF, True),      # a token's mean: no shares
+    (1, 1, 64, 64, 128, 64, "head", "half", BF, True),
+]
+
+
+@pytest.mark.parametrize("case", WIDE)
+def test_norm_rope_wide_tokens(case):
+    test_norm_rope_forward_and_tangent(case)
+    test_norm_rope_backward(case, "tensor")
+    if case[6] != "none":
+        test_norm_rope_backward(case, "ckpt8")
+
+
 def test_norm_rope_fused_projection_slices():
     case = CASES[1]
     B, N, H, Hk, D, P, norm, layout, dtype, full = case
