@@ -416,7 +416,7 @@ caj_status caj_ckpt_unpack(const int8_t *codes, const uint8_t *scales, int64_t r
  *        freq   [pairs] fp64, radians per position; |pos * freq| < 2^50
  *        axis   [pairs] int32, which column of pos turns pair i; null: column 0.
  *               A pair whose axis is not in [0, axes) gets NaN.
- *        mscale |mscale| < 2^126
+ *        mscale |mscale| < 2^126;  axes, pairs at most 2^28
  *   out: cos, sin [N, pairs] fp32
  * The angle is reduced in 64 bits, with the rest of freq * 2/pi carried along, so
  * far positions are as exact as near ones. Scaled frequencies

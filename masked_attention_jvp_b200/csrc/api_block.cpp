@@ -114,7 +114,7 @@ caj_status caj_rope_table(const void *pos, int32_t pos64, const double *freq, co
   if (!pos || !aligned_to(pos, pos64 ? 8 : 4) || !freq || !aligned_to(freq, 8)) return CAJ_ERR_INVALID_ARG;
   if (axis && !aligned_to(axis, 4)) return CAJ_ERR_INVALID_ARG;
   if (!cos || !sin || !aligned_to(cos, 4) || !aligned_to(sin, 4)) return CAJ_ERR_INVALID_ARG;
-  if (N > (int64_t(1) << 40) / pairs) return CAJ_ERR_UNSUPPORTED;
+  if (N > (int64_t(1) << 40) / pairs || axes > (1 << 28) || pairs > (1 << 28)) return CAJ_ERR_UNSUPPORTED;
   const caj_status st = caj::check_device();
   if (st != CAJ_OK) return st;
   caj::RopeTableParams p{};

@@ -19,6 +19,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "ckpt8.cuh"
 #include "kernels.h"
@@ -95,41 +96,48 @@ __device__ __forceinline__ void sin_cos_pair(const TurnSeries &k, uint64_t f, ui
   cs = add2(fma2(f_f, cs, twice(k.c0_rest)), twice(k.c0));
 }
 
-// A thread owns V neighbouring pairs (V = 4: 16-byte stores) and walks over the positions, so
-// turns and axes stay in registers; the next position is on its way meanwhile. Written once
-// (8 bytes a pair): 131072 x 64 take 13.8 us of 10.4 that the stores alone would (four blocks
-// an SM, 64 registers; five at 48 registers 17.3; 8 pairs a thread at two blocks 13.1, but
-// with 32-byte rows). With the reduction in radians, seven 64-bit operations a pair
-// instead of four, and scalar series it took 16.7.
+// A thread owns V neighbouring places of a block of R rows and walks over such blocks, so
+// turns and axes stay in registers; the next position is on its way meanwhile. V = 4 gives
+// 16-byte stores: of one row where P is a multiple of 4, else of four, where a thread's places
+// may lie in two of them. Written once (8 bytes a pair): 131072 x 64 take 13.7 us of 10.4 that
+// the stores alone would (15.4 as blocks of four rows; four blocks an SM, 64 registers; five
+// at 48 registers 17.3; 8 pairs a thread at two blocks 13.1, but with 32-byte rows), and
+// 131072 x 61 18.2 (25.0 with V = 1, which is left to tables that are not 16-byte aligned).
+// With the reduction in radians, seven 64-bit operations a pair instead of four, and scalar
+// series 131072 x 64 took 16.7.
 constexpr int kTableBlocks = 4;
-template <typename I, int V>
+template <typename I, int V, int R>
 __global__ void __launch_bounds__(256, kTableBlocks) rope_table_kernel(const RopeTableParams p, const TurnSeries series) {
   begin_after_previous();
-  const int32_t cols = p.P / V;  // threads across a row of pairs
   const int64_t id = int64_t(blockIdx.x) * 256 + threadIdx.x;
-  const int64_t row0 = id / cols, step = int64_t(gridDim.x) * 256 / cols;  // a whole number of rows
-  const int32_t i = int32_t(id - row0 * cols) * V;
+  const int32_t cols = R == V ? p.P : p.P / V;  // threads of a block of rows
+  const int64_t first = id / cols, step = int64_t(gridDim.x) * 256 / cols;  // a whole number of such blocks
+  const int32_t place = int32_t(id - first * cols) * V;
   double turn[V], rest[V];
-  int32_t ax[V];
+  int32_t row[V], from[V];  // row of the block; element of its positions
 #pragma unroll
   for (int e = 0; e < V; ++e) {
-    double freq = __ldg(p.freq + i + e);
-    ax[e] = p.axis ? __ldg(p.axis + i + e) : 0;
-    if (ax[e] < 0 || ax[e] >= p.A) freq = __longlong_as_double(0x7FF8000000000000ll), ax[e] = 0;  // NaN
+    row[e] = R > 1 ? (place + e) / p.P : 0;
+    const int32_t i = place + e - row[e] * p.P;
+    double freq = __ldg(p.freq + i);
+    int32_t ax = p.axis ? __ldg(p.axis + i) : 0;
+    if (ax < 0 || ax >= p.A) freq = __longlong_as_double(0x7FF8000000000000ll), ax = 0;  // NaN
+    from[e] = row[e] * p.A + ax;
     turn[e] = __dmul_rn(freq, 0.6366197723675814);  // 2/pi, leading 53 bits
     rest[e] = __fma_rn(freq, -3.935735335036497e-17, __fma_rn(freq, 0.6366197723675814, -turn[e]));  // and the next
   }
-  const I *at_pos = static_cast<const I *>(p.pos);
-  I next = row0 < p.N ? __ldg(at_pos + row0 * p.A + ax[0]) : I(0);
-  for (int64_t n = row0; n < p.N; n += step) {
-    const I *row = at_pos + n * p.A;
+  const I *positions = static_cast<const I *>(p.pos);
+  I next = R * first + row[0] < p.N ? __ldg(positions + R * first * p.A + from[0]) : I(0);
+  for (int64_t n = R * first; n + row[0] < p.N; n += R * step) {
+    const I *here = positions + n * p.A;
     double pos = double(next);
-    if (n + step < p.N) next = __ldg(row + step * p.A + ax[0]);
+    if (n + R * step + row[0] < p.N) next = __ldg(here + R * step * p.A + from[0]);
+    const bool whole = R == 1 || n + row[V - 1] < p.N;
     float f[V], c[V], s[V];
     int quadrant[V];
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-      if (e && ax[e] != ax[e - 1]) pos = double(__ldg(row + ax[e]));  // neighbouring pairs mostly share their axis
+    for (int e = 0; e < V; ++e) {  // neighbouring places mostly share their position
+      if (e && from[e] != from[e - 1]) pos = whole || n + row[e] < p.N ? double(__ldg(here + from[e])) : 0.;
       f[e] = quarter_turns(pos, turn[e], rest[e], quadrant[e]);
     }
 #pragma unroll
@@ -143,13 +151,17 @@ __global__ void __launch_bounds__(256, kTableBlocks) rope_table_kernel(const Rop
       turned(s0, c0, quadrant[e], s[e], c[e]);
       if (kNext) turned(s1, c1, quadrant[e + kNext], s[e + kNext], c[e + kNext]);
     }
-    const int64_t at = n * p.P + i;
-    if constexpr (V == 4) {
-      __stcs(reinterpret_cast<float4 *>(p.cos + at), make_float4(c[0], c[1], c[2], c[3]));
-      __stcs(reinterpret_cast<float4 *>(p.sin + at), make_float4(s[0], s[1], s[2], s[3]));
+    const int64_t at = n * p.P + place;
+    if (V == 4 && whole) {
+      __stcs(reinterpret_cast<float4 *>(p.cos + at), make_float4(c[0], c[V / 4], c[V / 2], c[V - 1]));
+      __stcs(reinterpret_cast<float4 *>(p.sin + at), make_float4(s[0], s[V / 4], s[V / 2], s[V - 1]));
     } else {
-      p.cos[at] = c[0];
-      p.sin[at] = s[0];
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        if (n + row[e] >= p.N) break;
+        p.cos[at + e] = c[e];
+        p.sin[at + e] = s[e];
+      }
     }
   }
 }
@@ -446,7 +458,10 @@ int32_t bwd_angle_slots(const QkRopeParams &p, bool shared) { return shared ? (p
 // gains' gradient stays in registers for the whole run and addresses only step on; block
 // i leaves its partial dg in p.partial[q or k][i]. What a token needs comes through a
 // ring of asynchronous copies, up to two tokens ahead: with plain loads the kernel waited
-// for memory half of its time. CK: xq and xk are 8-bit checkpoints.
+// for memory half of its time. CK: xq and xk are 8-bit checkpoints. MAXT: 256 and 512 threads
+// leave 128 registers each at 512 threads an SM; a token's mean over more channels needs up
+// to 768 or 1024 threads, at 80 or 64 (24 x 128 channels: 156 us for 16384 tokens with 128
+// registers, 559 with 64).
 template <typename T, bool CK, bool HALF, bool SHARED, int MAXT>
 __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) qk_rope_bwd_kernel(const QkRopeParams p) {
   extern __shared__ __align__(16) uint8_t smem[];
@@ -554,91 +569,101 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) qk_rope_bwd_kernel(
   }
   const float inv_len[2] = {1.f / float(p.norm == kNormHead ? p.D : heads[0] * p.D),
                             1.f / float(p.norm == kNormHead ? p.D : heads[1] * p.D)};
-  int at = 0, to = p.ring - 1;  // ring positions
-  for (int32_t round = 0; round < rounds; ++round) {
-    if (SHARED) __syncwarp();  // every lane has read what the next copies replace
-    fetch(next, mine + to * kSlots * stride);
-    advance(next);
-    const uint32_t slot0 = mine + at * kSlots * stride;
-    const bool here = now.tok < end;
-    const bool on[3] = {here && has[0], here && has[1], here && has[2]};
-    v8::Raw<T> dv = v8::zero<T>();
-    if (on[2]) dv = v8::load(static_cast<const T *>(p.dy[2]) + head_row(now, 1));
-    if (p.ring == 3)
-      asm volatile("cp.async.wait_group 2;" ::: "memory");
-    else if (p.ring == 2)
-      asm volatile("cp.async.wait_group 1;" ::: "memory");
-    else
-      asm volatile("cp.async.wait_group 0;" ::: "memory");
-    // (slots of tokens or heads that are not there hold anything: nothing below lets it
-    // past the `on` conditions, and a head's lanes are all there or all not)
-    Rot turn;
-    turn.rest();
-    if (SHARED) __syncwarp();  // the other lanes' copies have landed too
-    if (turns) {
+  // kTensors: q and k, or q alone for warps none of whose lanes has a head of k (16384 tokens
+  // of 32 query and 8 key heads: 208 to 192 us). A token's mean joins all warps at barriers, so
+  // there they all take the same way.
+  auto walk = [&](auto tensors) {
+    constexpr int kTensors = decltype(tensors)::value;
+    int at = 0, to = p.ring - 1;  // ring positions
+    for (int32_t round = 0; round < rounds; ++round) {
+      if (SHARED) __syncwarp();  // every lane has read what the next copies replace
+      fetch(next, mine + to * kSlots * stride);
+      advance(next);
+      const uint32_t slot0 = mine + at * kSlots * stride;
+      const bool here = now.tok < end;
+      const bool on[3] = {here && has[0], here && has[1], here && has[2]};
+      v8::Raw<T> dv = v8::zero<T>();
+      if (on[2]) dv = v8::load(static_cast<const T *>(p.dy[2]) + head_row(now, 1));
+      if (p.ring == 3)
+        asm volatile("cp.async.wait_group 2;" ::: "memory");
+      else if (p.ring == 2)
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+      else
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+      // (slots of tokens or heads that are not there hold anything: nothing below lets it
+      // past the `on` conditions, and a head's lanes are all there or all not)
+      Rot turn;
+      turn.rest();
+      if (SHARED) __syncwarp();  // the other lanes' copies have landed too
+      if (turns) {
 #pragma unroll
-      for (int i = 0; i < Rot::kSlots; ++i) {
-        uint32_t from = slot0 + (kAngles + i) * stride;
-        if (SHARED) {
-          const int32_t piece = Rot::offset(p, l) / 4 + i % (Rot::kSlots / 2) + (i < Rot::kSlots / 2 ? 0 : p.P / 4);
-          from = slot0 - 16 * (threadIdx.x & 31) + (kAngles + piece / 32) * stride + 16 * (piece % 32);
+        for (int i = 0; i < Rot::kSlots; ++i) {
+          uint32_t from = slot0 + (kAngles + i) * stride;
+          if (SHARED) {
+            const int32_t piece = Rot::offset(p, l) / 4 + i % (Rot::kSlots / 2) + (i < Rot::kSlots / 2 ? 0 : p.P / 4);
+            from = slot0 - 16 * (threadIdx.x & 31) + (kAngles + piece / 32) * stride + 16 * (piece % 32);
+          }
+          const uint4 w = lds16(from);
+          turn.raw[i] = make_float4(__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w));
         }
-        const uint4 w = lds16(from);
-        turn.raw[i] = make_float4(__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w));
       }
-    }
-    turn.set(p, l);
-    uint64_t u[2][4], x[2][4];
+      turn.set(p, l);
+      uint64_t u[kTensors][4], x[kTensors][4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      unpack(lds_vec<T>(slot0 + i * kVec * stride, stride), u[i]);
-      turn.apply(u[i]);
-      if (!normed) continue;
-      const uint32_t xs = slot0 + (2 * kVec + i * (CK ? 1 : kVec)) * stride;
-      if constexpr (CK) {
-        const uint4 w = lds16(xs);
-        const float unit = ck::unit_of((w.z >> (8 * ((l.vec >> 2) & 3))) & 0xFFu);
-        float f[8];
-        ck::unpack_codes4(w.x, unit, f[0], f[1], f[2], f[3]);
-        ck::unpack_codes4(w.y, unit, f[4], f[5], f[6], f[7]);
-        pairs_of(f, x[i]);
-      } else {
-        unpack(lds_vec<T>(xs, stride), x[i]);
+      for (int i = 0; i < kTensors; ++i) {
+        unpack(lds_vec<T>(slot0 + i * kVec * stride, stride), u[i]);
+        turn.apply(u[i]);
+        if (!normed) continue;
+        const uint32_t xs = slot0 + (2 * kVec + i * (CK ? 1 : kVec)) * stride;
+        if constexpr (CK) {
+          const uint4 w = lds16(xs);
+          const float unit = ck::unit_of((w.z >> (8 * ((l.vec >> 2) & 3))) & 0xFFu);
+          float f[8];
+          ck::unpack_codes4(w.x, unit, f[0], f[1], f[2], f[3]);
+          ck::unpack_codes4(w.y, unit, f[4], f[5], f[6], f[7]);
+          pairs_of(f, x[i]);
+        } else {
+          unpack(lds_vec<T>(xs, stride), x[i]);
+        }
       }
-    }
-    if (normed) {
-      uint64_t gu[2][4];
-      float sums[4];
+      if (normed) {
+        uint64_t gu[kTensors][4];
+        float sums[2 * kTensors];  // of x^2, then of x g u
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kTensors; ++i) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) gu[i][j] = mul2(g[i][j], u[i][j]);
-        sums[i] = on[i] ? dot(x[i], x[i]) : 0.f;
-        sums[2 + i] = on[i] ? dot(x[i], gu[i]) : 0.f;
-      }
-      group_sums(sums, l, p, red);
+          for (int j = 0; j < 4; ++j) gu[i][j] = mul2(g[i][j], u[i][j]);
+          sums[i] = on[i] ? dot(x[i], x[i]) : 0.f;
+          sums[kTensors + i] = on[i] ? dot(x[i], gu[i]) : 0.f;
+        }
+        group_sums(sums, l, p, red);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float inv = rsqrtf(fmaf(sums[i], inv_len[i], p.eps));
-        const float k3 = -(inv * inv * inv * (sums[2 + i] * inv_len[i]));
-        const uint64_t inv2 = f2(inv, inv), k32 = f2(k3, k3);
-        if (on[i]) {
+        for (int i = 0; i < kTensors; ++i) {
+          const float inv = rsqrtf(fmaf(sums[i], inv_len[i], p.eps));
+          const float k3 = -(inv * inv * inv * (sums[kTensors + i] * inv_len[i]));
+          const uint64_t inv2 = f2(inv, inv), k32 = f2(k3, k3);
+          if (on[i]) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            dg[i][j] = fma2(u[i][j], mul2(x[i][j], inv2), dg[i][j]);
-            u[i][j] = fma2(gu[i][j], inv2, mul2(x[i][j], k32));
+            for (int j = 0; j < 4; ++j) {
+              dg[i][j] = fma2(u[i][j], mul2(x[i][j], inv2), dg[i][j]);
+              u[i][j] = fma2(gu[i][j], inv2, mul2(x[i][j], k32));
+            }
           }
         }
       }
-    }
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-      if (on[i]) v8::store(static_cast<T *>(p.dx[i]) + token_row(now, heads[i] * p.D), pack<T>(u[i]));
-    if (on[2]) v8::store(static_cast<T *>(p.dx[2]) + token_row(now, heads[1] * p.D), dv);
-    advance(now);
-    at = at + 1 == p.ring ? 0 : at + 1;
-    to = to + 1 == p.ring ? 0 : to + 1;
-  }
+      for (int i = 0; i < kTensors; ++i)
+        if (on[i]) v8::store(static_cast<T *>(p.dx[i]) + token_row(now, heads[i] * p.D), pack<T>(u[i]));
+      if (on[2]) v8::store(static_cast<T *>(p.dx[2]) + token_row(now, heads[1] * p.D), dv);
+      advance(now);
+      at = at + 1 == p.ring ? 0 : at + 1;
+      to = to + 1 == p.ring ? 0 : to + 1;
+    }
+  };
+  if (p.norm == kNormToken || __any_sync(0xFFFFFFFFu, has[1]))
+    walk(std::integral_constant<int, 2>{});
+  else
+    walk(std::integral_constant<int, 1>{});
   asm volatile("cp.async.wait_all;" ::: "memory");
   if (!normed) return;
   // this block's dg: over its T tokens a round, and over its heads where they share a gain
@@ -710,8 +735,8 @@ size_t token_norm_bytes(const QkRopeParams &p, int32_t values) {  // group_sums'
 int32_t qk_rope_resident(int32_t threads) { return threads >= 512 ? 1 : 512 / threads; }
 // Heads of the backward's blocks: all of a token's, or, where that is more than 512 threads
 // and heads are normalised each by itself, equal shares (128 registers a thread instead of
-// 80 or 64, at which it spills; 16384 tokens of 40 x 128: @40@, of 64 query and 8 key
-// heads @64@).
+// 80 or 64, at which it spills: 16384 tokens of 40 x 128 402 to 283 us, of 64 query and 8
+// key heads 578 to 405).
 int32_t share_heads(const QkRopeParams &p) {
   const int32_t heads = p.Hq > p.Hk ? p.Hq : p.Hk, shares = p.norm == kNormToken ? 1 : (vectors(p) + 511) / 512;
   return (heads + shares - 1) / shares;
@@ -775,22 +800,27 @@ cudaError_t launch_bwd(const QkRopeParams &params, cudaStream_t stream) {
 }  // namespace
 
 namespace {
-// The grid's threads are a whole number of rows: a multiple of `cols` blocks, and no more
-// than are resident at once.
-template <typename I, int V>
+// The grid's threads are a whole number of blocks of R rows, and no more than are resident at
+// once (unless P alone asks for more).
+template <typename I, int V, int R>
 cudaError_t launch_table(const RopeTableParams &p, cudaStream_t stream) {
-  const int64_t cols = p.P / V, most = 148 * kTableBlocks;
-  const int64_t want = (p.N * cols + 255) / 256;
-  int64_t blocks = (want + cols - 1) / cols * cols;
-  if (blocks > most) blocks = cols < most ? most / cols * cols : cols;
-  return launch_in_order(rope_table_kernel<I, V>, dim3(unsigned(blocks)), 256, 0, stream, p, turn_series(p.mscale));
+  const int64_t cols = int64_t(p.P) * R / V;
+  int64_t unit = cols;  // thread blocks whose threads are a whole number of them
+  for (int k = 0; k < 8 && unit % 2 == 0; ++k) unit /= 2;
+  const int64_t most = 148 * kTableBlocks, want = ((p.N + R - 1) / R * cols + 255) / 256;
+  int64_t blocks = (want + unit - 1) / unit * unit;
+  if (blocks > most) blocks = unit < most ? most / unit * unit : unit;
+  return launch_in_order(rope_table_kernel<I, V, R>, dim3(unsigned(blocks)), 256, 0, stream, p, turn_series(p.mscale));
+}
+template <typename I>
+cudaError_t launch_table(const RopeTableParams &p, cudaStream_t stream) {
+  if ((reinterpret_cast<uintptr_t>(p.cos) | reinterpret_cast<uintptr_t>(p.sin)) & 15u) return launch_table<I, 1, 1>(p, stream);
+  return p.P % 4 ? launch_table<I, 4, 4>(p, stream) : launch_table<I, 4, 1>(p, stream);
 }
 }  // namespace
 
 cudaError_t launch_rope_table(const RopeTableParams &p, bool pos64, cudaStream_t stream) {
-  const bool vec = p.P % 4 == 0 && ((reinterpret_cast<uintptr_t>(p.cos) | reinterpret_cast<uintptr_t>(p.sin)) & 15u) == 0;
-  if (vec) return pos64 ? launch_table<int64_t, 4>(p, stream) : launch_table<int32_t, 4>(p, stream);
-  return pos64 ? launch_table<int64_t, 1>(p, stream) : launch_table<int32_t, 1>(p, stream);
+  return pos64 ? launch_table<int64_t>(p, stream) : launch_table<int32_t>(p, stream);
 }
 
 // Blocks of the backward: fixed by the sizes alone, so that the order of the gains'

@@ -102,6 +102,11 @@ def test_rope_table_refusals(kw, want):
     assert _table(**kw) == want
 
 
+@pytest.mark.parametrize("kw", [dict(axes=(1 << 28) + 1), dict(pairs=(1 << 28) + 1)])
+def test_rope_table_refuses_widths_past_32_bits(kw):
+    assert _table(**kw) == UNSUPPORTED
+
+
 @pytest.mark.parametrize("mscale", [2.0**126, -2.0**126, 1e300])
 def test_rope_table_refuses_scales_past_fp32(mscale):
     assert _table(mscale=mscale) == INVALID

@@ -9,6 +9,7 @@ import torch
 
 import block_reference as ref
 import masked_attention_jvp_b200 as caj
+from masked_attention_jvp_b200 import _lib
 
 pytestmark = pytest.mark.gpu
 
@@ -117,6 +118,22 @@ def test_rope_table_long(P, dt):
         # the reduced angle and each series round a few times: 4 half-steps at 1, and the result's own
         assert float((got - want).abs().max()) <= m * 5 * U
     assert float((cos.double() ** 2 + sin.double() ** 2 - m * m).abs().max()) <= 2 * m * m * 5 * U * 2
+
+
+@pytest.mark.parametrize("N,P", [(1, 1), (7, 61), (9, 62), (6, 64), (10001, 3)])
+@pytest.mark.parametrize("off", [0, 1, 4])
+def test_rope_table_writes_its_rows_alone(N, P, off):
+    """Tables at any fp32 address: the same values, and nothing before or behind them."""
+    freq, axis = caj.rope_frequencies(2 * P)
+    pos = torch.arange(N, device="cuda") + 77
+    want = caj.rope_table(pos, freq, axis)
+    bufs = [torch.full((off + N * P + 8,), 7.0, device="cuda") for _ in range(2)]
+    st = _lib.lib().caj_rope_table(pos.data_ptr(), 1, freq.data_ptr(), axis.data_ptr(), N, 1, P, 1.0,
+                                   *[b.data_ptr() + 4 * off for b in bufs], torch.cuda.current_stream().cuda_stream)
+    assert st == 0
+    for b, w in zip(bufs, want):
+        assert torch.equal(b[off:off + N * P].view(N, P), w)
+        assert bool((b[:off] == 7).all()) and bool((b[off + N * P:] == 7).all())
 
 
 def test_rope_table_one_axis_and_bad_axis():
