@@ -222,9 +222,9 @@ struct LinearDzParams {
   const void *dy;         // [M, C] bf16, rows ld_dy apart
   const int8_t *codes;    // z's checkpoint (act != none)
   const uint8_t *scales;
-  void *dz;               // [M, C] bf16 (act != none)
+  void *dz;               // [M, C] bf16, rows ld_dz apart (act != none)
   float *partial;         // [chunks][C], or null
-  int64_t M, ld_dy;
+  int64_t M, ld_dy, ld_dz;
   int32_t C, nb, ns, act, chunk_rows;
   int32_t late;           // beside the products that went before (act = none: nothing of theirs is read)
 };

@@ -781,7 +781,7 @@ __global__ void __launch_bounds__(256, 4) linear_dz_kernel(const LinearDzParams 
         }
         v8::Raw<__nv_bfloat16> o;
         v8::pack(f, o);
-        *reinterpret_cast<uint4 *>(dz + r * p.C) = o.a;
+        *reinterpret_cast<uint4 *>(dz + r * p.ld_dz) = o.a;
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) sum[i] = add2(sum[i], d[i]);
