@@ -507,8 +507,9 @@ caj_status caj_qk_rope_bwd(const void *dq, const void *dk, const void *dv, const
  *   out: y, ty      [M, C] bf16, contiguous, fully overwritten (ty null without tx)
  *        pre_codes, pre_scales  z's checkpoint, rows of C values (codes 32-byte aligned:
  *                   a block is stored at once); both null: none
- *   workspace       caj_linear_act_fwd_workspace() bytes (0 for most sizes), 16-byte
- *                   aligned; no other work may use it until the call is done
+ *   workspace       caj_linear_act_fwd_workspace() bytes (0 for most sizes; the rows'
+ *                   distances count), 16-byte aligned, better 128; no other work may use
+ *                   it until the call is done
  * Sums are fp32; bias, activation, tangent and residual are applied in fp32 before
  * the one rounding to bf16.
  *

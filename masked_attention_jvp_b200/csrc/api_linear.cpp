@@ -151,10 +151,38 @@ bool good_rows(const void *p, int64_t ld, int64_t width) {
 // pieces of them lie in one line each (4485 x 4152 -> 776: gradients 66 us with both operands'
 // rows at odd multiples of 16 bytes, 56 with both aligned).
 int64_t row_of(int64_t width) { return (width + 63) & ~int64_t(63); }
+// A caller's matrix [M, K] in rows at odd multiples of 16 bytes is copied to such rows first
+// where the products read it often enough: `reuse` columns of output to each of its rows
+// (9360 x 1624 -> 4104 135 to 118 us; 1032 columns 46 to 47, and from 296 channels, whose
+// tiles their epilogue bounds, 32 to 37).
+bool worth_copying(int64_t M, int64_t K, int64_t ld, int64_t reuse) {
+  return ld % 16 != 0 && K >= 768 && reuse >= 2048 && double(M) * double(K) * double(reuse) >= 8e9;
+}
+// One of a launch's copies.
+void add_copy(caj::CopyRowsParams *c, int32_t *n, const void *src, int64_t ld, int64_t M, int64_t K, void *dst) {
+  c->src[*n] = src;
+  c->dst[*n] = dst;
+  c->ld_src[*n] = ld / 8;
+  c->ld_dst[*n] = row_of(K) / 8;
+  c->rows = M;
+  c->vecs[*n] = int32_t(K / 8);
+  ++*n;
+}
+struct FwdSizes {
+  size_t parts, x, tx;
+};
+FwdSizes fwd_sizes(const caj_linear_act_shape *s, bool tangent, const Plan &plan) {
+  FwdSizes f{};
+  f.parts = padded(plan.part_bytes);
+  if (worth_copying(s->M, s->K, s->ldx, s->C)) f.x = padded(s->M * row_of(s->K) * 2);
+  if (tangent && worth_copying(s->M, s->K, s->ldtx, s->C)) f.tx = padded(s->M * row_of(s->K) * 2);
+  return f;
+}
 
 struct BwdSizes {
   GradPlan grads;
   int32_t chunk_rows;
+  bool copy_x, copy_dy;
   size_t x, dz, sums, dx_parts, dw_parts, total;
 };
 BwdSizes bwd_sizes(const caj_linear_act_shape *s, bool x_ckpt, bool want_dx, bool want_dw, bool want_db) {
@@ -163,8 +191,11 @@ BwdSizes bwd_sizes(const caj_linear_act_shape *s, bool x_ckpt, bool want_dx, boo
   if (!want_dx) b.grads.dx = Plan{};
   if (!want_dw) b.grads.dw = Plan{};
   b.chunk_rows = caj::linear_dz_chunk_rows(s->M, s->C);
-  if (x_ckpt && want_dw) b.x = padded(s->M * row_of(s->K) * 2);
-  if (s->act != CAJ_ACT_NONE) b.dz = padded(s->M * row_of(s->C) * 2);
+  b.copy_x = !x_ckpt && want_dw && worth_copying(s->M, s->K, s->ldx, s->C);
+  b.copy_dy = s->act == CAJ_ACT_NONE && (want_dx || want_dw) &&
+              worth_copying(s->M, s->C, s->ldy, s->K * (int(want_dx) + int(want_dw)));
+  if ((x_ckpt && want_dw) || b.copy_x) b.x = padded(s->M * row_of(s->K) * 2);
+  if (s->act != CAJ_ACT_NONE || b.copy_dy) b.dz = padded(s->M * row_of(s->C) * 2);
   if (want_db) b.sums = padded(ceil_div(s->M, b.chunk_rows) * s->C * 4);
   b.dx_parts = padded(b.grads.dx.part_bytes);
   b.dw_parts = padded(b.grads.dw.part_bytes);
@@ -180,7 +211,10 @@ caj_status caj_linear_act_fwd_workspace(const caj_linear_act_shape *shape, int32
   if (!bytes || (tangent != 0 && tangent != 1)) return CAJ_ERR_INVALID_ARG;
   const caj_status st = check_shape(shape);
   if (st != CAJ_OK) return st;
-  *bytes = few_rows(shape->M, tangent) ? 0 : size_t(plan_fwd(shape->M, shape->C, shape->K, tangent).part_bytes);
+  *bytes = 0;
+  if (few_rows(shape->M, tangent)) return CAJ_OK;
+  const FwdSizes f = fwd_sizes(shape, tangent, plan_fwd(shape->M, shape->C, shape->K, tangent));
+  *bytes = f.parts + f.x + f.tx;
   return CAJ_OK;
 }
 
@@ -202,8 +236,9 @@ caj_status caj_linear_act_fwd(const void *x, const void *tx, const void *w, cons
   if (pre_codes && (!aligned_to(pre_codes, 32) || !aligned_to(pre_scales, 4))) return CAJ_ERR_INVALID_ARG;
   const bool few = few_rows(M, tan);
   const FwdPlan pl = plan_fwd(M, C, K, tan);
-  if (!few && pl.part_bytes && (!workspace || !aligned_to(workspace, 16) || workspace_bytes < size_t(pl.part_bytes)))
-    return CAJ_ERR_INVALID_ARG;
+  const FwdSizes sizes = few ? FwdSizes{} : fwd_sizes(shape, tan, pl);
+  const size_t need = sizes.parts + sizes.x + sizes.tx;
+  if (need && (!workspace || !aligned_to(workspace, 16) || workspace_bytes < need)) return CAJ_ERR_INVALID_ARG;
   st = caj::check_device();
   if (st != CAJ_OK) return st;
   caj::LinearParams p{};
@@ -232,11 +267,27 @@ caj_status caj_linear_act_fwd(const void *x, const void *tx, const void *w, cons
     p.part = static_cast<float *>(workspace);
     p.timeout_ns = caj::wait_timeout_ns();
     p.fault_mode = caj::fault_mode();
+    char *at = static_cast<char *>(workspace);
+    caj::CopyRowsParams copies{};
+    int32_t n = 0;
+    int64_t ldx = shape->ldx, ldtx = shape->ldtx;
+    if (sizes.x) {
+      add_copy(&copies, &n, x, ldx, M, K, at + sizes.parts);
+      x = at + sizes.parts;
+      ldx = row_of(K);
+    }
+    if (sizes.tx) {
+      add_copy(&copies, &n, tx, ldtx, M, K, at + sizes.parts + sizes.x);
+      tx = at + sizes.parts + sizes.x;
+      ldtx = row_of(K);
+    }
+    if (n) st = done(caj::launch_copy_rows(copies, n, static_cast<cudaStream_t>(stream)));
+    if (st != CAJ_OK) return st;
     ok = part_map(&p.tm_part, pl, tan, workspace) &&
-         caj::encode_map_2d_ld(&p.tm_a, x, M, K, shape->ldx, tan ? 64 : 128) &&
+         caj::encode_map_2d_ld(&p.tm_a, x, M, K, ldx, tan ? 64 : 128) &&
          caj::encode_map_2d_ld(&p.tm_b, w, C, K, K, pl.tile_cols / 2) && caj::encode_out_2d(&p.tm_y, y, M, C, false);
     if (ok && tan)
-      ok = caj::encode_map_2d_ld(&p.tm_a2, tx, M, K, shape->ldtx, 64) &&
+      ok = caj::encode_map_2d_ld(&p.tm_a2, tx, M, K, ldtx, 64) &&
            caj::encode_out_2d(&p.tm_y2, ty, M, C, false);
   }
   if (!ok) return caj::cuda_fail(cudaErrorInvalidValue);
@@ -281,7 +332,7 @@ caj_status caj_linear_act_bwd(const void *dy, const void *x, const uint8_t *x_sc
   char *parts = at + b.x + b.dz + b.sums;
 
   int64_t ld_dz = row_of(C);
-  if (!act) {
+  if (!act && !b.copy_dy) {
     dz = const_cast<void *>(dy);
     ld_dz = shape->ldy;
   }
@@ -324,6 +375,16 @@ caj_status caj_linear_act_bwd(const void *dy, const void *x, const uint8_t *x_sc
     if (st != CAJ_OK) return st;
     x = x_values;
   }
+  caj::CopyRowsParams copies{};
+  int32_t n = 0;
+  if (b.copy_x) {
+    add_copy(&copies, &n, x, ld_x, M, K, x_values);
+    x = x_values;
+    ld_x = row_of(K);
+  }
+  if (b.copy_dy) add_copy(&copies, &n, dy, shape->ldy, M, C, dz);
+  if (n) st = done(caj::launch_copy_rows(copies, n, s));
+  if (st != CAJ_OK) return st;
   caj::LinearParams p{};
   p.prob[0] = b.grads.dx.prob;
   p.prob[1] = b.grads.dw.prob;

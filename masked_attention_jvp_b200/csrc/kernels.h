@@ -276,6 +276,16 @@ cudaError_t launch_qk_rope_fwd(const QkRopeParams &p, bool bf16, cudaStream_t st
 cudaError_t launch_qk_rope_bwd(const QkRopeParams &p, bool bf16, cudaStream_t stream);
 int32_t qk_rope_bwd_blocks(int32_t B, int32_t N, int32_t Hq, int32_t Hk, int32_t D, int32_t norm);
 cudaError_t launch_linear_fwd(const LinearParams &p, cudaStream_t stream);
+// Up to two matrices of `rows` rows of `vecs` 16-byte vectors, copied to rows of another pitch
+// (in vectors).
+struct CopyRowsParams {
+  const void *src[2];
+  void *dst[2];
+  int64_t ld_src[2], ld_dst[2];
+  int64_t rows;
+  int32_t vecs[2];
+};
+cudaError_t launch_copy_rows(const CopyRowsParams &p, int32_t matrices, cudaStream_t stream);
 // `sums`: column sums alone (late), to run beside the products
 cudaError_t launch_linear_grads(const LinearParams &p, const LinearDzParams *sums, cudaStream_t stream);
 cudaError_t launch_linear_dz(const LinearDzParams &p, cudaStream_t stream);

@@ -713,6 +713,26 @@ __global__ void __launch_bounds__(256) linear_rows_kernel(const LinearParams p) 
   rows_epilogue<kCols>(p, red, kLd, base);
 }
 
+// ------------------------------------------------------------- operands laid out anew
+// A warp a row, 16 bytes a lane; bound by memory (read once, written once).
+__global__ void __launch_bounds__(256) copy_rows_kernel(const CopyRowsParams p) {
+  begin_after_previous();
+  const int m = blockIdx.y;
+  const int64_t row = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  if (row >= p.rows) return;
+  const uint4 *src = static_cast<const uint4 *>(p.src[m]) + row * p.ld_src[m];
+  uint4 *dst = static_cast<uint4 *>(p.dst[m]) + row * p.ld_dst[m];
+  for (int32_t c = int32_t(threadIdx.x & 31); c < p.vecs[m]; c += 128) {
+    uint4 v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (c + 32 * i < p.vecs[m]) v[i] = __ldcs(src + c + 32 * i);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (c + 32 * i < p.vecs[m]) dst[c + 32 * i] = v[i];
+  }
+}
+
 // ----------------------------------------------------- gradient of the activation
 // dz = dy * act'(z), z from its 8-bit checkpoint, and the columns' sums of dz for the
 // bias, in one pass over dy. A warp's lanes hold 256 neighbouring columns, eight a
@@ -908,6 +928,10 @@ cudaError_t launch_linear_grads(const LinearParams &p, const LinearDzParams *sum
   dw.part = p.part2;
   dw.y = p.ty;
   return finish<false, false>(dw, stream);
+}
+
+cudaError_t launch_copy_rows(const CopyRowsParams &p, int32_t matrices, cudaStream_t stream) {
+  return launch_in_order(copy_rows_kernel, dim3(unsigned((p.rows + 7) / 8), unsigned(matrices)), 256, 0, stream, p);
 }
 
 // Chunks of rows of the dz pass: about eight blocks an SM, at least 32 rows each.

@@ -355,3 +355,33 @@ def test_bias_gradients_back_to_back(M, K, C, act):
         for i, d in enumerate(dys):
             d = d.double()
             assert bool(((want[6 * i + 2] - d.sum(0)).abs() <= M * 2.0**-24 * d.abs().sum(0)).all())
+
+
+@pytest.mark.parametrize("M,K,C,act,tangent", [(1700, 840, 2568, "none", True), (600, 3160, 4104, "silu", False),
+                                               (2100, 4104, 1544, "none", False)])
+def test_rows_at_odd_multiples_of_16_bytes(M, K, C, act, tangent):
+    """Large products of such inputs run on copies in even rows: the same values, to the bit, as
+    from inputs that lie in even rows, and the inputs stay as they are."""
+    g = torch.Generator().manual_seed(C)
+    x, tx, dy = rnd(g, M, K).cuda(), rnd(g, M, K).cuda() if tangent else None, rnd(g, M, C).cuda()
+    w, b = rnd(g, C, K, std=K ** -0.5).cuda(), rnd(g, C).cuda()
+
+    def even(t):
+        if t is None:
+            return None
+        wide = torch.full((t.shape[0], -(-t.shape[1] // 64) * 64), float("nan"), dtype=BF, device="cuda")
+        wide[:, :t.shape[1]] = t
+        return wide[:, :t.shape[1]]
+
+    want = caj.linear_act_fwd(even(x), w, b, act=act, tx=even(tx), save_pre=True)
+    for _ in range(2):
+        got = caj.linear_act_fwd(x, w, b, act=act, tx=tx, save_pre=True)
+        assert torch.equal(got[0], want[0]) and (not tangent or torch.equal(got[1], want[1]))
+        assert torch.equal(got[2].codes, want[2].codes) and torch.equal(got[2].scales, want[2].scales)
+    pre = want[2] if act != "none" else None
+    kept = x.clone(), dy.clone()
+    for need in ((True, True), (True, False), (False, True)):
+        a = caj.linear_act_bwd(even(dy), even(x), w, act=act, pre=pre, need=need)
+        for s, t in zip(a, caj.linear_act_bwd(dy, x, w, act=act, pre=pre, need=need)):
+            assert s is None and t is None or torch.equal(s, t)
+    assert torch.equal(x, kept[0]) and torch.equal(dy, kept[1])
