@@ -185,8 +185,8 @@ struct QkRopeParams {
   float eps;
   int32_t norm, half, gain_full;
   int32_t blocks;              // backward: all blocks, those of every share of the heads
-  // backward, set by the launch: heads a block has, tokens in a thread's ring of copies, slots for angles
-  int32_t share_heads, ring, angle_slots;
+  int32_t share_heads;         // heads a block has (set by the launch)
+  int32_t ring, angle_slots;   // backward: tokens in a thread's ring of copies, slots for angles (set by the launch)
 };
 
 // Matrix products of the linear operators; the operands' maps have 128-byte-swizzled

@@ -171,7 +171,8 @@ struct Lane {        // a thread's place: eight channels of one head, one token 
   int32_t V, T;      // vectors of a token (of the wider tensor, or a share of it), tokens of a block
   int32_t t, vec, head, d0;
 };
-__device__ __forceinline__ Lane lane_of(const QkRopeParams &p, int32_t heads) {
+// Of a block that has `heads` heads, from `head0` on.
+__device__ __forceinline__ Lane lane_of(const QkRopeParams &p, int32_t heads, int32_t head0) {
   Lane l;
   l.V = heads * p.D / 8;
   l.T = int32_t(blockDim.x) / l.V;
@@ -179,6 +180,8 @@ __device__ __forceinline__ Lane lane_of(const QkRopeParams &p, int32_t heads) {
   l.vec = int32_t(threadIdx.x) - l.t * l.V;
   l.head = 8 * l.vec / p.D;
   l.d0 = 8 * l.vec - l.head * p.D;
+  l.vec += head0 * p.D / 8;
+  l.head += head0;
   return l;
 }
 
@@ -315,13 +318,13 @@ __host__ __device__ constexpr int fwd_tokens() {
 // six 16-byte loads are in flight and the angles serve two to four vectors: two tokens a
 // thread without tangents, one with. (One token without tangents: 239 us for 65520 tokens
 // of 12 x 128, against 230.)
-// MAXT: 256 threads leave 80 registers each, 1024 (tokens wider than 2048 channels) 64.
+// MAXT: 256 threads leave 80 registers each, 1024 (a mean over more than 2048 channels) 64.
 template <typename T, bool TAN, bool HALF, int MAXT>
 __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 3 : 1) qk_rope_fwd_kernel(const QkRopeParams p) {
   extern __shared__ __align__(16) float red[];
   begin_after_previous();
   constexpr int U = fwd_tokens<T, TAN>();
-  const Lane l = lane_of(p, max(p.Hq, p.Hk));
+  const Lane l = lane_of(p, p.share_heads, int32_t(blockIdx.y) * p.share_heads);
   const int32_t heads[3] = {p.Hq, p.Hk, p.x[2] ? p.Hk : 0};
   const bool turns = l.d0 < 2 * p.P;
   v8::Raw<T> raw[U][3], traw[U][3];
@@ -471,10 +474,8 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) qk_rope_bwd_kernel(
   constexpr int kAngles = bwd_slots<T, CK>();  // the angles' first slot
   const int kSlots = kAngles + (SHARED ? p.angle_slots : Rot::kSlots);
   float *red = reinterpret_cast<float *>(smem + size_t(p.ring) * kSlots * 16 * blockDim.x);
-  Lane l = lane_of(p, p.share_heads);
   const int32_t head0 = int32_t(blockIdx.y) * p.share_heads;
-  l.vec += head0 * p.D / 8;
-  l.head += head0;
+  const Lane l = lane_of(p, p.share_heads, head0);
   const int32_t rows = p.B * p.N, stride = 16 * int32_t(blockDim.x);
   const uint32_t mine = ptx::smem_u32(smem) + 16 * threadIdx.x;
   const int32_t heads[3] = {p.Hq, p.Hk, p.dy[2] ? p.Hk : 0};
@@ -733,27 +734,34 @@ size_t token_norm_bytes(const QkRopeParams &p, int32_t values) {  // group_sums'
 
 // Blocks of the backward that an SM holds (registers: 512 threads).
 int32_t qk_rope_resident(int32_t threads) { return threads >= 512 ? 1 : 512 / threads; }
-// Heads of the backward's blocks: all of a token's, or, where that is more than 512 threads
-// and heads are normalised each by itself, equal shares (128 registers a thread instead of
-// 80 or 64, at which it spills: 16384 tokens of 40 x 128 402 to 283 us, of 64 query and 8
-// key heads 578 to 405).
-int32_t share_heads(const QkRopeParams &p) {
-  const int32_t heads = p.Hq > p.Hk ? p.Hq : p.Hk, shares = p.norm == kNormToken ? 1 : (vectors(p) + 511) / 512;
+// Heads of a block: all of a token's, or, where that is more than `most` threads and heads
+// are normalised each by itself, equal shares. Backward: 512, for 128 registers a thread
+// instead of 80 or 64, at which it spills (16384 tokens of 40 x 128 402 to 283 us, of 64 query
+// and 8 key heads 578 to 405). Forward: 256, for 80 registers and three blocks an SM
+// (16384 tokens of 40 x 128, half layout, 334 to 238 us, of 32 query and 8 key heads 187 to
+// 153).
+int32_t share_heads(const QkRopeParams &p, int32_t most) {
+  const int32_t heads = p.Hq > p.Hk ? p.Hq : p.Hk;
+  const int32_t shares = p.norm == kNormToken ? 1 : (vectors(p) + most - 1) / most;
   return (heads + shares - 1) / shares;
 }
+int32_t shares_of(const QkRopeParams &p) { return ((p.Hq > p.Hk ? p.Hq : p.Hk) + p.share_heads - 1) / p.share_heads; }
 
 template <typename T, bool TAN, int MAXT>
 cudaError_t launch_fwd(const QkRopeParams &p, cudaStream_t stream) {
-  const int32_t threads = threads_for(vectors(p));
+  const int32_t V = p.share_heads * p.D / 8, threads = threads_for(V);
   constexpr int U = fwd_tokens<T, TAN>();
-  const unsigned grid = unsigned((groups_for(p, vectors(p)) + U - 1) / U);
+  const unsigned grid = unsigned((groups_for(p, V) + U - 1) / U);
   const size_t smem = token_norm_bytes(p, TAN ? 4 : 2);
   return launch_in_order(p.half ? qk_rope_fwd_kernel<T, TAN, true, MAXT> : qk_rope_fwd_kernel<T, TAN, false, MAXT>,
-                         dim3(grid), threads, smem, stream, p);
+                         dim3(grid, unsigned(shares_of(p))), threads, smem, stream, p);
 }
 template <typename T>
-cudaError_t launch_fwd(const QkRopeParams &p, cudaStream_t stream) {
-  if (threads_for(vectors(p)) <= 256) return p.tx[0] ? launch_fwd<T, true, 256>(p, stream) : launch_fwd<T, false, 256>(p, stream);
+cudaError_t launch_fwd(const QkRopeParams &params, cudaStream_t stream) {
+  QkRopeParams p = params;
+  p.share_heads = share_heads(p, 256);
+  if (threads_for(p.share_heads * p.D / 8) <= 256)
+    return p.tx[0] ? launch_fwd<T, true, 256>(p, stream) : launch_fwd<T, false, 256>(p, stream);
   return p.tx[0] ? launch_fwd<T, true, 1024>(p, stream) : launch_fwd<T, false, 1024>(p, stream);
 }
 
@@ -774,7 +782,7 @@ cudaError_t launch_bwd(const QkRopeParams &params, cudaStream_t stream) {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kMaxSmem));
   });
   if (e != cudaSuccess) return e;
-  const int32_t heads = p.Hq > p.Hk ? p.Hq : p.Hk, shares = (heads + p.share_heads - 1) / p.share_heads;
+  const int32_t shares = shares_of(p);
   e = launch_in_order(kernel, dim3(unsigned(p.blocks / shares), unsigned(shares)), threads, p.ring * token + extra, stream, p);
   if (e != cudaSuccess || p.norm == kNormNone) return e;
   const int32_t len = p.gain_full ? vectors(p) * 8 : p.D;
@@ -789,7 +797,7 @@ cudaError_t launch_bwd(const QkRopeParams &p, cudaStream_t stream) {
 template <typename T, bool CK>
 cudaError_t launch_bwd(const QkRopeParams &params, cudaStream_t stream) {
   QkRopeParams p = params;
-  p.share_heads = share_heads(p);
+  p.share_heads = share_heads(p, 512);
   const int32_t threads = threads_for(p.share_heads * p.D / 8);
   return threads <= 256   ? launch_bwd<T, CK, 256>(p, stream)
          : threads <= 512 ? launch_bwd<T, CK, 512>(p, stream)
@@ -833,7 +841,8 @@ int32_t qk_rope_bwd_blocks(int32_t B, int32_t N, int32_t Hq, int32_t Hk, int32_t
   p.Hk = Hk;
   p.D = D;
   p.norm = norm;
-  const int32_t heads = Hq > Hk ? Hq : Hk, own = share_heads(p), shares = (heads + own - 1) / own, V = own * D / 8;
+  p.share_heads = share_heads(p, 512);
+  const int32_t shares = shares_of(p), V = p.share_heads * D / 8;
   const int64_t groups = groups_for(p, V), most = 148 * int64_t(qk_rope_resident(threads_for(V))) / shares;
   return shares * int32_t(groups < most ? groups : most);
 }
